@@ -28,7 +28,7 @@ CXX = os.environ.get("CXX_HOST", shutil.which("g++") or "c++")
 
 HOST_SOURCES = ["host_quant.cpp"]
 DEVICE_SOURCES = ["abi.hip", "k_route.hip", "k_decode.hip", "k_decode1.hip", "k_decodem.hip", "k_prefill.hip", "k_misc.hip",
-                  "expert_cache.hip"]
+                  "expert_cache.hip", "attn_abi.hip", "k_kv.hip", "k_attn_decode.hip", "k_attn_prefill.hip"]
 
 HIP_FLAGS = ["-O3", "-fPIC", "-std=c++17", f"--offload-arch={ARCH}",
              "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

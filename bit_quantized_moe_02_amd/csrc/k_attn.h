@@ -1,0 +1,94 @@
+// Launch interface of the attention kernels (k_kv.hip, k_attn_decode.hip,
+// k_attn_prefill.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace qmoe {
+
+// A cache and a step's sequences over it (include/qmoe_attn.h).
+struct KvArgs {
+  uint8_t* codes;
+  float* scales;
+  const int32_t* table;
+  int64_t table_stride;
+  const int32_t* lens;
+  const int32_t* cu;        // null: per_seq rows each
+  int per_seq;
+  int B, T, max_new;
+  int n_pages, max_len;     // max_len = pages_per_seq * page_tokens
+  int Hk, D;
+  int lb;                   // log2 of the blocks of a page
+};
+
+struct AppendArgs {
+  KvArgs kv;
+  const void *q, *k, *v;
+  void *q_out, *k_out;
+  int64_t qs, ks, vs, qos, kos;
+  int Hq;                   // 0: no q
+  int rot, inter;
+  float rscale;
+  const double* freqs;
+};
+hipError_t launch_kv_append(const AppendArgs& a, int dtype, int cus, hipStream_t s);
+
+struct ReadArgs {
+  KvArgs kv;
+  void *k_out, *v_out;
+  int64_t kos, vos;
+};
+hipError_t launch_kv_read(const ReadArgs& a, int dtype, hipStream_t s);
+
+// Parts of a row's context that attention computes apart, joined by
+// launch_attn_join: un-normalised sums [n_split][T][Hq][D] and (maximum in
+// powers of two, sum) [n_split][T][Hq][2].
+struct SplitBuf {
+  float* o;
+  float* ml;
+  int n;                    // 1: no parts, the kernel writes the outputs itself
+};
+
+struct DecodeArgs {
+  KvArgs kv;
+  const void* q;
+  void* out;
+  float* lse;
+  int64_t qs, os;
+  int Hq;
+  float c;                  // scale * log2(e)
+  SplitBuf split;
+};
+int attn_decode_splits(const KvArgs& kv, int Hq, int cus);
+hipError_t launch_attn_decode(const DecodeArgs& a, int dtype, hipStream_t s);
+
+struct PrefillArgs {
+  const int32_t *cu_q, *cu_k;
+  int B, Tq, Tk, max_q, per_q, per_k;
+  int Hq, Hk, D;
+  const void *q, *k, *v;
+  void* out;
+  float* lse;
+  int64_t qs, ks, vs, os;
+  float c;
+  int causal;
+  SplitBuf split;
+};
+int attn_prefill_splits(int B, int Tq, int Tk, int max_q, int Hq, int Hk, int D, int cus);
+hipError_t launch_attn_prefill(const PrefillArgs& a, int dtype, int cus, hipStream_t s);
+
+// Joins the parts of rows 0..T-1 (rows outside every sequence are left as
+// they are: cu/per_seq/B/max_new as above).
+struct JoinArgs {
+  SplitBuf split;
+  const int32_t* cu;
+  int B, T, Hq, D, max_new, per_seq;
+  void* out;
+  float* lse;
+  int64_t os;
+};
+hipError_t launch_attn_join(const JoinArgs& a, int dtype, hipStream_t s);
+
+}  // namespace qmoe

@@ -1,0 +1,381 @@
+// The paged 8-bit key/value cache: rotary positions and appending
+// (moe_kv_append), reading rows back (moe_kv_read).  Layout and rules in
+// include/qmoe_attn.h.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "attn_common.hpp"
+
+using namespace qmoe;
+using namespace qmoe_dev;
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+
+// Least power of two s with amax <= 448 s, not below 2^-64.  448 = 1.75 * 2^8,
+// so s has amax's exponent minus 8, one more when the mantissa exceeds 1.75.
+__device__ __forceinline__ float least_scale(float amax) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, amax);
+  int e = (int)(u >> 23) - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);   // biased
+  if (e < 127 - 64) e = 127 - 64;
+  return __builtin_bit_cast(float, (uint32_t)e << 23);
+}
+
+// 1/s of a power of two between 2^-64 and 2^121
+__device__ __forceinline__ float inverse_pow2(float s) {
+  return __builtin_bit_cast(float, (254u << 23) - __builtin_bit_cast(uint32_t, s));
+}
+
+__device__ __forceinline__ bool finite(float x) { return (__builtin_bit_cast(uint32_t, x) & 0x7F800000u) != 0x7F800000u; }
+
+__device__ __forceinline__ float amax_of(float m, float x) { return finite(x) ? fmaxf(m, fabsf(x)) : m; }
+
+// Code of x (already divided by the scale); not finite -> not a number.
+__device__ __forceinline__ uint32_t code2(float a, float b) {
+  const float nan = __builtin_nanf("");
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(finite(a) ? a : nan, finite(b) ? b : nan, 0, false) & 0xFFFFu;
+}
+
+__device__ __forceinline__ uint32_t code4(float a, float b, float c, float d) {
+  return code2(a, b) | code2(c, d) << 16;
+}
+
+// Four codes times r, rounded again.
+__device__ __forceinline__ uint32_t rescale4(uint32_t w, float r) {
+  const auto x = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false);
+  const auto y = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+  return code4(x[0] * r, x[1] * r, y[0] * r, y[1] * r);
+}
+
+__device__ __forceinline__ float wave_max(float x) {
+  for (int o = 32; o >= 1; o >>= 1) x = fmaxf(x, __shfl_xor(x, o));
+  return x;
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack8(const u32x4& v, float* x) {
+  x[0] = T::lo(v.x); x[1] = T::hi(v.x); x[2] = T::lo(v.y); x[3] = T::hi(v.y);
+  x[4] = T::lo(v.z); x[5] = T::hi(v.z); x[6] = T::lo(v.w); x[7] = T::hi(v.w);
+}
+
+template <typename T>
+__device__ __forceinline__ u32x4 pack8(const float* x) {
+  u32x4 v;
+  v.x = T::cvt2(x[0], x[1]); v.y = T::cvt2(x[2], x[3]); v.z = T::cvt2(x[4], x[5]); v.w = T::cvt2(x[6], x[7]);
+  return v;
+}
+
+__device__ __forceinline__ u32x4 ldg16(const uint16_t* p) { return *reinterpret_cast<const u32x4*>(p); }
+
+// One workgroup takes the tokens that one block of one sequence gets, and a
+// share (blockIdx.y) of the heads.  Its threads compute the angles of those
+// tokens once into LDS (64-bit reduction, then 32-bit sine and cosine); then
+// each wave takes one job at a time: a q head (turn), a K head (turn, scale,
+// codes) or a V head (scale, codes).  A wave holds 16 tokens of one head in
+// registers, so each input is read once and each output written once.
+template <typename T, int D>
+__global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int nb) {
+  constexpr int kLanes = D / 16;            // lanes of a row of q or k, 16 columns each
+  constexpr int kRows = 64 / kLanes;        // rows a wave takes at once
+  constexpr int kSteps = 16 / kRows;
+  __shared__ __attribute__((aligned(16))) float2 turn[16][D / 2 + 1];
+
+  const int b = blockIdx.x / nb, ib = blockIdx.x % nb;
+  const Seq s = seq_of(a.kv, b);
+  const int pos0 = s.len - s.n;             // may be negative
+  const int blk = (pos0 >> 4) + ib;
+  const int lo = max(blk * 16, pos0), hi = min(blk * 16 + 16, s.len);
+  if (lo >= hi) return;                     // the whole workgroup
+  const int f = lo - blk * 16, e = hi - blk * 16;      // slots [f, e) are new
+  const int64_t row_of_slot0 = (int64_t)s.row0 + (blk * 16 - pos0);
+  const int half = a.rot / 2;
+
+  for (int i = threadIdx.x; i < 16 * half; i += kThreads) {
+    const int n = i / half, p = i % half;
+    if (n < f || n >= e) continue;
+    double t = (double)(blk * 16 + n) * (a.freqs[p] * 0.15915494309189535);   // turns
+    t -= floor(t);
+    float sn, cs;
+    sincospif(2.0f * (float)t, &sn, &cs);
+    turn[n][p] = make_float2(cs * a.rscale, sn * a.rscale);
+  }
+  __syncthreads();
+
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int jobs = a.Hq + 2 * a.kv.Hk;
+  // rows of q and k: lane -> (row of the step, 16 columns as two chunks of 8)
+  const int c = lane % kLanes, rr = lane / kLanes;
+  const bool turned = 16 * c < a.rot;
+  const int dA = (!a.inter && turned) ? 8 * c : 16 * c;
+  const int dB = (!a.inter && turned) ? half + 8 * c : 16 * c + 8;
+
+  for (int job = blockIdx.y * kWaves + wave; job < jobs; job += kWaves * gridDim.y) {
+    if (job < a.Hq + a.kv.Hk) {
+      const bool is_q = job < a.Hq;
+      const int h = is_q ? job : job - a.Hq;
+      const uint16_t* src = (const uint16_t*)(is_q ? a.q : a.k) + (int64_t)h * D;
+      const int64_t stride = is_q ? a.qs : a.ks;
+      uint16_t* dst = (uint16_t*)(is_q ? a.q_out : a.k_out);
+      const int64_t dstride = is_q ? a.qos : a.kos;
+      float x[kSteps][16];
+      float m = 0.f;
+#pragma unroll
+      for (int st = 0; st < kSteps; ++st) {
+        const int n = st * kRows + rr;
+        const bool on = n >= f && n < e;
+        u32x4 va = {0, 0, 0, 0}, vb = {0, 0, 0, 0};
+        if (on) {
+          const uint16_t* p = src + (row_of_slot0 + n) * stride;
+          va = ldg16(p + dA);
+          vb = ldg16(p + dB);
+        }
+        float* A = x[st];
+        float* B = x[st] + 8;
+        unpack8<T>(va, A);
+        unpack8<T>(vb, B);
+        if (turned && on) {
+          const float2* t = &turn[n][8 * c];
+          if (a.inter) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 u = t[j], v = t[4 + j];
+              const float a0 = A[2 * j], a1 = A[2 * j + 1], b0 = B[2 * j], b1 = B[2 * j + 1];
+              A[2 * j] = a0 * u.x - a1 * u.y;
+              A[2 * j + 1] = a0 * u.y + a1 * u.x;
+              B[2 * j] = b0 * v.x - b1 * v.y;
+              B[2 * j + 1] = b0 * v.y + b1 * v.x;
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float2 u = t[j];
+              const float a0 = A[j], b0 = B[j];
+              A[j] = a0 * u.x - b0 * u.y;
+              B[j] = a0 * u.y + b0 * u.x;
+            }
+          }
+        }
+        if (on && dst) {
+          uint16_t* p = dst + (row_of_slot0 + n) * dstride + (int64_t)h * D;
+          *reinterpret_cast<u32x4*>(p + dA) = pack8<T>(A);
+          *reinterpret_cast<u32x4*>(p + dB) = pack8<T>(B);
+        }
+        if (!is_q) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) m = amax_of(m, x[st][j]);
+        }
+      }
+      if (is_q || blk < 0) continue;
+      const int64_t at = block_of(a.kv, b, blk, h);
+      if (at < 0) continue;
+      uint8_t* tile = a.kv.codes + at * (32 * D);
+      float* sc = a.kv.scales + 2 * at;
+      const float was = f > 0 ? *sc : 0.f;
+      const float now = fmaxf(was, least_scale(wave_max(m)));
+      const float inv = inverse_pow2(now);
+      if (f > 0 && now > was) {             // earlier tokens of the block: lane c = 16*g + n
+        if ((lane & 15) < f) {
+          const float r = was * inv;
+#pragma unroll
+          for (int p = 0; p < D / 64; ++p) {
+            u32x4* w = reinterpret_cast<u32x4*>(tile + 1024 * p + 16 * lane);
+            u32x4 v = *w;
+            v.x = rescale4(v.x, r);
+            v.y = rescale4(v.y, r);
+            v.z = rescale4(v.z, r);
+            v.w = rescale4(v.w, r);
+            *w = v;
+          }
+        }
+      }
+#pragma unroll
+      for (int st = 0; st < kSteps; ++st) {
+        const int n = st * kRows + rr;
+        if (n < f || n >= e) continue;
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          const float* y = x[st] + 8 * part;
+          const int d = part ? dB : dA;
+          u32x2 w;
+          w.x = code4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+          w.y = code4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv);
+          *reinterpret_cast<u32x2*>(tile + 1024 * (d >> 6) + 16 * (16 * ((d >> 3) & 3) + n) + 8 * ((d >> 5) & 1)) = w;
+        }
+      }
+      if (lane == 0) *sc = now;
+    } else {
+      // V: a lane takes 8 columns of 4 tokens, the words of its 8 columns
+      const int h = job - a.Hq - a.kv.Hk;
+      if (blk < 0) continue;
+      const int64_t at = block_of(a.kv, b, blk, h);
+      if (at < 0) continue;
+      constexpr int kCh = D / 8;                               // chunks of 8 columns
+      constexpr int kSt = kCh * 4 > 64 ? kCh * 4 / 64 : 1;
+      const uint16_t* src = (const uint16_t*)a.v + (int64_t)h * D;
+      u32x4 v[kSt][4];
+      float m = 0.f;
+#pragma unroll
+      for (int st = 0; st < kSt; ++st) {
+        const int l = st * 64 + lane, ch = l % kCh, g = l / kCh;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int n = 4 * g + i;
+          v[st][i] = u32x4{0, 0, 0, 0};
+          if (g < 4 && n >= f && n < e) v[st][i] = ldg16(src + (row_of_slot0 + n) * a.vs + 8 * ch);
+          float x[8];
+          unpack8<T>(v[st][i], x);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) m = amax_of(m, x[j]);
+        }
+      }
+      uint8_t* tile = a.kv.codes + at * (32 * D) + 16 * D;
+      float* sc = a.kv.scales + 2 * at + 1;
+      const float was = f > 0 ? *sc : 0.f;
+      const float now = fmaxf(was, least_scale(wave_max(m)));
+      const float inv = inverse_pow2(now);
+      const float r = was * inv;
+#pragma unroll
+      for (int st = 0; st < kSt; ++st) {
+        const int l = st * 64 + lane, ch = l % kCh, g = l / kCh;
+        const bool grow = f > 4 * g && now > was;              // holds tokens to be rounded again
+        const bool fresh = f < 4 * g + 4 && e > 4 * g;         // gets new tokens
+        if (g >= 4 || !(grow || fresh)) continue;
+        // bytes of new tokens, and of earlier ones
+        const int nf = min(max(f - 4 * g, 0), 4), ne = min(max(e - 4 * g, 0), 4);
+        const uint32_t below = nf >= 4 ? 0xFFFFFFFFu : (1u << (8 * nf)) - 1u;
+        const uint32_t upto = ne >= 4 ? 0xFFFFFFFFu : (1u << (8 * ne)) - 1u;
+        const uint32_t is_new = upto & ~below;
+        float x[4][8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) unpack8<T>(v[st][i], x[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int d = 8 * ch + j;
+          uint32_t* w = reinterpret_cast<uint32_t*>(tile + 1024 * (d >> 6) + 16 * (16 * g + (d & 15)) + 4 * ((d >> 4) & 3));
+          uint32_t word = code4(x[0][j] * inv, x[1][j] * inv, x[2][j] * inv, x[3][j] * inv);
+          if (is_new != 0xFFFFFFFFu) {
+            const uint32_t old = *w;
+            word = (word & is_new) | (old & ~is_new);
+            if (grow) word = (word & ~below) | (rescale4(old, r) & below);
+          }
+          *w = word;
+        }
+      }
+      if (lane == 0) *sc = now;
+    }
+  }
+}
+
+// One wave takes one block of one sequence and head: the K codes go out as
+// they lie (a lane holds 8 consecutive columns of one token), the V codes
+// through a transposing tile in LDS.
+template <typename T, int D>
+__global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a, int nb) {
+  constexpr int kPad = 8;
+  __shared__ __attribute__((aligned(16))) uint16_t vt[kWaves][16][D + kPad];
+  const int b = blockIdx.x / nb, ib = blockIdx.x % nb;
+  const Seq s = seq_of(a.kv, b);
+  const int pos0 = s.len - s.n;
+  const int blk = (pos0 >> 4) + ib;
+  const int lo = max(blk * 16, pos0), hi = min(blk * 16 + 16, s.len);
+  if (lo >= hi) return;
+  const int f = lo - blk * 16, e = hi - blk * 16;
+  const int64_t row_of_slot0 = (int64_t)s.row0 + (blk * 16 - pos0);
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int n = lane & 15, g = lane >> 4;
+  const int h = blockIdx.y * kWaves + wave;
+  if (h >= a.kv.Hk) return;
+  const int64_t at = blk < 0 ? -1 : block_of(a.kv, b, blk, h);
+  const uint8_t* tile = a.kv.codes + (at < 0 ? 0 : at) * (32 * D);
+  float sk = 1.f, sv = 1.f;
+  if (at >= 0) {
+    sk = a.kv.scales[2 * at];
+    sv = a.kv.scales[2 * at + 1];
+  }
+  u32x4 kw[D / 64], vw[D / 64];
+#pragma unroll
+  for (int p = 0; p < D / 64; ++p) {
+    kw[p] = vw[p] = u32x4{0, 0, 0, 0};
+    if (at >= 0) {
+      kw[p] = *reinterpret_cast<const u32x4*>(tile + 1024 * p + 16 * lane);
+      vw[p] = *reinterpret_cast<const u32x4*>(tile + 16 * D + 1024 * p + 16 * lane);
+    }
+  }
+  const bool on = n >= f && n < e;
+  if (on) {
+    uint16_t* p = (uint16_t*)a.k_out + (row_of_slot0 + n) * a.kos + (int64_t)h * D + 8 * g;
+#pragma unroll
+    for (int q = 0; q < D / 64; ++q) {
+      *reinterpret_cast<u32x4*>(p + 64 * q) = dec8<T>(kw[q].x, kw[q].y, sk);
+      *reinterpret_cast<u32x4*>(p + 64 * q + 32) = dec8<T>(kw[q].z, kw[q].w, sk);
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < D / 64; ++q) {
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const uint32_t word = w == 0 ? vw[q].x : w == 1 ? vw[q].y : w == 2 ? vw[q].z : vw[q].w;
+      const uint32_t x = T::dec2(word, sv, false), y = T::dec2(word, sv, true);
+      const int d = 64 * q + 16 * w + n;
+      vt[wave][4 * g][d] = (uint16_t)x;
+      vt[wave][4 * g + 1][d] = (uint16_t)(x >> 16);
+      vt[wave][4 * g + 2][d] = (uint16_t)y;
+      vt[wave][4 * g + 3][d] = (uint16_t)(y >> 16);
+    }
+  }
+  __builtin_amdgcn_wave_barrier();          // the tile is the wave's own
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  constexpr int kCh = D / 8;
+#pragma unroll
+  for (int i = lane; i < 16 * kCh; i += 64) {
+    const int m = i / kCh, ch = i % kCh;
+    if (m < f || m >= e) continue;
+    *reinterpret_cast<u32x4*>((uint16_t*)a.v_out + (row_of_slot0 + m) * a.vos + (int64_t)h * D + 8 * ch) =
+        *reinterpret_cast<const u32x4*>(&vt[wave][m][8 * ch]);
+  }
+}
+
+// Blocks of 16 positions that n consecutive ones can touch.
+int blocks_of(int n) { return (n + 30) / 16; }
+
+}  // namespace
+
+namespace qmoe {
+
+hipError_t launch_kv_append(const AppendArgs& a, int dtype, int cus, hipStream_t s) {
+  const int nb = blocks_of(a.kv.cu ? a.kv.max_new : a.kv.per_seq);
+  const int64_t items = (int64_t)a.kv.B * nb;
+  const int jobs = a.Hq + 2 * a.kv.Hk;
+  // few tokens: a wave per job, so that the heads' latencies overlap; many:
+  // a workgroup takes all heads and its angles serve them all
+  int64_t gy = (4ll * cus + items - 1) / items;
+  const int most = (jobs + kWaves - 1) / kWaves;
+  if (gy > most) gy = most;
+  void (*fn)(AppendArgs, int) = nullptr;
+  const bool bf = dtype == 0;
+  switch (a.kv.D) {
+    case 64: fn = bf ? append_kernel<Bf16, 64> : append_kernel<F16, 64>; break;
+    case 128: fn = bf ? append_kernel<Bf16, 128> : append_kernel<F16, 128>; break;
+    default: fn = bf ? append_kernel<Bf16, 256> : append_kernel<F16, 256>; break;
+  }
+  hipLaunchKernelGGL(fn, dim3((unsigned)items, (unsigned)gy), dim3(kThreads), 0, s, a, nb);
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_read(const ReadArgs& a, int dtype, hipStream_t s) {
+  const int nb = blocks_of(a.kv.cu ? a.kv.max_new : a.kv.per_seq);
+  void (*fn)(ReadArgs, int) = nullptr;
+  const bool bf = dtype == 0;
+  switch (a.kv.D) {
+    case 64: fn = bf ? read_kernel<Bf16, 64> : read_kernel<F16, 64>; break;
+    case 128: fn = bf ? read_kernel<Bf16, 128> : read_kernel<F16, 128>; break;
+    default: fn = bf ? read_kernel<Bf16, 256> : read_kernel<F16, 256>; break;
+  }
+  hipLaunchKernelGGL(fn, dim3((unsigned)(a.kv.B * (int64_t)nb), (unsigned)((a.kv.Hk + kWaves - 1) / kWaves)),
+                     dim3(kThreads), 0, s, a, nb);
+  return hipGetLastError();
+}
+
+}  // namespace qmoe

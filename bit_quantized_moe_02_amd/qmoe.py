@@ -1,4 +1,4 @@
-"""Python binding of libqmoe (include/qmoe.h): the same calls under the same
+"""Python binding of libqmoe (include/qmoe.h, include/qmoe_attn.h): the same calls under the same
 names, with argument marshalling only -- torch tensors become device
 pointers, the current torch stream becomes the hipStream_t, a nonzero status
 becomes a QmoeError carrying moe_last_error().  Every computation happens in
@@ -44,7 +44,16 @@ EXPORTED = [
     "moe_expert_cache_weights", "moe_expert_cache_plan", "moe_expert_cache_fetch", "moe_expert_cache_state",
     "moe_layer_decode_streamed_workspace_bytes", "moe_layer_decode_streamed",
 ]
+# the attention calls (include/qmoe_attn.h)
+EXPORTED_ATTN = [
+    "moe_kv_code_bytes", "moe_kv_scale_bytes", "moe_rope_freqs", "moe_kv_append", "moe_kv_read",
+    "moe_attn_decode_workspace_bytes", "moe_attn_decode", "moe_attn_prefill_workspace_bytes", "moe_attn_prefill",
+]
 MOE_NOALLOC_SCRATCH_BYTES = 8 << 20
+
+MOE_DT_BF16 = 0
+MOE_DT_F16 = 1
+MOE_ROPE = {"plain": 0, "linear": 1, "base": 2, "parts": 3}
 
 MOE_KERNEL = {"route_logits": 0, "route_topk": 1, "decode_upgate": 2, "decode_down": 3,
               "decode_combine": 4, "group": 5, "prefill_upgate": 6, "prefill_down": 7,
@@ -71,11 +80,38 @@ class MoeWeights(ctypes.Structure):
     ]
 
 
+class MoeKvCache(ctypes.Structure):
+    """Mirror of struct moe_kv_cache."""
+    _fields_ = [("n_pages", ctypes.c_int32), ("page_tokens", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class MoeKvBatch(ctypes.Structure):
+    """Mirror of struct moe_kv_batch."""
+    _fields_ = [("batch", ctypes.c_int32), ("rows", ctypes.c_int32), ("max_new", ctypes.c_int32),
+                ("pages_per_seq", ctypes.c_int32), ("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("kv_lens", ctypes.c_void_p), ("cu_rows", ctypes.c_void_p)]
+
+
+class MoeRope(ctypes.Structure):
+    """Mirror of struct moe_rope."""
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("freqs", ctypes.c_void_p)]
+
+
+class MoePacked(ctypes.Structure):
+    """Mirror of struct moe_packed."""
+    _fields_ = [("batch", ctypes.c_int32), ("rows_q", ctypes.c_int32), ("rows_k", ctypes.c_int32),
+                ("max_q", ctypes.c_int32), ("cu_q", ctypes.c_void_p), ("cu_k", ctypes.c_void_p),
+                ("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built; run `python -m bit_quantized_moe_02_amd.build`")
     lib = ctypes.CDLL(LIB_PATH)
     vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    f64 = ctypes.c_double
     sig = {
         "moe_codebook_generate": (ctypes.c_int, [ctypes.c_uint64, vp]),
         "moe_packed_bytes": (sz, [ctypes.c_int, i64, i64]),
@@ -108,6 +144,16 @@ def _load():
         "moe_expert_cache_state": (ctypes.c_int, [vp, vp, ctypes.POINTER(i64), ctypes.POINTER(i64)]),
         "moe_layer_decode_streamed_workspace_bytes": (sz, [vp, i32, i32]),
         "moe_layer_decode_streamed": (ctypes.c_int, [vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, sz, vp, vp]),
+        "moe_kv_code_bytes": (sz, [i32, i32, i32, i32]),
+        "moe_kv_scale_bytes": (sz, [i32, i32, i32]),
+        "moe_rope_freqs": (ctypes.c_int, [i32, f64, ctypes.c_int, f64, f64, f64, f64, vp]),
+        "moe_kv_append": (ctypes.c_int, [vp, vp, vp, ctypes.c_int, vp, i64, i32, vp, i64, vp, i64, vp, i64, vp, i64, vp]),
+        "moe_kv_read": (ctypes.c_int, [vp, vp, ctypes.c_int, vp, i64, vp, i64, vp]),
+        "moe_attn_decode_workspace_bytes": (sz, [vp, vp, i32]),
+        "moe_attn_decode": (ctypes.c_int, [vp, vp, ctypes.c_int, vp, i64, i32, ctypes.c_float, vp, i64, vp, vp, sz, vp]),
+        "moe_attn_prefill_workspace_bytes": (sz, [vp]),
+        "moe_attn_prefill": (ctypes.c_int, [vp, ctypes.c_int, vp, i64, vp, i64, vp, i64, ctypes.c_float, ctypes.c_int, vp, i64,
+                                            vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -421,3 +467,188 @@ class ExpertCache:
             self.close()
         except Exception:
             pass
+
+
+# ---------------------------------------------------------------------------
+# Attention (include/qmoe_attn.h).
+
+
+_DTYPE = {torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16}
+
+
+def _here(t, name):
+    """Refuses a tensor that is not on the current device, where the library launches."""
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+
+
+def _rows(t, name, heads, dim, n, dtype=None):
+    """(address, row stride) of a row tensor [>= n, heads, dim] whose heads lie back to back."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _DTYPE or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name} must be {dtype or 'torch.bfloat16 or torch.float16'}, not {t.dtype}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or t.shape[0] < n:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; the call needs [{n}, {heads}, {dim}]")
+    stride = t.stride()
+    if stride[2] != 1 or (stride[1] != dim and heads > 1):
+        raise ValueError(f"{name}'s heads must lie back to back")
+    _here(t, name)
+    return t.data_ptr(), stride[0] if t.shape[0] > 1 else max(stride[0], heads * dim)
+
+
+def _vec(t, name, dtype, n, optional=False):
+    p = _dev(t, name, dtype, n, optional)
+    if p is not None:
+        _here(t, name)
+    return p
+
+
+def _lse(t, n):
+    return _vec(t, "lse", torch.float32, n, optional=True)
+
+
+def moe_kv_code_bytes(n_pages: int, page_tokens: int, kv_heads: int, head_dim: int) -> int:
+    return int(lib.moe_kv_code_bytes(n_pages, page_tokens, kv_heads, head_dim))
+
+
+def moe_kv_scale_bytes(n_pages: int, page_tokens: int, kv_heads: int) -> int:
+    return int(lib.moe_kv_scale_bytes(n_pages, page_tokens, kv_heads))
+
+
+def moe_rope_freqs(rot_dim, base=10000.0, rule="plain", factor=1.0, trained=0.0, slow=1.0, fast=32.0) -> np.ndarray:
+    """Radians a position of each pair, fp64 [rot_dim/2] (host)."""
+    out = np.empty(max(int(rot_dim) // 2, 1), np.float64)
+    _check(lib.moe_rope_freqs(rot_dim, base, MOE_ROPE.get(rule, rule), factor, trained, slow, fast, out.ctypes.data))
+    return out
+
+
+class KvCache:
+    """A paged 8-bit cache (struct moe_kv_cache) over the caller's `codes` and
+    `scales` tensors (uint8 and fp32, any shape, contiguous), or over new ones
+    where they are None (n_pages is then required)."""
+
+    def __init__(self, codes, scales, page_tokens, kv_heads, head_dim, n_pages=None):
+        if n_pages is None:
+            per = moe_kv_code_bytes(1, page_tokens, kv_heads, head_dim)
+            if codes is None or per == 0:
+                raise ValueError("n_pages is required without codes; page_tokens, kv_heads, head_dim must be valid")
+            n_pages = codes.numel() // per
+        nc, ns = moe_kv_code_bytes(n_pages, page_tokens, kv_heads, head_dim), moe_kv_scale_bytes(n_pages, page_tokens, kv_heads)
+        if nc == 0:
+            raise ValueError("bad cache geometry")
+        if codes is None:
+            codes = torch.empty(nc, dtype=torch.uint8, device="cuda")
+        if scales is None:
+            scales = torch.empty(ns // 4, dtype=torch.float32, device="cuda")
+        self.codes, self.scales = codes, scales
+        self.n_pages, self.page_tokens, self.kv_heads, self.head_dim = n_pages, page_tokens, kv_heads, head_dim
+        self.c = MoeKvCache(n_pages, page_tokens, kv_heads, head_dim, _dev(codes, "codes", torch.uint8, nc),
+                            _dev(scales, "scales", torch.float32, ns // 4))
+        self.ref = ctypes.byref(self.c)
+
+
+class KvBatch:
+    """A step's sequences (struct moe_kv_batch): page_table int32 [batch, pages] (rows may be strided), kv_lens
+    int32 [batch], `rows` new rows in all, at most `max_new` of one sequence; cu_rows int32 [batch+1] or None (the
+    same number each)."""
+
+    def __init__(self, page_table, kv_lens, rows, max_new=None, cu_rows=None):
+        if not isinstance(page_table, torch.Tensor) or not page_table.is_cuda or page_table.dim() != 2 or page_table.dtype != torch.int32:
+            raise ValueError("page_table must be a 2-dimensional int32 CUDA tensor")
+        batch, pages = page_table.shape
+        if page_table.stride(1) != 1 and pages > 1:
+            raise ValueError("page_table's rows must be contiguous")
+        if max_new is None:
+            if cu_rows is not None or batch == 0:
+                raise ValueError("max_new is required with cu_rows")
+            max_new = rows // batch
+        self.tensors = (page_table, kv_lens, cu_rows)
+        self.batch, self.rows = batch, rows
+        self.c = MoeKvBatch(batch, rows, max_new, pages, page_table.data_ptr(),
+                            page_table.stride(0) if batch > 1 else max(page_table.stride(0), pages),
+                            _dev(kv_lens, "kv_lens", torch.int32, batch),
+                            _dev(cu_rows, "cu_rows", torch.int32, batch + 1, optional=True))
+        self.ref = ctypes.byref(self.c)
+
+
+class Rope:
+    """Rotary positions (struct moe_rope): freqs fp64 CUDA [rot_dim/2] (moe_rope_freqs)."""
+
+    def __init__(self, freqs, rot_dim, interleaved=False, scale=1.0):
+        self.freqs = freqs
+        self.c = MoeRope(rot_dim, int(bool(interleaved)), scale,
+                         _dev(freqs, "freqs", torch.float64, rot_dim // 2, optional=rot_dim == 0))
+        self.ref = ctypes.byref(self.c)
+
+
+def _on_device(cache, batch):
+    _here(cache.codes, "the cache")
+    _here(batch.tensors[0], "page_table")
+
+
+def moe_kv_append(cache, batch, k, v, rope=None, q=None, q_out=None, k_out=None, stream=None):
+    """k, v (and q) [rows, heads, head_dim], any row stride; q turned into q_out (may be q), k_out (may be k or None)."""
+    H, D, n = cache.kv_heads, cache.head_dim, batch.rows
+    _on_device(cache, batch)
+    if rope is not None and rope.freqs is not None:
+        _here(rope.freqs, "freqs")
+    kp, ks = _rows(k, "k", H, D, n)
+    vp, vs = _rows(v, "v", H, D, n, k.dtype)
+    qp = qs = hq = qop = qos = kop = kos = 0
+    if q is not None:
+        hq = q.shape[1] if q.dim() == 3 else 0
+        qp, qs = _rows(q, "q", hq, D, n, k.dtype)
+        qop, qos = _rows(q_out, "q_out", hq, D, n, k.dtype)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if k_out is not None:
+        kop, kos = _rows(k_out, "k_out", H, D, n, k.dtype)
+    _check(lib.moe_kv_append(cache.ref, batch.ref, rope.ref if rope is not None else None, _DTYPE[k.dtype], qp or None, qs,
+                             hq, kp, ks, vp, vs, qop or None, qos, kop or None, kos, _stream(stream)))
+
+
+def moe_kv_read(cache, batch, k_out, v_out, stream=None):
+    """Rows of the batch's last positions into k_out, v_out [rows, kv_heads, head_dim]."""
+    _on_device(cache, batch)
+    kp, ks = _rows(k_out, "k_out", cache.kv_heads, cache.head_dim, batch.rows)
+    vp, vs = _rows(v_out, "v_out", cache.kv_heads, cache.head_dim, batch.rows, k_out.dtype)
+    _check(lib.moe_kv_read(cache.ref, batch.ref, _DTYPE[k_out.dtype], kp, ks, vp, vs, _stream(stream)))
+
+
+def moe_attn_decode_workspace_bytes(cache, batch, q_heads: int) -> int:
+    return int(lib.moe_attn_decode_workspace_bytes(cache.ref, batch.ref, q_heads))
+
+
+def moe_attn_decode(cache, batch, q, out, ws, scale, lse=None, stream=None):
+    """q, out [rows, q_heads, head_dim]; lse fp32 [rows, q_heads] or None."""
+    D, n = cache.head_dim, batch.rows
+    _on_device(cache, batch)
+    hq = q.shape[1] if q.dim() == 3 else 0
+    qp, qs = _rows(q, "q", hq, D, n)
+    op, os_ = _rows(out, "out", hq, D, n, q.dtype)
+    _check(lib.moe_attn_decode(cache.ref, batch.ref, _DTYPE[q.dtype], qp, qs, hq, scale, op, os_, _lse(lse, n * hq), *_ws(ws),
+                               _stream(stream)))
+
+
+def moe_attn_prefill_workspace_bytes(rows_q: int, batch: int, max_q: int, rows_k: int, q_heads: int, kv_heads: int,
+                                     head_dim: int) -> int:
+    # (which rows belong to which sequence does not matter here: any offsets stand for them)
+    p = MoePacked(batch, rows_q, rows_k, max_q, 1, 1, q_heads, kv_heads, head_dim)
+    return int(lib.moe_attn_prefill_workspace_bytes(ctypes.byref(p)))
+
+
+def moe_attn_prefill(q, k, v, cu_q, cu_k, max_q, out, ws, scale, causal=True, lse=None, stream=None):
+    """q, out [rows_q, q_heads, head_dim]; k, v [rows_k, kv_heads, head_dim]; cu_q, cu_k int32 [batch+1]."""
+    if any(t.dim() != 3 for t in (q, k, v)):
+        raise ValueError("q, k and v must be [rows, heads, head_dim]")
+    nq, hq, D = q.shape
+    nk, hk = k.shape[:2]
+    qp, qs = _rows(q, "q", hq, D, nq)
+    kp, ks = _rows(k, "k", hk, D, nk, q.dtype)
+    vp, vs = _rows(v, "v", hk, D, nk, q.dtype)
+    op, os_ = _rows(out, "out", hq, D, nq, q.dtype)
+    batch = cu_q.numel() - 1
+    p = MoePacked(batch, nq, nk, max_q, _vec(cu_q, "cu_q", torch.int32, 2), _vec(cu_k, "cu_k", torch.int32, batch + 1), hq, hk, D)
+    _check(lib.moe_attn_prefill(ctypes.byref(p), _DTYPE[q.dtype], qp, qs, kp, ks, vp, vs, scale, int(bool(causal)), op, os_,
+                                _lse(lse, nq * hq), *_ws(ws), _stream(stream)))
