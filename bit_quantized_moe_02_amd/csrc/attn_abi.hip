@@ -4,6 +4,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <string>
 
 #include "../../include/qmoe_attn.h"
@@ -28,10 +29,15 @@ int hip_fail(const char* who, hipError_t e) {
   return fail(MOE_ERR_HIP, std::string(who) + ": " + hipGetErrorString(e));
 }
 
+// Compute units of the current device (asked for once per device).
 int n_cus() {
+  static std::atomic<int> known[64];
   int dev = 0, cus = 0;
-  if (hipGetDevice(&dev) != hipSuccess) return 256;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+  cus = known[dev].load(std::memory_order_relaxed);
+  if (cus > 0) return cus;
   if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus <= 0) return 256;
+  known[dev].store(cus, std::memory_order_relaxed);
   return cus;
 }
 
@@ -100,22 +106,26 @@ int check_heads(const char* who, int q_heads, int kv_heads) {
   return MOE_OK;
 }
 
-// Grids of the attention kernels: 16-row tiles in the third dimension.
+// Grids of the attention kernels: 16-row tiles in the third dimension, a join for each row.
 int check_attn_grid(const char* who, int64_t batch, int64_t max_new, int64_t q_heads, int64_t kv_heads) {
-  if (batch * kv_heads > kMaxGrid || (max_new * (q_heads / kv_heads) + 15) / 16 > 65535 || batch * max_new > kMaxGrid)
+  if (batch > (1 << 20) || (max_new * (q_heads / kv_heads) + 15) / 16 > 65535 || batch * max_new > kMaxGrid)
     return bad(who, "batch, max_new or heads too large");
   return MOE_OK;
 }
 
 struct AttnWs {
-  size_t o, ml, total;
+  size_t o, ml, where, total;
 };
 
-AttnWs attn_ws(int n_split, int64_t rows, int q_heads, int dim) {
-  AttnWs w;
-  w.o = 0;
-  w.ml = n_split > 1 ? align_up((size_t)n_split * rows * q_heads * dim * 4) : 0;
-  w.total = n_split > 1 ? w.ml + align_up((size_t)n_split * rows * q_heads * 8) : kAlign;
+// `n` ranges over B contexts make at most n + B - 1 parts.
+AttnWs attn_ws(int n, const KvArgs& kv, int q_heads) {
+  AttnWs w{0, 0, 0, kAlign};
+  if (n > 1) {
+    const size_t rows = ((size_t)n + kv.B) * kv.max_new * q_heads;
+    w.ml = align_up(rows * kv.D * 4);
+    w.where = w.ml + align_up(rows * 8);
+    w.total = w.where + align_up((size_t)kv.B * 8);
+  }
   return w;
 }
 
@@ -241,7 +251,7 @@ extern "C" size_t moe_attn_decode_workspace_bytes(const moe_kv_cache* cache, con
   clear_error();
   KvArgs kv{};
   if (check_decode_args("moe_attn_decode_workspace_bytes", cache, batch, q_heads, &kv) != MOE_OK) return 0;
-  return attn_ws(attn_decode_splits(kv, q_heads, n_cus()), kv.T, q_heads, kv.D).total;
+  return attn_ws(attn_decode_workers(kv, q_heads, n_cus()), kv, q_heads).total;
 }
 
 extern "C" int moe_attn_decode(const moe_kv_cache* cache, const moe_kv_batch* batch, int dtype, const void* q,
@@ -257,8 +267,8 @@ extern "C" int moe_attn_decode(const moe_kv_cache* cache, const moe_kv_batch* ba
   if ((rc = check_rows(who, "out", out, out_stride, q_heads, a.kv.D)) != MOE_OK) return rc;
   if (!(scale > 0) || !isfinite(scale)) return bad(who, "scale must be positive and finite");
   if (!ws || !aligned16(ws)) return bad(who, "ws must be 16-byte aligned memory");
-  const int n = attn_decode_splits(a.kv, q_heads, n_cus());
-  const AttnWs w = attn_ws(n, a.kv.T, q_heads, a.kv.D);
+  const int n = attn_decode_workers(a.kv, q_heads, n_cus());
+  const AttnWs w = attn_ws(n, a.kv, q_heads);
   if (ws_bytes < w.total)
     return fail(MOE_ERR_WORKSPACE, std::string(who) + ": workspace too small (need " + std::to_string(w.total) + ")");
   a.q = q;
@@ -268,15 +278,9 @@ extern "C" int moe_attn_decode(const moe_kv_cache* cache, const moe_kv_batch* ba
   a.os = out_stride;
   a.Hq = q_heads;
   a.c = scale * 1.4426950408889634f;
-  a.split = {(float*)((uint8_t*)ws + w.o), (float*)((uint8_t*)ws + w.ml), n};
+  a.split = {(float*)((uint8_t*)ws + w.o), (float*)((uint8_t*)ws + w.ml), (int2*)((uint8_t*)ws + w.where), n};
   hipError_t e = launch_attn_decode(a, dtype, (hipStream_t)stream);
-  if (e != hipSuccess) return hip_fail(who, e);
-  if (n > 1) {
-    const JoinArgs j{a.split, a.kv.cu, a.kv.B, a.kv.T, q_heads, a.kv.D, a.kv.max_new, a.kv.per_seq, out, lse, out_stride};
-    e = launch_attn_join(j, dtype, (hipStream_t)stream);
-    if (e != hipSuccess) return hip_fail(who, e);
-  }
-  return MOE_OK;
+  return e == hipSuccess ? MOE_OK : hip_fail(who, e);
 }
 
 namespace {
@@ -315,7 +319,7 @@ extern "C" size_t moe_attn_prefill_workspace_bytes(const moe_packed* p) {
   clear_error();
   PrefillArgs a{};
   if (check_packed("moe_attn_prefill_workspace_bytes", p, &a) != MOE_OK) return 0;
-  return attn_ws(attn_prefill_splits(a.B, a.Tq, a.Tk, a.max_q, a.Hq, a.Hk, a.D, n_cus()), a.Tq, a.Hq, a.D).total;
+  return kAlign;
 }
 
 extern "C" int moe_attn_prefill(const moe_packed* p, int dtype, const void* q, int64_t q_stride, const void* k,
@@ -335,11 +339,8 @@ extern "C" int moe_attn_prefill(const moe_packed* p, int dtype, const void* q, i
   if ((rc = check_rows(who, "out", out, out_stride, a.Hq, a.D)) != MOE_OK) return rc;
   if (!(scale > 0) || !isfinite(scale)) return bad(who, "scale must be positive and finite");
   if (!ws || !aligned16(ws)) return bad(who, "ws must be 16-byte aligned memory");
-  const int cus = n_cus();
-  const int n = attn_prefill_splits(a.B, a.Tq, a.Tk, a.max_q, a.Hq, a.Hk, a.D, cus);
-  const AttnWs w = attn_ws(n, a.Tq, a.Hq, a.D);
-  if (ws_bytes < w.total)
-    return fail(MOE_ERR_WORKSPACE, std::string(who) + ": workspace too small (need " + std::to_string(w.total) + ")");
+  if (ws_bytes < kAlign)
+    return fail(MOE_ERR_WORKSPACE, std::string(who) + ": workspace too small (need " + std::to_string(kAlign) + ")");
   a.q = q;
   a.k = k;
   a.v = v;
@@ -351,13 +352,6 @@ extern "C" int moe_attn_prefill(const moe_packed* p, int dtype, const void* q, i
   a.os = out_stride;
   a.c = scale * 1.4426950408889634f;
   a.causal = causal != 0;
-  a.split = {(float*)((uint8_t*)ws + w.o), (float*)((uint8_t*)ws + w.ml), n};
-  hipError_t e = launch_attn_prefill(a, dtype, cus, (hipStream_t)stream);
-  if (e != hipSuccess) return hip_fail(who, e);
-  if (n > 1) {
-    const JoinArgs j{a.split, a.cu_q, a.B, a.Tq, a.Hq, a.D, a.max_q, a.per_q, out, lse, out_stride};
-    e = launch_attn_join(j, dtype, (hipStream_t)stream);
-    if (e != hipSuccess) return hip_fail(who, e);
-  }
-  return MOE_OK;
+  hipError_t e = launch_attn_prefill(a, dtype, n_cus(), (hipStream_t)stream);
+  return e == hipSuccess ? MOE_OK : hip_fail(who, e);
 }

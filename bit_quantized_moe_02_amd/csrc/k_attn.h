@@ -42,13 +42,15 @@ struct ReadArgs {
 };
 hipError_t launch_kv_read(const ReadArgs& a, int dtype, hipStream_t s);
 
-// Parts of a row's context that attention computes apart, joined by
-// launch_attn_join: un-normalised sums [n_split][T][Hq][D] and (maximum in
-// powers of two, sum) [n_split][T][Hq][2].
+// Sums of parts of contexts, for the join: un-normalised outputs
+// [part][max_new][Hq][D] and (maximum in powers of two, sum)
+// [part][max_new][Hq][2], and for each sequence its first part's range and
+// its number of parts.
 struct SplitBuf {
   float* o;
   float* ml;
-  int n;                    // 1: no parts, the kernel writes the outputs itself
+  int2* where;
+  int n;                    // ranges the contexts are cut into (1: no join)
 };
 
 struct DecodeArgs {
@@ -61,7 +63,7 @@ struct DecodeArgs {
   float c;                  // scale * log2(e)
   SplitBuf split;
 };
-int attn_decode_splits(const KvArgs& kv, int Hq, int cus);
+int attn_decode_workers(const KvArgs& kv, int Hq, int cus);
 hipError_t launch_attn_decode(const DecodeArgs& a, int dtype, hipStream_t s);
 
 struct PrefillArgs {
@@ -74,21 +76,7 @@ struct PrefillArgs {
   int64_t qs, ks, vs, os;
   float c;
   int causal;
-  SplitBuf split;
 };
-int attn_prefill_splits(int B, int Tq, int Tk, int max_q, int Hq, int Hk, int D, int cus);
 hipError_t launch_attn_prefill(const PrefillArgs& a, int dtype, int cus, hipStream_t s);
-
-// Joins the parts of rows 0..T-1 (rows outside every sequence are left as
-// they are: cu/per_seq/B/max_new as above).
-struct JoinArgs {
-  SplitBuf split;
-  const int32_t* cu;
-  int B, T, Hq, D, max_new, per_seq;
-  void* out;
-  float* lse;
-  int64_t os;
-};
-hipError_t launch_attn_join(const JoinArgs& a, int dtype, hipStream_t s);
 
 }  // namespace qmoe

@@ -303,11 +303,6 @@ hipError_t by_dim(const PrefillArgs& a, hipStream_t s) {
 
 namespace qmoe {
 
-int attn_prefill_splits(int B, int Tq, int Tk, int max_q, int Hq, int Hk, int D, int cus) {
-  (void)B; (void)Tq; (void)Tk; (void)max_q; (void)Hq; (void)Hk; (void)D; (void)cus;
-  return 1;
-}
-
 hipError_t launch_attn_prefill(const PrefillArgs& a, int dtype, int cus, hipStream_t s) {
   (void)cus;
   return dtype == 0 ? by_dim<Bf16>(a, s) : by_dim<F16>(a, s);

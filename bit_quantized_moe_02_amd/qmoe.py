@@ -476,36 +476,48 @@ class ExpertCache:
 _DTYPE = {torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16}
 
 
-def _here(t, name):
-    """Refuses a tensor that is not on the current device, where the library launches."""
-    if t.device.index != torch.cuda.current_device():
+def _device():
+    """Index of the current device, where the library launches."""
+    return torch._C._cuda_getDevice()
+
+
+def _here(t, name, dev):
+    if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, not on the current device")
 
 
-def _rows(t, name, heads, dim, n, dtype=None):
-    """(address, row stride) of a row tensor [>= n, heads, dim] whose heads lie back to back."""
+def _rows(t, name, heads, dim, n, dtype, dev):
+    """(address, row stride) of a row tensor [>= n, heads, dim] of `dtype` on device `dev`, its heads back to back."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in _DTYPE or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{name} must be {dtype or 'torch.bfloat16 or torch.float16'}, not {t.dtype}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or t.shape[0] < n:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}; the call needs [{n}, {heads}, {dim}]")
-    stride = t.stride()
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim or shape[0] < n:
+        raise ValueError(f"{name} has shape {tuple(shape)}; the call needs [{n}, {heads}, {dim}]")
     if stride[2] != 1 or (stride[1] != dim and heads > 1):
         raise ValueError(f"{name}'s heads must lie back to back")
-    _here(t, name)
-    return t.data_ptr(), stride[0] if t.shape[0] > 1 else max(stride[0], heads * dim)
+    if t.get_device() != dev:
+        _here(t, name, dev)
+    return t.data_ptr(), stride[0] if shape[0] > 1 else heads * dim
 
 
-def _vec(t, name, dtype, n, optional=False):
+def _type(t, name):
+    """Library code of a row tensor's type."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPE or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor of torch.bfloat16 or torch.float16")
+    return _DTYPE[t.dtype]
+
+
+def _vec(t, name, dtype, n, dev, optional=False):
     p = _dev(t, name, dtype, n, optional)
     if p is not None:
-        _here(t, name)
+        _here(t, name, dev)
     return p
 
 
-def _lse(t, n):
-    return _vec(t, "lse", torch.float32, n, optional=True)
+def _stream_on(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def moe_kv_code_bytes(n_pages: int, page_tokens: int, kv_heads: int, head_dim: int) -> int:
@@ -545,6 +557,8 @@ class KvCache:
         self.n_pages, self.page_tokens, self.kv_heads, self.head_dim = n_pages, page_tokens, kv_heads, head_dim
         self.c = MoeKvCache(n_pages, page_tokens, kv_heads, head_dim, _dev(codes, "codes", torch.uint8, nc),
                             _dev(scales, "scales", torch.float32, ns // 4))
+        self.device = codes.get_device()
+        _here(scales, "scales", self.device)
         self.ref = ctypes.byref(self.c)
 
 
@@ -569,6 +583,10 @@ class KvBatch:
                             page_table.stride(0) if batch > 1 else max(page_table.stride(0), pages),
                             _dev(kv_lens, "kv_lens", torch.int32, batch),
                             _dev(cu_rows, "cu_rows", torch.int32, batch + 1, optional=True))
+        self.device = page_table.get_device()
+        for t, name in ((kv_lens, "kv_lens"), (cu_rows, "cu_rows")):
+            if t is not None:
+                _here(t, name, self.device)
         self.ref = ctypes.byref(self.c)
 
 
@@ -579,41 +597,51 @@ class Rope:
         self.freqs = freqs
         self.c = MoeRope(rot_dim, int(bool(interleaved)), scale,
                          _dev(freqs, "freqs", torch.float64, rot_dim // 2, optional=rot_dim == 0))
+        self.device = None if freqs is None else freqs.get_device()
         self.ref = ctypes.byref(self.c)
 
 
-def _on_device(cache, batch):
-    _here(cache.codes, "the cache")
-    _here(batch.tensors[0], "page_table")
+def _step(cache, batch):
+    """The current device, which must be the cache's and the batch's."""
+    dev = _device()
+    if cache.device != dev or batch.device != dev:
+        raise ValueError(f"the cache is on device {cache.device}, the batch on {batch.device}, the current one is {dev}")
+    return dev
 
 
 def moe_kv_append(cache, batch, k, v, rope=None, q=None, q_out=None, k_out=None, stream=None):
     """k, v (and q) [rows, heads, head_dim], any row stride; q turned into q_out (may be q), k_out (may be k or None)."""
     H, D, n = cache.kv_heads, cache.head_dim, batch.rows
-    _on_device(cache, batch)
-    if rope is not None and rope.freqs is not None:
-        _here(rope.freqs, "freqs")
-    kp, ks = _rows(k, "k", H, D, n)
-    vp, vs = _rows(v, "v", H, D, n, k.dtype)
-    qp = qs = hq = qop = qos = kop = kos = 0
+    dev, code, dt = _step(cache, batch), _type(k, "k"), k.dtype
+    if rope is not None and rope.device not in (None, dev):
+        raise ValueError(f"rope is on device {rope.device}, the current one is {dev}")
+    kp, ks = _rows(k, "k", H, D, n, dt, dev)
+    vp, vs = _rows(v, "v", H, D, n, dt, dev)
+    qp = qop = kop = None
+    qs = hq = qos = kos = 0
     if q is not None:
         hq = q.shape[1] if q.dim() == 3 else 0
-        qp, qs = _rows(q, "q", hq, D, n, k.dtype)
-        qop, qos = _rows(q_out, "q_out", hq, D, n, k.dtype)
+        qp, qs = _rows(q, "q", hq, D, n, dt, dev)
+        qop, qos = _rows(q_out, "q_out", hq, D, n, dt, dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
     if k_out is not None:
-        kop, kos = _rows(k_out, "k_out", H, D, n, k.dtype)
-    _check(lib.moe_kv_append(cache.ref, batch.ref, rope.ref if rope is not None else None, _DTYPE[k.dtype], qp or None, qs,
-                             hq, kp, ks, vp, vs, qop or None, qos, kop or None, kos, _stream(stream)))
+        kop, kos = _rows(k_out, "k_out", H, D, n, dt, dev)
+    rc = lib.moe_kv_append(cache.ref, batch.ref, rope.ref if rope is not None else None, code, qp, qs, hq, kp, ks, vp, vs,
+                           qop, qos, kop, kos, _stream_on(stream, dev))
+    if rc:
+        _check(rc)
 
 
 def moe_kv_read(cache, batch, k_out, v_out, stream=None):
     """Rows of the batch's last positions into k_out, v_out [rows, kv_heads, head_dim]."""
-    _on_device(cache, batch)
-    kp, ks = _rows(k_out, "k_out", cache.kv_heads, cache.head_dim, batch.rows)
-    vp, vs = _rows(v_out, "v_out", cache.kv_heads, cache.head_dim, batch.rows, k_out.dtype)
-    _check(lib.moe_kv_read(cache.ref, batch.ref, _DTYPE[k_out.dtype], kp, ks, vp, vs, _stream(stream)))
+    H, D, n = cache.kv_heads, cache.head_dim, batch.rows
+    dev, code, dt = _step(cache, batch), _type(k_out, "k_out"), k_out.dtype
+    kp, ks = _rows(k_out, "k_out", H, D, n, dt, dev)
+    vp, vs = _rows(v_out, "v_out", H, D, n, dt, dev)
+    rc = lib.moe_kv_read(cache.ref, batch.ref, code, kp, ks, vp, vs, _stream_on(stream, dev))
+    if rc:
+        _check(rc)
 
 
 def moe_attn_decode_workspace_bytes(cache, batch, q_heads: int) -> int:
@@ -623,12 +651,15 @@ def moe_attn_decode_workspace_bytes(cache, batch, q_heads: int) -> int:
 def moe_attn_decode(cache, batch, q, out, ws, scale, lse=None, stream=None):
     """q, out [rows, q_heads, head_dim]; lse fp32 [rows, q_heads] or None."""
     D, n = cache.head_dim, batch.rows
-    _on_device(cache, batch)
+    dev, code, dt = _step(cache, batch), _type(q, "q"), q.dtype
     hq = q.shape[1] if q.dim() == 3 else 0
-    qp, qs = _rows(q, "q", hq, D, n)
-    op, os_ = _rows(out, "out", hq, D, n, q.dtype)
-    _check(lib.moe_attn_decode(cache.ref, batch.ref, _DTYPE[q.dtype], qp, qs, hq, scale, op, os_, _lse(lse, n * hq), *_ws(ws),
-                               _stream(stream)))
+    qp, qs = _rows(q, "q", hq, D, n, dt, dev)
+    op, os_ = _rows(out, "out", hq, D, n, dt, dev)
+    rc = lib.moe_attn_decode(cache.ref, batch.ref, code, qp, qs, hq, scale, op, os_,
+                             _vec(lse, "lse", torch.float32, n * hq, dev, optional=True),
+                             _vec(ws, "ws", torch.uint8, 0, dev), ws.numel(), _stream_on(stream, dev))
+    if rc:
+        _check(rc)
 
 
 def moe_attn_prefill_workspace_bytes(rows_q: int, batch: int, max_q: int, rows_k: int, q_heads: int, kv_heads: int,
@@ -640,15 +671,21 @@ def moe_attn_prefill_workspace_bytes(rows_q: int, batch: int, max_q: int, rows_k
 
 def moe_attn_prefill(q, k, v, cu_q, cu_k, max_q, out, ws, scale, causal=True, lse=None, stream=None):
     """q, out [rows_q, q_heads, head_dim]; k, v [rows_k, kv_heads, head_dim]; cu_q, cu_k int32 [batch+1]."""
-    if any(t.dim() != 3 for t in (q, k, v)):
-        raise ValueError("q, k and v must be [rows, heads, head_dim]")
+    code, dt = _type(q, "q"), q.dtype
+    dev = _device()
+    if q.dim() != 3 or _type(k, "k") != code or k.dim() != 3:
+        raise ValueError("q and k must be [rows, heads, head_dim] of one type")
     nq, hq, D = q.shape
     nk, hk = k.shape[:2]
-    qp, qs = _rows(q, "q", hq, D, nq)
-    kp, ks = _rows(k, "k", hk, D, nk, q.dtype)
-    vp, vs = _rows(v, "v", hk, D, nk, q.dtype)
-    op, os_ = _rows(out, "out", hq, D, nq, q.dtype)
+    qp, qs = _rows(q, "q", hq, D, nq, dt, dev)
+    kp, ks = _rows(k, "k", hk, D, nk, dt, dev)
+    vp, vs = _rows(v, "v", hk, D, nk, dt, dev)
+    op, os_ = _rows(out, "out", hq, D, nq, dt, dev)
+    cq = _vec(cu_q, "cu_q", torch.int32, 2, dev)
     batch = cu_q.numel() - 1
-    p = MoePacked(batch, nq, nk, max_q, _vec(cu_q, "cu_q", torch.int32, 2), _vec(cu_k, "cu_k", torch.int32, batch + 1), hq, hk, D)
-    _check(lib.moe_attn_prefill(ctypes.byref(p), _DTYPE[q.dtype], qp, qs, kp, ks, vp, vs, scale, int(bool(causal)), op, os_,
-                                _lse(lse, nq * hq), *_ws(ws), _stream(stream)))
+    p = MoePacked(batch, nq, nk, max_q, cq, _vec(cu_k, "cu_k", torch.int32, batch + 1, dev), hq, hk, D)
+    rc = lib.moe_attn_prefill(ctypes.byref(p), code, qp, qs, kp, ks, vp, vs, scale, 1 if causal else 0, op, os_,
+                              _vec(lse, "lse", torch.float32, nq * hq, dev, optional=True),
+                              _vec(ws, "ws", torch.uint8, 0, dev), ws.numel(), _stream_on(stream, dev))
+    if rc:
+        _check(rc)

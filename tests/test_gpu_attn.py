@@ -298,6 +298,22 @@ def test_decode_special_values(q, dt):
     _decode(q, cache, to_device(q, cache), table, lens, ns, 4, dt, rng, "special values", sigma=6.0)
 
 
+@pytest.mark.parametrize("pad", [0, 60])
+def test_decode_many_sequences(q, pad):
+    """150 sequences of mixed lengths, empty slots and sequences without rows among them, so that ranges of the work
+    begin and end anywhere; with wide page tables too."""
+    rng = np.random.default_rng(43)
+    Hk, D, page, B = 1, 64, 16, 150
+    lens = [int(x) for x in rng.integers(0, 200, B)]
+    lens[3], lens[70], lens[149] = 900, 0, 700
+    ns = [int(x) for x in rng.integers(0, 3, B)]
+    ns[3], ns[70], ns[149] = 2, 1, 1
+    table, n_pages = page_table(rng, lens, page, width=57 + pad)
+    cache = A.Cache(*random_cache(rng, n_pages, page, Hk, D), page, Hk, D)
+    spoil_tails(cache, table, lens)
+    _decode(q, cache, to_device(q, cache), table, lens, ns, 2, torch.float16, rng, "many sequences", extra=1)
+
+
 def test_decode_bad_pages(q):
     """Pages that are none of the cache's hold no tokens; a table of nothing else gives empty rows."""
     rng = np.random.default_rng(32)
