@@ -17,6 +17,7 @@ namespace {
 
 constexpr size_t kAlign = 256;
 constexpr int64_t kMaxRows = 1 << 24;       // rows of a call
+constexpr int64_t kMaxStride = 1 << 24;     // elements: a tile's offsets then fit 32 bits
 constexpr int64_t kMaxGrid = 0x7FFFFFFF;
 
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
@@ -57,8 +58,8 @@ int log2i(int v) {
 int check_rows(const char* who, const char* name, const void* p, int64_t stride, int heads, int dim) {
   if (!p) return bad(who, std::string(name) + " is NULL");
   if (!aligned16(p)) return bad(who, std::string(name) + " must be 16-byte aligned");
-  if (stride < (int64_t)heads * dim || stride % 8 != 0 || stride > (1ll << 32))
-    return bad(who, std::string(name) + "'s stride must be a multiple of 8 and at least heads * head_dim");
+  if (stride < (int64_t)heads * dim || stride % 8 != 0 || stride > kMaxStride)
+    return bad(who, std::string(name) + "'s stride must be a multiple of 8, at least heads * head_dim, at most 2^24");
   return MOE_OK;
 }
 

@@ -42,14 +42,7 @@ struct Bf16 {
   static __device__ __forceinline__ f32x16 mma32(const u32x4& a, const u32x4& b, const f32x16& c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
   }
-  static constexpr uint32_t kExpMask = 0x7F807F80u;   // both halves' exponents
   static constexpr uint32_t kExpOne = 0x7F80u;
-  static constexpr uint32_t kOnes = 0x3F803F80u;
-  // acc + w.lo + w.hi
-  static __device__ __forceinline__ float sum2(uint32_t w, float acc) {
-    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w), __builtin_bit_cast(bf16x2, kOnes), acc,
-                                           false);
-  }
 };
 
 struct F16 {
@@ -70,12 +63,7 @@ struct F16 {
   static __device__ __forceinline__ f32x16 mma32(const u32x4& a, const u32x4& b, const f32x16& c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
   }
-  static constexpr uint32_t kExpMask = 0x7C007C00u;
   static constexpr uint32_t kExpOne = 0x7C00u;
-  static constexpr uint32_t kOnes = 0x3C003C00u;
-  static __device__ __forceinline__ float sum2(uint32_t w, float acc) {
-    return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, w), __builtin_bit_cast(f16x2, kOnes), acc, false);
-  }
 };
 
 // Eight codes (two words) times a power of two: an MFMA operand.

@@ -11,6 +11,7 @@ namespace {
 
 constexpr int kTile = 64;                   // keys a workgroup stages at once
 constexpr int kWaves = 4;
+constexpr float kLazy = 8.f;                // how far a score may exceed the running maximum, in powers of 2
 constexpr int kThreads = 64 * kWaves;
 
 // K and V rows lie in LDS as they do in memory, 2*D bytes each, their
@@ -28,23 +29,48 @@ __device__ __forceinline__ int v_piece(int row, int piece) {
 
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 
-// Starts the copy of keys [j0, j0 + kTile) (rows behind the last repeat it)
-// into LDS: 1024 bytes an instruction, which go there in lane order.
-template <int D, bool V>
-__device__ __forceinline__ void stage(const uint16_t* base, int64_t stride, int j0, int len, uint8_t* lds, int wave,
-                                      int lane) {
-  constexpr int kPieces = D / 8;
-  constexpr int kPer = kTile * kPieces / 64 / kWaves;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int at = (wave * kPer + i) * 64 + lane;
-    const int row = at / kPieces, slot = at % kPieces;
-    const int piece = V ? v_piece<D>(row, slot) : k_piece<D>(row, slot);
-    const uint16_t* src = base + (int64_t)min(j0 + row, len - 1) * stride + 8 * piece;
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                     (__attribute__((address_space(3))) void*)(lds + (wave * kPer + i) * 1024), 16, 0, 0);
-  }
+// x, computed here and not before the loop: what only rare branches need
+// must not hold registers through the loop.
+__device__ __forceinline__ int only_here(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
 }
+
+// Copies tiles of keys into LDS: 1024 bytes an instruction, which go there in
+// lane order, so the permutation is in what each lane reads.  The reads go
+// through a buffer descriptor that ends behind the sequence's last row: rows
+// behind it come as zeros, and no tile needs a branch.
+template <int D, bool V>
+struct Stage {
+  static constexpr int kPieces = D / 8;
+  static constexpr int kPer = kTile * kPieces / 64 / kWaves;   // instructions of a wave
+  int off[kPer];                            // bytes of this lane's pieces from the tile's first row
+  const uint8_t* base;
+  int64_t row_bytes;
+
+  __device__ __forceinline__ void init(const void* p, int64_t stride, int wave, int lane) {
+    base = reinterpret_cast<const uint8_t*>(p);
+    row_bytes = 2 * stride;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int at = (wave * kPer + i) * 64 + lane, row = at / kPieces, slot = at % kPieces;
+      off[i] = row * (int)row_bytes + 16 * (V ? v_piece<D>(row, slot) : k_piece<D>(row, slot));
+    }
+  }
+  // keys [j0, j0 + kTile) of len
+  __device__ __forceinline__ void start(int j0, int len, uint8_t* lds, int wave) const {
+#ifdef __HIP_DEVICE_COMPILE__               // (the host pass does not know descriptors)
+    const int rows = min(len - j0, kTile);
+    const int bytes = rows > 0 ? (rows - 1) * (int)row_bytes + 2 * D : 0;
+    const __amdgpu_buffer_rsrc_t rsrc =
+        __builtin_amdgcn_make_buffer_rsrc((void*)(base + (rows > 0 ? j0 : 0) * row_bytes), 0, bytes, 0x00027000);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)(lds + (wave * kPer + i) * 1024),
+                                               16, off[i], 0, 0, 0);
+#endif
+  }
+};
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
@@ -61,118 +87,204 @@ struct Rows {
   int last[CT];                             // last key the row sees, -1: none
 };
 
-// One tile of keys.  With K as the first operand of a 32x32x16 product a
-// lane gets 16 of 32 keys of one query row (column lane % 32): maximum and
-// sum are nearly all inside a lane, and the weights are already the second
-// operand of the product with V, whose first operand (columns x keys) comes
-// out of LDS by transposing reads in the same order of keys.
+// Scores of a tile.  With K as the first operand of a 32x32x16 product a lane
+// gets 16 of 32 keys of one query row (column lane % 32): maximum and sum are
+// nearly all inside a lane, and the weights are already the second operand
+// of the product with V.
+template <int CT>
+struct Scores {
+  f32x16 s[CT][2];                          // key 32 i + 8 (e / 4) + 4 hh + e % 4 in s[.][i][e]
+};
+
 template <typename T, int D, int CT>
-__device__ __forceinline__ void tile_step(Rows<T, D, CT>& R, const uint8_t* kt, const uint8_t* vt, int j0, bool all,
-                                          float c, int lane) {
+__device__ __forceinline__ void scores(const Rows<T, D, CT>& R, Scores<CT>& S, const uint8_t* kt, int lane) {
   const int col = lane & 31, hh = lane >> 5;
-  f32x16 s[CT][2];
-#pragma unroll
-  for (int t = 0; t < CT; ++t)
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) s[t][i][e] = 0.f;
 #pragma unroll
   for (int kb = 0; kb < D / 16; ++kb) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const u32x4 k = *reinterpret_cast<const u32x4*>(kt + (32 * i + col) * (2 * D) + 16 * k_piece<D>(32 * i + col, 2 * kb + hh));
+      const u32x4 k = *reinterpret_cast<const u32x4*>(kt + ((32 * i + col) * (2 * D) + 16 * k_piece<D>(32 * i + col, 2 * kb + hh)));
 #pragma unroll
-      for (int t = 0; t < CT; ++t) s[t][i] = T::mma32(k, R.q[t][kb], s[t][i]);
+      for (int t = 0; t < CT; ++t) {
+        if (kb == 0)
+          S.s[t][i] = T::mma32(k, R.q[t][kb], f32x16{});
+        else
+          S.s[t][i] = T::mma32(k, R.q[t][kb], S.s[t][i]);
+      }
     }
   }
-  if (!all) {
-#pragma unroll
-    for (int t = 0; t < CT; ++t)
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (j0 + 32 * i + 8 * (e >> 2) + 4 * hh + (e & 3) > R.last[t]) s[t][i][e] = kMinusInf;
-  }
+}
+
+// Weights of a tile's 64 keys, as operands: four groups of 16 keys.
+template <int CT>
+struct Weights {
   u32x4 p[CT][4];
+};
+
+// Scores as powers of two under the running maximum, in place; says whether
+// some row's maximum has to be raised, and gives the tile's.  It is only
+// raised when a score exceeds it by 2^8 (or a row has none yet): the weights
+// are then at most 2^8, which costs no precision, and the sums are hardly ever
+// rescaled.
+// Masked: some row of the wave does not see some key of the tile.
+template <bool Masked, typename T, int D, int CT>
+__device__ __forceinline__ bool exponents(const Rows<T, D, CT>& R, Scores<CT>& S, float* mx, int j0, float c, int lane) {
+  const int hh = lane >> 5;
+  bool raise = false;
 #pragma unroll
   for (int t = 0; t < CT; ++t) {
-    float mx = kMinusInf;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int e = 0; e < 16; e += 2) mx = fmaxf(mx, fmaxf(s[t][i][e], s[t][i][e + 1]));
-    mx = max_halves(mx) * c;
-    if (__any(mx > R.m[t])) {
-      mx = fmaxf(R.m[t], mx);
-      const float r = R.m[t] == kMinusInf ? 0.f : exp2_fast(R.m[t] - mx);
-      R.l[t] *= r;
-#pragma unroll
-      for (int d = 0; d < D / 32; ++d) R.o[t][d] *= r;
-      R.m[t] = mx;
-    }
     const float base = R.m[t] == kMinusInf ? 0.f : R.m[t];
 #pragma unroll
+    for (int e = 0; e < 32; ++e) S.s[t][e >> 4][e & 15] = __builtin_fmaf(S.s[t][e >> 4][e & 15], c, -base);
+    if (Masked) {
+      const int seen = only_here(R.last[t] - j0 - 4 * hh);
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        if (32 * (e >> 4) + 8 * ((e & 15) >> 2) + (e & 3) > seen) S.s[t][e >> 4][e & 15] = kMinusInf;
+    }
+    float m[2];
+#pragma unroll
     for (int i = 0; i < 2; ++i) {
+      m[i] = fmaxf(fmaxf(S.s[t][i][0], S.s[t][i][1]), S.s[t][i][2]);
+#pragma unroll
+      for (int e = 3; e < 15; e += 2) m[i] = fmaxf(fmaxf(m[i], S.s[t][i][e]), S.s[t][i][e + 1]);
+      m[i] = fmaxf(m[i], S.s[t][i][15]);
+    }
+    mx[t] = max_halves(fmaxf(m[0], m[1]));
+    raise |= mx[t] > kLazy || (R.m[t] == kMinusInf && mx[t] > kMinusInf);
+  }
+  return __any(raise);
+}
+
+template <typename T, int D, int CT>
+__device__ __forceinline__ void raise_maximum(Rows<T, D, CT>& R, Scores<CT>& S, const float* mx) {
+#pragma unroll
+  for (int t = 0; t < CT; ++t) {
+    const bool raise = mx[t] > kLazy || (R.m[t] == kMinusInf && mx[t] > kMinusInf);
+    const float d = raise ? mx[t] : 0.f;
+    const float r = !raise ? 1.f : R.m[t] == kMinusInf ? 0.f : exp2_fast(-d);
+    if (raise) R.m[t] = (R.m[t] == kMinusInf ? 0.f : R.m[t]) + d;
+    R.l[t] *= r;
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) R.o[t][k] *= r;
+#pragma unroll
+    for (int e = 0; e < 32; ++e) S.s[t][e >> 4][e & 15] -= d;
+  }
+}
+
+template <typename T, int D, int CT>
+__device__ __forceinline__ void weights(Rows<T, D, CT>& R, const Scores<CT>& S, Weights<CT>& W) {
+#pragma unroll
+  for (int t = 0; t < CT; ++t) {
+    float sum[4] = {R.l[t], 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        y[e] = exp2_fast(S.s[t][w >> 1][8 * (w & 1) + e]);
+        sum[e & 3] += y[e];                 // (before they are rounded: the sum is an output)
+      }
+      W.p[t][w] = u32x4{T::cvt2(y[0], y[1]), T::cvt2(y[2], y[3]), T::cvt2(y[4], y[5]), T::cvt2(y[6], y[7])};
+    }
+    R.l[t] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  }
+}
+
+// The product with V, 32 columns x 16 keys an operand: transposing reads in
+// the order of keys that the weights have.  (Addresses in one sum: the
+// compiler follows a pointer to its buffer through few steps only, and waits
+// for the copies under way where it does not know the buffer.)
+template <int D>
+__device__ __forceinline__ u32x4 value_operand(const uint8_t* vt, int k, int d, int lane) {
+  // lane -> row (key) 4 hh + li / 4 of 16, 4 columns from 16 (gi & 1) + 4 (li % 4)
+  const int li = lane & 15, gi = lane >> 4, hh = lane >> 5;
+  const int row = 4 * hh + (li >> 2), vc = 2 * (gi & 1) + ((li & 3) >> 1), vb = 8 * (li & 1);
+  // (the pieces' permutation goes by the row's last bits, the same for all k)
+  const int at = row * (2 * D) + 16 * v_piece<D>(row, 4 * d + vc) + vb;
+  const u32x2 a = lds_tr(vt + (at + 16 * k * (2 * D))), b = lds_tr(vt + (at + (16 * k + 8) * (2 * D)));
+  return u32x4{a.x, a.y, b.x, b.y};
+}
+
+// In a masked tile a value that is not finite is kept out of the product
+// (0 * inf would spoil rows that do not see its key); says whether there are
+// any, for add_special.
+template <typename T>
+__device__ __forceinline__ uint32_t take_special(u32x4& v) {
+  uint32_t special = 0;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const uint32_t hi = (v[w] & (T::kExpOne << 16)) == (T::kExpOne << 16) ? 0xFFFF0000u : 0u;
+    const uint32_t lo = (v[w] & T::kExpOne) == T::kExpOne ? 0xFFFFu : 0u;
+    special |= hi | lo;
+    v[w] &= ~(hi | lo);
+  }
+  return special;
+}
+
+template <typename T, int D, int CT>
+__device__ __forceinline__ void add_special(Rows<T, D, CT>& R, const uint8_t* vt, int j0, int lane) {
+  const int hh = only_here(lane) >> 5;
+  for (int j = 0; j < kTile; ++j) {
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        s[t][i][e] = exp2_fast(__builtin_fmaf(s[t][i][e], c, -base));
-        R.l[t] += s[t][i][e];
-      }
+        const int cc = 32 * d + 8 * (e >> 2) + 4 * hh + (e & 3);
+        const uint32_t bits = *reinterpret_cast<const uint16_t*>(vt + j * (2 * D) + 16 * v_piece<D>(j, cc >> 3) + 2 * (cc & 7));
+        if ((bits & T::kExpOne) != T::kExpOne) continue;
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        u32x4 x;
-        x.x = T::cvt2(s[t][i][8 * w], s[t][i][8 * w + 1]);
-        x.y = T::cvt2(s[t][i][8 * w + 2], s[t][i][8 * w + 3]);
-        x.z = T::cvt2(s[t][i][8 * w + 4], s[t][i][8 * w + 5]);
-        x.w = T::cvt2(s[t][i][8 * w + 6], s[t][i][8 * w + 7]);
-        p[t][2 * i + w] = x;
+        for (int t = 0; t < CT; ++t)
+          if (j0 + j <= R.last[t]) R.o[t][d][e] += T::lo(bits);
       }
-    }
   }
-  // V: lane -> row (key) 4 hh + li / 4 of 16, 4 columns from 16 (gi & 1) + 4 (li % 4)
-  const int li = lane & 15, gi = lane >> 4;
-  const int row = 4 * hh + (li >> 2), vc = 2 * (gi & 1) + ((li & 3) >> 1), vb = 8 * (li & 1);
-  uint32_t special = 0;                     // exponents of all ones among V's values
+}
+
+template <bool Masked, typename T, int D, int CT>
+__device__ __forceinline__ void add_values(Rows<T, D, CT>& R, const Weights<CT>& W, const uint8_t* vt, int j0, int lane) {
+  uint32_t special = 0;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 0; k < 4; ++k)
 #pragma unroll
     for (int d = 0; d < D / 32; ++d) {
-      const int ra = 16 * k + row, rb = ra + 8;
-      const u32x2 a = lds_tr(vt + ra * (2 * D) + 16 * v_piece<D>(ra, 4 * d + vc) + vb);
-      const u32x2 b = lds_tr(vt + rb * (2 * D) + 16 * v_piece<D>(rb, 4 * d + vc) + vb);
-      u32x4 v = {a.x, a.y, b.x, b.y};
-      if (!all) {
-        // a value that is not finite is kept out of the product (0 * inf
-        // would spoil rows that do not see its key) and given below
+      u32x4 v = value_operand<D>(vt, k, d, lane);
+      if (Masked) special |= take_special<T>(v);
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const uint32_t hi = (v[w] & (T::kExpOne << 16)) == (T::kExpOne << 16) ? 0xFFFF0000u : 0u;
-          const uint32_t lo = (v[w] & T::kExpOne) == T::kExpOne ? 0xFFFFu : 0u;
-          special |= hi | lo;
-          v[w] &= ~(hi | lo);
-        }
-      }
-#pragma unroll
-      for (int t = 0; t < CT; ++t) R.o[t][d] = T::mma32(v, p[t][k], R.o[t][d]);
+      for (int t = 0; t < CT; ++t) R.o[t][d] = T::mma32(v, W.p[t][k], R.o[t][d]);
     }
-  }
-  if (!all && __any(special != 0)) {
-    for (int j = 0; j < kTile; ++j) {
-#pragma unroll
-      for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int cc = 32 * d + 8 * (e >> 2) + 4 * hh + (e & 3);
-          const uint32_t bits = *reinterpret_cast<const uint16_t*>(vt + j * (2 * D) + 16 * v_piece<D>(j, cc >> 3) + 2 * (cc & 7));
-          if ((bits & T::kExpOne) != T::kExpOne) continue;
-#pragma unroll
-          for (int t = 0; t < CT; ++t)
-            if (j0 + j <= R.last[t]) R.o[t][d][e] += T::lo(bits);
-        }
-    }
-  }
+  if (Masked && __any(special != 0)) add_special<T, D, CT>(R, vt, j0, lane);
+}
+
+template <int D>
+struct Keys {
+  Stage<D, false> k;
+  Stage<D, true> v;
+  int len;
+};
+
+// Step t: the scores of tile t and the weights of tile t-1 are there.  The
+// product with tile t-1's V goes with the exponents of tile t, the scores of
+// tile t+1 with the weights of tile t, so that the matrix core and the vector
+// unit work at the same time in one wave too.  When every wave is through
+// with step t-1, and the next K and the previous V have come, the copies of
+// the next but one K and of this tile's V start; they have a whole step's
+// time, and there is one barrier a step.  Tiles behind the last come as
+// zeros, so nothing here asks which is the last.
+template <bool First, bool Masked, typename T, int D, int CT>
+__device__ __forceinline__ void step(Rows<T, D, CT>& R, Scores<CT>& S, Weights<CT>& W, const Keys<D>& K, int t,
+                                     uint8_t* k_this, uint8_t* k_next, uint8_t* v_this, uint8_t* v_last, float c, int wave,
+                                     int lane) {
+  const int j0 = t * kTile;
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  K.k.start(j0 + 2 * kTile, K.len, k_this, wave);
+  K.v.start(j0, K.len, v_this, wave);
+  float mx[CT];
+  const bool raise = exponents<Masked, T, D, CT>(R, S, mx, j0, c, lane);
+  if (!First) add_values<Masked, T, D, CT>(R, W, v_last, j0 - kTile, lane);
+  if (raise) raise_maximum<T, D, CT>(R, S, mx);
+  weights<T, D, CT>(R, S, W);
+  scores<T, D, CT>(R, S, k_next, lane);
 }
 
 // Workgroup: 32*CT*kWaves rows of one sequence and key head (row r = token
@@ -227,38 +339,38 @@ __global__ __launch_bounds__(kThreads, CT == 1 && D <= 128 ? 2 : 1) void prefill
 #pragma unroll
       for (int e = 0; e < 16; ++e) R.o[t][d][e] = 0.f;
   }
-  // keys that all rows of the wave see, and that any does
-  const int w_end = min(w0 + 32 * CT, rows) - 1, wg_end = min(r0 + kRowsWg, rows) - 1;
-  const int w_all = a.causal ? min(shift + w0 / group, sk.n - 1) : sk.n - 1;
-  const int w_any = w0 >= rows ? -1 : a.causal ? shift + w_end / group : sk.n - 1;
-  const int wg_any = a.causal ? shift + wg_end / group : sk.n - 1;
-  const int n_tiles = wg_any < 0 || sk.n == 0 ? 0 : wg_any / kTile + 1;
+  // tiles that all of the workgroup's rows see whole, and that any row sees
+  const int last_row = min(r0 + kRowsWg, rows) - 1;
+  const int all = a.causal ? min(shift + r0 / group, sk.n - 1) : sk.n - 1;
+  const int any = a.causal ? shift + last_row / group : sk.n - 1;
+  const int n_whole = all < 0 ? 0 : (all + 1) / kTile, n_tiles = any < 0 ? 0 : any / kTile + 1;
 
-  const uint16_t* kbase = (const uint16_t*)a.k + (int64_t)sk.row0 * a.ks + (int64_t)hk * D;
-  const uint16_t* vbase = (const uint16_t*)a.v + (int64_t)sk.row0 * a.vs + (int64_t)hk * D;
   if (n_tiles > 0) {
-    stage<D, false>(kbase, a.ks, 0, sk.n, k0, wave, lane);
-    stage<D, true>(vbase, a.vs, 0, sk.n, v0, wave, lane);
-  }
-  for (int t = 0; t < n_tiles; t += 2) {
-    // this tile has come, for every wave; and every wave is done with the
-    // other buffer, which the next tile may now fill
+    Keys<D> K;
+    K.len = sk.n;
+    K.k.init((const uint16_t*)a.k + (int64_t)sk.row0 * a.ks + (int64_t)hk * D, a.ks, wave, lane);
+    K.v.init((const uint16_t*)a.v + (int64_t)sk.row0 * a.vs + (int64_t)hk * D, a.vs, wave, lane);
+    K.k.start(0, sk.n, k0, wave);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    if (t + 1 < n_tiles) {
-      stage<D, false>(kbase, a.ks, (t + 1) * kTile, sk.n, k1, wave, lane);
-      stage<D, true>(vbase, a.vs, (t + 1) * kTile, sk.n, v1, wave, lane);
+    K.k.start(kTile, sk.n, k1, wave);
+    Scores<CT> S;
+    Weights<CT> W;
+    scores<T, D, CT>(R, S, k0, lane);
+    step<true, true, T, D, CT>(R, S, W, K, 0, k0, k1, v0, v1, a.c, wave, lane);
+    int t = 1;
+    for (; t + 2 <= n_whole; t += 2) {
+      step<false, false, T, D, CT>(R, S, W, K, t, k1, k0, v1, v0, a.c, wave, lane);
+      step<false, false, T, D, CT>(R, S, W, K, t + 1, k0, k1, v0, v1, a.c, wave, lane);
     }
-    if (t * kTile <= w_any) tile_step<T, D, CT>(R, k0, v0, t * kTile, t * kTile + kTile - 1 <= w_all, a.c, lane);
-    if (t + 1 >= n_tiles) break;
+    for (; t < n_tiles; t += 2) {
+      step<false, true, T, D, CT>(R, S, W, K, t, k1, k0, v1, v0, a.c, wave, lane);
+      if (t + 1 >= n_tiles) break;
+      step<false, true, T, D, CT>(R, S, W, K, t + 1, k0, k1, v0, v1, a.c, wave, lane);
+    }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    if (t + 2 < n_tiles) {
-      stage<D, false>(kbase, a.ks, (t + 2) * kTile, sk.n, k0, wave, lane);
-      stage<D, true>(vbase, a.vs, (t + 2) * kTile, sk.n, v0, wave, lane);
-    }
-    if ((t + 1) * kTile <= w_any)
-      tile_step<T, D, CT>(R, k1, v1, (t + 1) * kTile, (t + 1) * kTile + kTile - 1 <= w_all, a.c, lane);
+    add_values<true, T, D, CT>(R, W, n_tiles & 1 ? v0 : v1, (n_tiles - 1) * kTile, lane);
   }
 #pragma unroll
   for (int t = 0; t < CT; ++t) {

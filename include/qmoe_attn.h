@@ -21,8 +21,8 @@
  *
  * Row tensors (q, k, v, outputs): [rows][heads][head_dim] of one 16-bit type
  * (MOE_DT_BF16 or MOE_DT_F16), a row's heads back to back, rows `stride`
- * elements apart (a multiple of 8, at least heads * head_dim), so q, k and v
- * may be parts of one projection's output.  head_dim is 64, 128 or 256;
+ * elements apart (a multiple of 8, at least heads * head_dim, at most 2^24), so
+ * q, k and v may be parts of one projection's output.  head_dim is 64, 128 or 256;
  * q_heads is a multiple of kv_heads, query head h reads key head
  * h / (q_heads / kv_heads).
  */
