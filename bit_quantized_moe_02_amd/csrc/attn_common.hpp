@@ -43,6 +43,11 @@ struct Bf16 {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
   }
   static constexpr uint32_t kExpOne = 0x7F80u;
+  // acc + lo^2 + hi^2
+  static __device__ __forceinline__ float square2(uint32_t w, float acc) {
+    const bf16x2 v = __builtin_bit_cast(bf16x2, w);
+    return __builtin_amdgcn_fdot2_f32_bf16(v, v, acc, false);
+  }
 };
 
 struct F16 {
@@ -64,6 +69,10 @@ struct F16 {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
   }
   static constexpr uint32_t kExpOne = 0x7C00u;
+  static __device__ __forceinline__ float square2(uint32_t w, float acc) {
+    const f16x2 v = __builtin_bit_cast(f16x2, w);
+    return __builtin_amdgcn_fdot2(v, v, acc, false);
+  }
 };
 
 // Eight codes (two words) times a power of two: an MFMA operand.

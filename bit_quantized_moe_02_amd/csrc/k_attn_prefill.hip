@@ -207,52 +207,69 @@ __device__ __forceinline__ u32x4 value_operand(const uint8_t* vt, int k, int d, 
 }
 
 // In a masked tile a value that is not finite is kept out of the product
-// (0 * inf would spoil rows that do not see its key); says whether there are
-// any, for add_special.
+// (0 * inf would spoil rows that do not see its key) and given to the rows
+// that see it at the end (add_special).
 template <typename T>
-__device__ __forceinline__ uint32_t take_special(u32x4& v) {
-  uint32_t special = 0;
+__device__ __forceinline__ void take_special(u32x4& v) {
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
     const uint32_t hi = (v[w] & (T::kExpOne << 16)) == (T::kExpOne << 16) ? 0xFFFF0000u : 0u;
     const uint32_t lo = (v[w] & T::kExpOne) == T::kExpOne ? 0xFFFFu : 0u;
-    special |= hi | lo;
     v[w] &= ~(hi | lo);
+  }
+}
+
+// Says whether it met such values (Masked; a sum of squares finds them, and
+// very large ones).
+template <bool Masked, typename T, int D, int CT>
+__device__ __forceinline__ bool add_values(Rows<T, D, CT>& R, const Weights<CT>& W, const uint8_t* vt, int lane) {
+  bool special = false;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    u32x4 v[D / 32];
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d) v[d] = value_operand<D>(vt, k, d, lane);
+    if (Masked) {
+      float sq[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) sq[w] = T::square2(v[d][w], sq[w]);
+      if (__any(!((sq[0] + sq[1]) + (sq[2] + sq[3]) < __builtin_inff()))) {
+        special = true;
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d) take_special<T>(v[d]);
+      }
+    }
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+      for (int t = 0; t < CT; ++t) R.o[t][d] = T::mma32(v[d], W.p[t][k], R.o[t][d]);
   }
   return special;
 }
 
+// Keys j0..j1-1 once more, for their values that are not finite.
 template <typename T, int D, int CT>
-__device__ __forceinline__ void add_special(Rows<T, D, CT>& R, const uint8_t* vt, int j0, int lane) {
-  const int hh = only_here(lane) >> 5;
-  for (int j = 0; j < kTile; ++j) {
+__device__ void add_special(Rows<T, D, CT>& R, const uint8_t* v, int64_t row_bytes, int j0, int j1, int lane) {
+  const int hh = lane >> 5;
+  for (int j = j0; j < j1; ++j) {
+    const uint8_t* row = v + j * row_bytes + 8 * hh;
 #pragma unroll
     for (int d = 0; d < D / 32; ++d)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int cc = 32 * d + 8 * (e >> 2) + 4 * hh + (e & 3);
-        const uint32_t bits = *reinterpret_cast<const uint16_t*>(vt + j * (2 * D) + 16 * v_piece<D>(j, cc >> 3) + 2 * (cc & 7));
-        if ((bits & T::kExpOne) != T::kExpOne) continue;
+      for (int e = 0; e < 16; e += 4) {
+        const u32x2 w = *reinterpret_cast<const u32x2*>(row + 64 * d + 4 * e);
 #pragma unroll
-        for (int t = 0; t < CT; ++t)
-          if (j0 + j <= R.last[t]) R.o[t][d][e] += T::lo(bits);
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t bits = (i & 2 ? w.y : w.x) >> (16 * (i & 1)) & 0xFFFFu;
+          const float x = (bits & T::kExpOne) == T::kExpOne ? T::lo(bits) : 0.f;
+#pragma unroll
+          for (int t = 0; t < CT; ++t)
+            if (j <= R.last[t]) R.o[t][d][e + i] += x;
+        }
       }
   }
-}
-
-template <bool Masked, typename T, int D, int CT>
-__device__ __forceinline__ void add_values(Rows<T, D, CT>& R, const Weights<CT>& W, const uint8_t* vt, int j0, int lane) {
-  uint32_t special = 0;
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-#pragma unroll
-    for (int d = 0; d < D / 32; ++d) {
-      u32x4 v = value_operand<D>(vt, k, d, lane);
-      if (Masked) special |= take_special<T>(v);
-#pragma unroll
-      for (int t = 0; t < CT; ++t) R.o[t][d] = T::mma32(v, W.p[t][k], R.o[t][d]);
-    }
-  if (Masked && __any(special != 0)) add_special<T, D, CT>(R, vt, j0, lane);
 }
 
 template <int D>
@@ -271,20 +288,47 @@ struct Keys {
 // time, and there is one barrier a step.  Tiles behind the last come as
 // zeros, so nothing here asks which is the last.
 template <bool First, bool Masked, typename T, int D, int CT>
-__device__ __forceinline__ void step(Rows<T, D, CT>& R, Scores<CT>& S, Weights<CT>& W, const Keys<D>& K, int t,
+__device__ __forceinline__ bool step(Rows<T, D, CT>& R, Scores<CT>& S, Weights<CT>& W, const Keys<D>& K, int t,
                                      uint8_t* k_this, uint8_t* k_next, uint8_t* v_this, uint8_t* v_last, float c, int wave,
                                      int lane) {
   const int j0 = t * kTile;
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
   K.k.start(j0 + 2 * kTile, K.len, k_this, wave);
-  K.v.start(j0, K.len, v_this, wave);
+  if (!First) K.v.start(j0, K.len, v_this, wave);
   float mx[CT];
   const bool raise = exponents<Masked, T, D, CT>(R, S, mx, j0, c, lane);
-  if (!First) add_values<Masked, T, D, CT>(R, W, v_last, j0 - kTile, lane);
+  bool special = false;
+  if (!First) special = add_values<Masked, T, D, CT>(R, W, v_last, lane);
+  if (!First && !Masked) {
+    __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {       // block A: D/8 products, 32 multiplications, 20 maxima
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, CT, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, (D == 64 ? 7 : 4) * CT, 0);
+    }
+  }
   if (raise) raise_maximum<T, D, CT>(R, S, mx);
   weights<T, D, CT>(R, S, W);
   scores<T, D, CT>(R, S, k_next, lane);
+  // (the weights are made here, among the products, not where they are used)
+#pragma unroll
+  for (int u = 0; u < CT; ++u)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) asm volatile("" : "+v"(W.p[u][w]));
+#pragma unroll
+  for (int u = 0; u < CT; ++u) asm volatile("" : "+v"(R.l[u]));
+  if (!Masked) {
+    __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {       // block B: D/8 products, 32 exponentials, 32 additions, 16 conversions
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, CT, 0);
+      __builtin_amdgcn_sched_group_barrier(0x402, (D == 64 ? 10 : 5) * CT, 0);
+    }
+  }
+  return special;
 }
 
 // Workgroup: 32*CT*kWaves rows of one sequence and key head (row r = token
@@ -298,19 +342,22 @@ __global__ __launch_bounds__(kThreads, CT == 1 && D <= 128 ? 2 : 1) void prefill
   __shared__ __attribute__((aligned(1024))) uint8_t k0[kBytes], v0[kBytes], k1[kBytes], v1[kBytes];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int pairs = a.B * a.Hk;
-  // the longest rows first; workgroups of one key head on one XCD (workgroups
-  // go round robin over the 8), where their keys stay in its L2
-  int pair, qt;
-  if (pairs % 8 == 0) {
-    const int x = blockIdx.x & 7, i = blockIdx.x >> 3;
-    pair = x + 8 * (i / tiles);
-    qt = tiles - 1 - i % tiles;
+  // Workgroups go round robin over the 8 XCDs.  A key head's workgroups stay
+  // on one of them, where its keys stay in the L2 (with fewer than 8 key heads
+  // on 8/Hk of them, where 8/Hk is whole), so that each XCD has the
+  // same share of every sequence.  The last rows, which see the most keys,
+  // come first, those of all sequences.
+  const int x = blockIdx.x & 7, b = (blockIdx.x >> 3) % a.B, i = (blockIdx.x >> 3) / a.B;
+  int hk, qt;
+  if (a.Hk % 8 == 0) {
+    hk = x + 8 * (i % (a.Hk / 8));
+    qt = tiles - 1 - i / (a.Hk / 8);
   } else {
-    pair = blockIdx.x % pairs;
-    qt = tiles - 1 - blockIdx.x / pairs;
+    const int at = 8 * i + x;
+    hk = at % a.Hk;
+    qt = tiles - 1 - at / a.Hk;
   }
-  const int b = pair / a.Hk, hk = pair % a.Hk;
+  if (qt < 0) return;                       // the whole workgroup
   const int group = a.Hq / a.Hk;
   const Seq sq = seq_rows(a.cu_q, a.per_q, a.Tq, b), sk = seq_rows(a.cu_k, a.per_k, a.Tk, b);
   const int rows = sq.n * group, r0 = qt * kRowsWg;
@@ -351,9 +398,10 @@ __global__ __launch_bounds__(kThreads, CT == 1 && D <= 128 ? 2 : 1) void prefill
     K.k.init((const uint16_t*)a.k + (int64_t)sk.row0 * a.ks + (int64_t)hk * D, a.ks, wave, lane);
     K.v.init((const uint16_t*)a.v + (int64_t)sk.row0 * a.vs + (int64_t)hk * D, a.vs, wave, lane);
     K.k.start(0, sk.n, k0, wave);
+    K.k.start(kTile, sk.n, k1, wave);
+    K.v.start(0, sk.n, v0, wave);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    K.k.start(kTile, sk.n, k1, wave);
     Scores<CT> S;
     Weights<CT> W;
     scores<T, D, CT>(R, S, k0, lane);
@@ -363,14 +411,18 @@ __global__ __launch_bounds__(kThreads, CT == 1 && D <= 128 ? 2 : 1) void prefill
       step<false, false, T, D, CT>(R, S, W, K, t, k1, k0, v1, v0, a.c, wave, lane);
       step<false, false, T, D, CT>(R, S, W, K, t + 1, k0, k1, v0, v1, a.c, wave, lane);
     }
+    const int masked_from = t - 1;          // (its V is still to come)
+    bool special = false;
     for (; t < n_tiles; t += 2) {
-      step<false, true, T, D, CT>(R, S, W, K, t, k1, k0, v1, v0, a.c, wave, lane);
+      special |= step<false, true, T, D, CT>(R, S, W, K, t, k1, k0, v1, v0, a.c, wave, lane);
       if (t + 1 >= n_tiles) break;
-      step<false, true, T, D, CT>(R, S, W, K, t + 1, k0, k1, v0, v1, a.c, wave, lane);
+      special |= step<false, true, T, D, CT>(R, S, W, K, t + 1, k0, k1, v0, v1, a.c, wave, lane);
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    add_values<true, T, D, CT>(R, W, n_tiles & 1 ? v0 : v1, (n_tiles - 1) * kTile, lane);
+    special |= add_values<true, T, D, CT>(R, W, n_tiles & 1 ? v0 : v1, lane);
+    if (special)
+      add_special<T, D, CT>(R, K.v.base, K.v.row_bytes, masked_from * kTile, min(n_tiles * kTile, sk.n), lane);
   }
 #pragma unroll
   for (int t = 0; t < CT; ++t) {
@@ -397,8 +449,8 @@ template <typename T, int D, int CT>
 hipError_t go(const PrefillArgs& a, hipStream_t s) {
   const int64_t rows = (int64_t)a.max_q * (a.Hq / a.Hk);
   const int tiles = (int)((rows + 32 * CT * kWaves - 1) / (32 * CT * kWaves));
-  hipLaunchKernelGGL((prefill_kernel<T, D, CT>), dim3((unsigned)((int64_t)tiles * a.B * a.Hk)), dim3(kThreads), 0, s,
-                     a, tiles);
+  const int64_t per_seq = ((int64_t)tiles * a.Hk + 7) / 8 * 8;   // whole rounds of the XCDs
+  hipLaunchKernelGGL((prefill_kernel<T, D, CT>), dim3((unsigned)(per_seq * a.B)), dim3(kThreads), 0, s, a, tiles);
   return hipGetLastError();
 }
 
