@@ -10,8 +10,9 @@ using namespace qmoe_dev;
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / 64;
+constexpr int kWaves = 4;                   // of a workgroup that takes a range
+constexpr int kShortWaves = 8;              // of one that takes a whole short context
+constexpr int kThreads = 256;               // of the join
 constexpr int kStep = 32;                   // positions a wave takes at once: two blocks
 
 // Shares.  The contexts of all sequences, in steps of 32 positions one after
@@ -144,13 +145,18 @@ constexpr int occupancy(int dim, int nr) { return nr == 1 && dim <= 128 ? 3 : nr
 // layout gives K and V codes in operand order by 16-byte loads.  HBM bounds
 // it, so a wave's loads never stop: the next step's K codes are asked for as
 // soon as this step's are in the first product, its V codes after the second.
-template <typename T, int D, int NR>
-__global__ __launch_bounds__(kThreads, occupancy(D, NR)) void decode_kernel(DecodeArgs a) {
+//
+// Short: a workgroup of 8 waves takes a whole sequence, so that there is no
+// join to launch (777 positions, 8 key heads: 6 us, parts and join 8.6 us and
+// a second launch).
+template <typename T, int D, int NR, bool Short>
+__global__ __launch_bounds__(64 * (Short ? kShortWaves : kWaves), Short ? 1 : occupancy(D, NR)) void decode_kernel(DecodeArgs a) {
+  constexpr int NW = Short ? kShortWaves : kWaves;
   constexpr int kKb = D / 32;               // k-blocks of a score
   constexpr int kDt = D / 16;               // 16-column tiles of the output
   constexpr int kP = D / 64;                // pieces of a block's K, of its V
-  __shared__ float so[kWaves][16][D + 4];
-  __shared__ float sm[kWaves][16], sl[kWaves][16];
+  __shared__ float so[NW][16][D + 4];
+  __shared__ float sm[NW][16], sl[NW][16];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n16 = lane & 15, g = lane >> 4;
@@ -158,24 +164,32 @@ __global__ __launch_bounds__(kThreads, occupancy(D, NR)) void decode_kernel(Deco
   const int group = a.Hq / a.kv.Hk;
   const int r0 = blockIdx.z * 16 * NR;
 
-  const LaneSeq head = lane_seq(a.kv, 0, lane);
-  const Cut cut = cut_of(a.kv, a.split.n, head, lane);
-  int pos = worker * cut.per;
-  const int end = min(pos + cut.per, cut.total);
-  if (pos >= end) return;                   // the whole workgroup
-  int first;
-  int b = seq_at(a.kv, pos, head, lane, &first);
+  LaneSeq head{};
+  Cut cut{};
+  int pos, end, first, b;
+  if (Short) {
+    b = worker;
+    first = pos = 0;
+    end = 0x7FFFFFFF;
+  } else {
+    head = lane_seq(a.kv, 0, lane);
+    cut = cut_of(a.kv, a.split.n, head, lane);
+    pos = worker * cut.per;
+    end = min(pos + cut.per, cut.total);
+    if (pos >= end) return;                 // the whole workgroup
+    b = seq_at(a.kv, pos, head, lane, &first);
+  }
 
   for (bool again = false; pos < end && b < a.kv.B; ++b) {
-    const Seq s = uniform_seq(a.kv, head, b);
+    const Seq s = Short ? seq_of(a.kv, b) : uniform_seq(a.kv, head, b);
     const int steps = (s.len + kStep - 1) / kStep, cost = cost_of(s);
     const int s0 = pos - first, s1 = min(min(end - first, cost), steps);
-    const bool whole = pos == first && first + cost <= end;
+    const bool whole = Short || (pos == first && first + cost <= end);
     // the range with a sequence's first step tells the join where its parts lie
-    if (a.split.n > 1 && pos == first && cost > 0 && hk == 0 && blockIdx.z == 0 && threadIdx.x == 0)
+    if (!Short && a.split.n > 1 && pos == first && cost > 0 && hk == 0 && blockIdx.z == 0 && threadIdx.x == 0)
       a.split.where[b] = make_int2(worker, (first + cost - 1) / cut.per - worker + 1);
     first += cost;
-    pos = min(first, end);
+    pos = Short ? end : min(first, end);
     const int rows = s.n * group;
     if (r0 >= rows) continue;               // (the same for the whole workgroup)
 
@@ -217,7 +231,7 @@ __global__ __launch_bounds__(kThreads, occupancy(D, NR)) void decode_kernel(Deco
 #pragma unroll
       for (int i = 0; i < 2; ++i) first_page[i] = page_at(a.kv, s.len, b, 2 * st + i);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) page[i] = page_at(a.kv, s.len, b, 2 * (st + kWaves) + i);
+      for (int i = 0; i < 2; ++i) page[i] = page_at(a.kv, s.len, b, 2 * (st + NW) + i);
 #pragma unroll
       for (int i = 0; i < 2; ++i) cur[i] = find_block(a.kv, s.len, hk, 2 * st + i, first_page[i]);
 #pragma unroll
@@ -229,7 +243,7 @@ __global__ __launch_bounds__(kThreads, occupancy(D, NR)) void decode_kernel(Deco
 #pragma unroll
         for (int k = 0; k < kP; ++k) vr[i][k] = load_codes(p + 16 * D + 1024 * k);
       }
-      for (; st < s1; st += kWaves) {
+      for (; st < s1; st += NW) {
         // scores: position 32 st + 16 i + 4 g + j in sc[t][i][j]
         f32x4 sc[NR][2];
         float sv[2];
@@ -253,17 +267,17 @@ __global__ __launch_bounds__(kThreads, occupancy(D, NR)) void decode_kernel(Deco
         }
         // the next step's K (in the last step: this one's again, so that the
         // number of loads under way is the same on every path)
-        const bool more = st + kWaves < s1;
+        const bool more = st + NW < s1;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          if (more) cur[i] = find_block(a.kv, s.len, hk, 2 * (st + kWaves) + i, page[i]);
+          if (more) cur[i] = find_block(a.kv, s.len, hk, 2 * (st + NW) + i, page[i]);
           const uint8_t* p = a.kv.codes + cur[i].at * (32 * D) + 16 * lane;
           sc2[i] = *reinterpret_cast<const float2*>(a.kv.scales + 2 * cur[i].at);
 #pragma unroll
           for (int k = 0; k < kP; ++k) kr[i][k] = load_codes(p + 1024 * k);
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) page[i] = page_at(a.kv, s.len, b, 2 * (st + 2 * kWaves) + i);
+        for (int i = 0; i < 2; ++i) page[i] = page_at(a.kv, s.len, b, 2 * (st + 2 * NW) + i);
         const bool all = valid[0] == 16 && valid[1] == 16 && kStep * st + kStep - 1 <= first_last;
         bool bad_v = false;                 // a code for not a number among V's valid tokens
         if (!all) {
@@ -388,18 +402,18 @@ __global__ __launch_bounds__(kThreads, occupancy(D, NR)) void decode_kernel(Deco
 #pragma unroll
       for (int d = 0; d < kDt; ++d) *reinterpret_cast<f32x4*>(&so[wave][n16][16 * d + 4 * g]) = o[t][d];
       __syncthreads();
-      for (int i = threadIdx.x; i < 16 * (D / 4); i += kThreads) {
+      for (int i = threadIdx.x; i < 16 * (D / 4); i += 64 * NW) {
         const int row = i / (D / 4), ch = i % (D / 4);
         const int r = r0 + 16 * t + row;
         if (r >= rows) continue;
         float mx = kMinusInf;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) mx = fmaxf(mx, sm[w][row]);
+        for (int w = 0; w < NW; ++w) mx = fmaxf(mx, sm[w][row]);
         const float base = mx == kMinusInf ? 0.f : mx;
         float sum = 0.f;
         f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
+        for (int w = 0; w < NW; ++w) {
           // (a wave that saw nothing has maximum -inf and zeros)
           const float e = exp2_fast(sm[w][row] - base);
           sum += e * sl[w][row];
@@ -481,9 +495,23 @@ int row_tiles(const KvArgs& kv, int Hq) {
   return rows <= 16 ? 1 : rows <= 32 || kv.D > 128 ? 2 : 4;
 }
 
+// Whether contexts (by the page table) are taken whole: four rounds of a
+// workgroup's waves; the join would cost more than the rounds it saves.  The
+// widest row tiles do not fit the registers of 8 waves.
+bool is_short(const KvArgs& kv, int nr) {
+  return kv.max_len <= 4 * kShortWaves * kStep && nr * kv.D <= 256 && kv.B <= 65535;
+}
+
 template <typename T, int D>
-void (*pick(int nr))(DecodeArgs) {
-  return nr == 1 ? decode_kernel<T, D, 1> : nr == 2 ? decode_kernel<T, D, 2> : decode_kernel<T, D, (D > 128 ? 2 : 4)>;
+void (*pick(int nr, bool shrt))(DecodeArgs) {
+  if (nr == 1) return shrt ? decode_kernel<T, D, 1, true> : decode_kernel<T, D, 1, false>;
+  if (nr == 2) return shrt ? decode_kernel<T, D, (D > 128 ? 1 : 2), true> : decode_kernel<T, D, 2, false>;
+  return shrt ? decode_kernel<T, D, (D > 64 ? 1 : 4), true> : decode_kernel<T, D, (D > 128 ? 2 : 4), false>;
+}
+
+template <typename T>
+void (*pick_dim(int dim, int nr, bool shrt))(DecodeArgs) {
+  return dim == 64 ? pick<T, 64>(nr, shrt) : dim == 128 ? pick<T, 128>(nr, shrt) : pick<T, 256>(nr, shrt);
 }
 
 }  // namespace
@@ -492,6 +520,7 @@ namespace qmoe {
 
 int attn_decode_workers(const KvArgs& kv, int Hq, int cus) {
   const int nr = row_tiles(kv, Hq);
+  if (is_short(kv, nr)) return 1;
   const int64_t wgs = (int64_t)kv.Hk * ((rows_of(kv, Hq) + 16 * nr - 1) / (16 * nr));
   const int64_t most = kv.B * (((int64_t)kv.max_len + kStep * kWaves - 1) / (kStep * kWaves));
   int64_t n = (int64_t)occupancy(kv.D, nr) * cus / wgs;
@@ -501,21 +530,17 @@ int attn_decode_workers(const KvArgs& kv, int Hq, int cus) {
 
 hipError_t launch_attn_decode(const DecodeArgs& a, int dtype, hipStream_t s) {
   const int nr = row_tiles(a.kv, a.Hq);
-  void (*fn)(DecodeArgs) = nullptr;
+  const bool bf = dtype == 0, shrt = is_short(a.kv, nr);
+  auto fn = bf ? pick_dim<Bf16>(a.kv.D, nr, shrt) : pick_dim<F16>(a.kv.D, nr, shrt);
   void (*join)(DecodeArgs) = nullptr;
-  const bool bf = dtype == 0;
-  switch (a.kv.D) {
-    case 64: fn = bf ? pick<Bf16, 64>(nr) : pick<F16, 64>(nr); break;
-    case 128: fn = bf ? pick<Bf16, 128>(nr) : pick<F16, 128>(nr); break;
-    default: fn = bf ? pick<Bf16, 256>(nr) : pick<F16, 256>(nr); break;
-  }
   switch (a.kv.D) {
     case 64: join = bf ? join_kernel<Bf16, 64> : join_kernel<F16, 64>; break;
     case 128: join = bf ? join_kernel<Bf16, 128> : join_kernel<F16, 128>; break;
     default: join = bf ? join_kernel<Bf16, 256> : join_kernel<F16, 256>; break;
   }
-  hipLaunchKernelGGL(fn, dim3((unsigned)a.kv.Hk, (unsigned)a.split.n, (unsigned)((rows_of(a.kv, a.Hq) + 16 * nr - 1) / (16 * nr))),
-                     dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL(fn, dim3((unsigned)a.kv.Hk, (unsigned)(shrt ? a.kv.B : a.split.n),
+                              (unsigned)((rows_of(a.kv, a.Hq) + 16 * nr - 1) / (16 * nr))),
+                     dim3(64 * (shrt ? kShortWaves : kWaves)), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.split.n == 1) return e;
   hipLaunchKernelGGL(join, dim3((unsigned)(a.kv.B * (int64_t)a.kv.max_new), (unsigned)a.Hq), dim3(kThreads), 0, s, a);

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -474,11 +475,12 @@ class ExpertCache:
 
 
 _DTYPE = {torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16}
+_PACKED = struct.Struct("@4i2P3i0P")        # struct moe_packed
+assert _PACKED.size == ctypes.sizeof(MoePacked)
 
 
-def _device():
-    """Index of the current device, where the library launches."""
-    return torch._C._cuda_getDevice()
+# index of the current device, where the library launches
+_device = torch._C._cuda_getDevice
 
 
 def _here(t, name, dev):
@@ -488,32 +490,41 @@ def _here(t, name, dev):
 
 def _rows(t, name, heads, dim, n, dtype, dev):
     """(address, row stride) of a row tensor [>= n, heads, dim] of `dtype` on device `dev`, its heads back to back."""
+    try:
+        (r, h, d), stride = t.shape, t.stride()
+        if (h == heads and d == dim and r >= n and t.dtype is dtype and t.get_device() == dev and stride[2] == 1 and
+                (stride[1] == dim or h == 1)):
+            return t.data_ptr(), stride[0] if r > 1 else h * d
+    except (AttributeError, ValueError):
+        pass
+    # what of it was wrong
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 3 or shape[1] != heads or shape[2] != dim or shape[0] < n:
-        raise ValueError(f"{name} has shape {tuple(shape)}; the call needs [{n}, {heads}, {dim}]")
-    if stride[2] != 1 or (stride[1] != dim and heads > 1):
-        raise ValueError(f"{name}'s heads must lie back to back")
-    if t.get_device() != dev:
-        _here(t, name, dev)
-    return t.data_ptr(), stride[0] if shape[0] > 1 else heads * dim
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or t.shape[0] < n:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; the call needs [{n}, {heads}, {dim}]")
+    _here(t, name, dev)
+    raise ValueError(f"{name}'s heads must lie back to back")
 
 
 def _type(t, name):
     """Library code of a row tensor's type."""
-    if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPE or not t.is_cuda:
+    code = _DTYPE.get(getattr(t, "dtype", None))
+    if code is None or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor of torch.bfloat16 or torch.float16")
-    return _DTYPE[t.dtype]
+    return code
 
 
-def _vec(t, name, dtype, n, dev, optional=False):
-    p = _dev(t, name, dtype, n, optional)
-    if p is not None:
-        _here(t, name, dev)
-    return p
+def _vec(t, name, dtype, n, dev):
+    """Address of a contiguous tensor of at least n elements of `dtype` on device `dev`."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.numel() >= n:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev(t, name, dtype, n)                 # raises, unless only the device is wrong
+    _here(t, name, dev)
 
 
 def _stream_on(stream, dev):
@@ -656,7 +667,7 @@ def moe_attn_decode(cache, batch, q, out, ws, scale, lse=None, stream=None):
     qp, qs = _rows(q, "q", hq, D, n, dt, dev)
     op, os_ = _rows(out, "out", hq, D, n, dt, dev)
     rc = lib.moe_attn_decode(cache.ref, batch.ref, code, qp, qs, hq, scale, op, os_,
-                             _vec(lse, "lse", torch.float32, n * hq, dev, optional=True),
+                             None if lse is None else _vec(lse, "lse", torch.float32, n * hq, dev),
                              _vec(ws, "ws", torch.uint8, 0, dev), ws.numel(), _stream_on(stream, dev))
     if rc:
         _check(rc)
@@ -671,8 +682,7 @@ def moe_attn_prefill_workspace_bytes(rows_q: int, batch: int, max_q: int, rows_k
 
 def moe_attn_prefill(q, k, v, cu_q, cu_k, max_q, out, ws, scale, causal=True, lse=None, stream=None):
     """q, out [rows_q, q_heads, head_dim]; k, v [rows_k, kv_heads, head_dim]; cu_q, cu_k int32 [batch+1]."""
-    code, dt = _type(q, "q"), q.dtype
-    dev = _device()
+    code, dt, dev = _type(q, "q"), q.dtype, _device()
     if q.dim() != 3 or _type(k, "k") != code or k.dim() != 3:
         raise ValueError("q and k must be [rows, heads, head_dim] of one type")
     nq, hq, D = q.shape
@@ -683,9 +693,9 @@ def moe_attn_prefill(q, k, v, cu_q, cu_k, max_q, out, ws, scale, causal=True, ls
     op, os_ = _rows(out, "out", hq, D, nq, dt, dev)
     cq = _vec(cu_q, "cu_q", torch.int32, 2, dev)
     batch = cu_q.numel() - 1
-    p = MoePacked(batch, nq, nk, max_q, cq, _vec(cu_k, "cu_k", torch.int32, batch + 1, dev), hq, hk, D)
-    rc = lib.moe_attn_prefill(ctypes.byref(p), code, qp, qs, kp, ks, vp, vs, scale, 1 if causal else 0, op, os_,
-                              _vec(lse, "lse", torch.float32, nq * hq, dev, optional=True),
+    p = _PACKED.pack(batch, nq, nk, max_q, cq, _vec(cu_k, "cu_k", torch.int32, batch + 1, dev), hq, hk, D)
+    rc = lib.moe_attn_prefill(p, code, qp, qs, kp, ks, vp, vs, scale, 1 if causal else 0, op, os_,
+                              None if lse is None else _vec(lse, "lse", torch.float32, nq * hq, dev),
                               _vec(ws, "ws", torch.uint8, 0, dev), ws.numel(), _stream_on(stream, dev))
     if rc:
         _check(rc)
