@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "attn_common.hpp"
 
 using namespace qmoe;
@@ -49,9 +51,17 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float r) {
   return code4(x[0] * r, x[1] * r, y[0] * r, y[1] * r);
 }
 
+// Maximum over a wave: within 4 lanes, 8, 16, then over its rows of 16.
 __device__ __forceinline__ float wave_max(float x) {
-  for (int o = 32; o >= 1; o >>= 1) x = fmaxf(x, __shfl_xor(x, o));
-  return x;
+  const auto step = [](float v, auto ctrl) {
+    const int w = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), decltype(ctrl)::value, 0xF, 0xF, true);
+    return fmaxf(v, __builtin_bit_cast(float, w));
+  };
+  x = step(x, std::integral_constant<int, 0xB1>());    // quad_perm 1 0 3 2
+  x = step(x, std::integral_constant<int, 0x4E>());    // quad_perm 2 3 0 1
+  x = step(x, std::integral_constant<int, 0x141>());   // row_half_mirror
+  x = step(x, std::integral_constant<int, 0x140>());   // row_mirror
+  return max_rows4(x);
 }
 
 template <typename T>
@@ -69,20 +79,31 @@ __device__ __forceinline__ u32x4 pack8(const float* x) {
 
 __device__ __forceinline__ u32x4 ldg16(const uint16_t* p) { return *reinterpret_cast<const u32x4*>(p); }
 
+// Scales and codes of a block of one head that an append has to know.
+__device__ __forceinline__ int64_t block_in(const KvArgs& a, int page, int blk, int hk) {
+  return ((((int64_t)page * a.Hk + hk) << a.lb) + (blk & ((1 << a.lb) - 1)));
+}
+
 // One workgroup takes the tokens that one block of one sequence gets, and a
 // share (blockIdx.y) of the heads.  Its threads compute the angles of those
 // tokens once into LDS (64-bit reduction, then 32-bit sine and cosine); then
 // each wave takes one job at a time: a q head (turn), a K head (turn, scale,
 // codes) or a V head (scale, codes).  A wave holds 16 tokens of one head in
-// registers, so each input is read once and each output written once.
+// registers, so each input is read once and each output written once.  The
+// first job's loads are asked for before the angles: with one token it is
+// latency that counts.  (With many, asking for each next job's loads while one
+// is worked on costs registers and 4% at 2048 tokens of 32 + 8 + 8 heads.)
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int nb) {
   constexpr int kLanes = D / 16;            // lanes of a row of q or k, 16 columns each
   constexpr int kRows = 64 / kLanes;        // rows a wave takes at once
   constexpr int kSteps = 16 / kRows;
+  constexpr int kCh = D / 8;                // V: a lane takes 8 columns of 4 tokens, the words of its columns
+  constexpr int kSt = kCh * 4 > 64 ? kCh * 4 / 64 : 1;
+  constexpr int kRaw = 2 * kSteps > 4 * kSt ? 2 * kSteps : 4 * kSt;
   __shared__ __attribute__((aligned(16))) float2 turn[16][D / 2 + 1];
 
-  const int b = blockIdx.x / nb, ib = blockIdx.x % nb;
+  const int b = nb == 1 ? blockIdx.x : blockIdx.x / nb, ib = nb == 1 ? 0 : blockIdx.x % nb;
   const Seq s = seq_of(a.kv, b);
   const int pos0 = s.len - s.n;             // may be negative
   const int blk = (pos0 >> 4) + ib;
@@ -91,32 +112,76 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int nb) 
   const int f = lo - blk * 16, e = hi - blk * 16;      // slots [f, e) are new
   const int64_t row_of_slot0 = (int64_t)s.row0 + (blk * 16 - pos0);
   const int half = a.rot / 2;
-
-  for (int i = threadIdx.x; i < 16 * half; i += kThreads) {
-    const int n = i / half, p = i % half;
-    if (n < f || n >= e) continue;
-    double t = (double)(blk * 16 + n) * (a.freqs[p] * 0.15915494309189535);   // turns
-    t -= floor(t);
-    float sn, cs;
-    sincospif(2.0f * (float)t, &sn, &cs);
-    turn[n][p] = make_float2(cs * a.rscale, sn * a.rscale);
-  }
-  __syncthreads();
-
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int jobs = a.Hq + 2 * a.kv.Hk;
+  const int page = blk < 0 ? -1 : a.kv.table[(int64_t)b * a.kv.table_stride + (blk >> a.kv.lb)];
+  const bool held = (unsigned)page < (unsigned)a.kv.n_pages;   // the block is one of the cache's
+
   // rows of q and k: lane -> (row of the step, 16 columns as two chunks of 8)
   const int c = lane % kLanes, rr = lane / kLanes;
   const bool turned = 16 * c < a.rot;
   const int dA = (!a.inter && turned) ? 8 * c : 16 * c;
   const int dB = (!a.inter && turned) ? half + 8 * c : 16 * c + 8;
 
-  for (int job = blockIdx.y * kWaves + wave; job < jobs; job += kWaves * gridDim.y) {
+  u32x4 raw[kRaw];                          // a job's rows as they come
+  float was = 0.f;                          // its block's scale so far
+  const auto load = [&](int job) {
+    if (job >= jobs) return;
+    if (job < a.Hq + a.kv.Hk) {
+      const bool is_q = job < a.Hq;
+      const uint16_t* src = (const uint16_t*)(is_q ? a.q : a.k) + (int64_t)(is_q ? job : job - a.Hq) * D;
+      const int64_t stride = is_q ? a.qs : a.ks;
+#pragma unroll
+      for (int st = 0; st < kSteps; ++st) {
+        const int n = st * kRows + rr;
+        raw[2 * st] = raw[2 * st + 1] = u32x4{0, 0, 0, 0};
+        if (n >= f && n < e) {
+          const uint16_t* p = src + (row_of_slot0 + n) * stride;
+          raw[2 * st] = ldg16(p + dA);
+          raw[2 * st + 1] = ldg16(p + dB);
+        }
+      }
+      if (!is_q && held && f > 0) was = a.kv.scales[2 * block_in(a.kv, page, blk, job - a.Hq)];
+    } else if (held) {
+      const uint16_t* src = (const uint16_t*)a.v + (int64_t)(job - a.Hq - a.kv.Hk) * D;
+#pragma unroll
+      for (int st = 0; st < kSt; ++st) {
+        const int l = st * 64 + lane, ch = l % kCh, g = l / kCh;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int n = 4 * g + i;
+          raw[4 * st + i] = u32x4{0, 0, 0, 0};
+          if (g < 4 && n >= f && n < e) raw[4 * st + i] = ldg16(src + (row_of_slot0 + n) * a.vs + 8 * ch);
+        }
+      }
+      if (f > 0) was = a.kv.scales[2 * block_in(a.kv, page, blk, job - a.Hq - a.kv.Hk) + 1];
+    }
+  };
+
+  int job = blockIdx.y * kWaves + wave;
+  load(job);
+
+  if (half > 0) {
+    // pair threadIdx.x % 128 of new tokens f + threadIdx.x / 128, ...
+    const int p = threadIdx.x % 128;
+    if (p < half) {
+      const double w = a.freqs[p] * 0.15915494309189535;       // turns a position
+      for (int n = f + (threadIdx.x / 128); n < e; n += kThreads / 128) {
+        double t = (double)(blk * 16 + n) * w;
+        t -= floor(t);
+        float sn, cs;
+        sincospif(2.0f * (float)t, &sn, &cs);
+        turn[n][p] = make_float2(cs * a.rscale, sn * a.rscale);
+      }
+    }
+    __syncthreads();
+  }
+
+  for (bool more = false; job < jobs; job += kWaves * gridDim.y, more = true) {
+    if (more) load(job);
     if (job < a.Hq + a.kv.Hk) {
       const bool is_q = job < a.Hq;
       const int h = is_q ? job : job - a.Hq;
-      const uint16_t* src = (const uint16_t*)(is_q ? a.q : a.k) + (int64_t)h * D;
-      const int64_t stride = is_q ? a.qs : a.ks;
       uint16_t* dst = (uint16_t*)(is_q ? a.q_out : a.k_out);
       const int64_t dstride = is_q ? a.qos : a.kos;
       float x[kSteps][16];
@@ -125,16 +190,10 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int nb) 
       for (int st = 0; st < kSteps; ++st) {
         const int n = st * kRows + rr;
         const bool on = n >= f && n < e;
-        u32x4 va = {0, 0, 0, 0}, vb = {0, 0, 0, 0};
-        if (on) {
-          const uint16_t* p = src + (row_of_slot0 + n) * stride;
-          va = ldg16(p + dA);
-          vb = ldg16(p + dB);
-        }
         float* A = x[st];
         float* B = x[st] + 8;
-        unpack8<T>(va, A);
-        unpack8<T>(vb, B);
+        unpack8<T>(raw[2 * st], A);
+        unpack8<T>(raw[2 * st + 1], B);
         if (turned && on) {
           const float2* t = &turn[n][8 * c];
           if (a.inter) {
@@ -167,15 +226,12 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int nb) 
           for (int j = 0; j < 16; ++j) m = amax_of(m, x[st][j]);
         }
       }
-      if (is_q || blk < 0) continue;
-      const int64_t at = block_of(a.kv, b, blk, h);
-      if (at < 0) continue;
+      if (is_q || !held) continue;
+      const int64_t at = block_in(a.kv, page, blk, h);
       uint8_t* tile = a.kv.codes + at * (32 * D);
-      float* sc = a.kv.scales + 2 * at;
-      const float was = f > 0 ? *sc : 0.f;
       const float now = fmaxf(was, least_scale(wave_max(m)));
       const float inv = inverse_pow2(now);
-      if (f > 0 && now > was) {             // earlier tokens of the block: lane c = 16*g + n
+      if (f > 0 && now > was) {       // earlier tokens of the block: lane c = 16*g + n
         if ((lane & 15) < f) {
           const float r = was * inv;
 #pragma unroll
@@ -204,42 +260,38 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int nb) 
           *reinterpret_cast<u32x2*>(tile + 1024 * (d >> 6) + 16 * (16 * ((d >> 3) & 3) + n) + 8 * ((d >> 5) & 1)) = w;
         }
       }
-      if (lane == 0) *sc = now;
-    } else {
-      // V: a lane takes 8 columns of 4 tokens, the words of its 8 columns
-      const int h = job - a.Hq - a.kv.Hk;
-      if (blk < 0) continue;
-      const int64_t at = block_of(a.kv, b, blk, h);
-      if (at < 0) continue;
-      constexpr int kCh = D / 8;                               // chunks of 8 columns
-      constexpr int kSt = kCh * 4 > 64 ? kCh * 4 / 64 : 1;
-      const uint16_t* src = (const uint16_t*)a.v + (int64_t)h * D;
-      u32x4 v[kSt][4];
-      float m = 0.f;
+      if (lane == 0) a.kv.scales[2 * at] = now;
+    } else if (held) {
+      const int64_t at = block_in(a.kv, page, blk, job - a.Hq - a.kv.Hk);
+      uint8_t* tile = a.kv.codes + at * (32 * D) + 16 * D;
+      // words that keep bytes of other tokens
+      uint32_t old[kSt][8];
 #pragma unroll
       for (int st = 0; st < kSt; ++st) {
         const int l = st * 64 + lane, ch = l % kCh, g = l / kCh;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int n = 4 * g + i;
-          v[st][i] = u32x4{0, 0, 0, 0};
-          if (g < 4 && n >= f && n < e) v[st][i] = ldg16(src + (row_of_slot0 + n) * a.vs + 8 * ch);
-          float x[8];
-          unpack8<T>(v[st][i], x);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) m = amax_of(m, x[j]);
+        for (int j = 0; j < 8; ++j) {
+          const int d = 8 * ch + j;
+          old[st][j] = 0;
+          if (g < 4 && (f > 4 * g || e < 4 * g + 4))
+            old[st][j] = *reinterpret_cast<const uint32_t*>(tile + 1024 * (d >> 6) + 16 * (16 * g + (d & 15)) + 4 * ((d >> 4) & 3));
         }
       }
-      uint8_t* tile = a.kv.codes + at * (32 * D) + 16 * D;
-      float* sc = a.kv.scales + 2 * at + 1;
-      const float was = f > 0 ? *sc : 0.f;
+      float m = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4 * kSt; ++i) {
+        float x[8];
+        unpack8<T>(raw[i], x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = amax_of(m, x[j]);
+      }
       const float now = fmaxf(was, least_scale(wave_max(m)));
       const float inv = inverse_pow2(now);
       const float r = was * inv;
 #pragma unroll
       for (int st = 0; st < kSt; ++st) {
         const int l = st * 64 + lane, ch = l % kCh, g = l / kCh;
-        const bool grow = f > 4 * g && now > was;              // holds tokens to be rounded again
+        const bool grow = f > 4 * g && now > was;        // holds tokens to be rounded again
         const bool fresh = f < 4 * g + 4 && e > 4 * g;         // gets new tokens
         if (g >= 4 || !(grow || fresh)) continue;
         // bytes of new tokens, and of earlier ones
@@ -249,21 +301,17 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int nb) 
         const uint32_t is_new = upto & ~below;
         float x[4][8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) unpack8<T>(v[st][i], x[i]);
+        for (int i = 0; i < 4; ++i) unpack8<T>(raw[4 * st + i], x[i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int d = 8 * ch + j;
-          uint32_t* w = reinterpret_cast<uint32_t*>(tile + 1024 * (d >> 6) + 16 * (16 * g + (d & 15)) + 4 * ((d >> 4) & 3));
           uint32_t word = code4(x[0][j] * inv, x[1][j] * inv, x[2][j] * inv, x[3][j] * inv);
-          if (is_new != 0xFFFFFFFFu) {
-            const uint32_t old = *w;
-            word = (word & is_new) | (old & ~is_new);
-            if (grow) word = (word & ~below) | (rescale4(old, r) & below);
-          }
-          *w = word;
+          word = (word & is_new) | (old[st][j] & ~is_new);
+          if (grow) word = (word & ~below) | (rescale4(old[st][j], r) & below);
+          *reinterpret_cast<uint32_t*>(tile + 1024 * (d >> 6) + 16 * (16 * g + (d & 15)) + 4 * ((d >> 4) & 3)) = word;
         }
       }
-      if (lane == 0) *sc = now;
+      if (lane == 0) a.kv.scales[2 * at + 1] = now;
     }
   }
 }
@@ -275,7 +323,7 @@ template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a, int nb) {
   constexpr int kPad = 8;
   __shared__ __attribute__((aligned(16))) uint16_t vt[kWaves][16][D + kPad];
-  const int b = blockIdx.x / nb, ib = blockIdx.x % nb;
+  const int b = nb == 1 ? blockIdx.x : blockIdx.x / nb, ib = nb == 1 ? 0 : blockIdx.x % nb;
   const Seq s = seq_of(a.kv, b);
   const int pos0 = s.len - s.n;
   const int blk = (pos0 >> 4) + ib;
