@@ -314,13 +314,23 @@ int check_packed(const char* who, const moe_packed* p, PrefillArgs* a) {
   return MOE_OK;
 }
 
+AttnWs prefill_ws(const PrefillArgs& a, int n) {
+  AttnWs w{0, 0, 0, kAlign};
+  if (n > 1) {
+    const size_t rows = (size_t)n * a.Tq * a.Hq;
+    w.ml = align_up(rows * a.D * 4);
+    w.total = w.ml + align_up(rows * 8);
+  }
+  return w;
+}
+
 }  // namespace
 
 extern "C" size_t moe_attn_prefill_workspace_bytes(const moe_packed* p) {
   clear_error();
   PrefillArgs a{};
   if (check_packed("moe_attn_prefill_workspace_bytes", p, &a) != MOE_OK) return 0;
-  return kAlign;
+  return prefill_ws(a, attn_prefill_parts(a, n_cus())).total;
 }
 
 extern "C" int moe_attn_prefill(const moe_packed* p, int dtype, const void* q, int64_t q_stride, const void* k,
@@ -340,8 +350,10 @@ extern "C" int moe_attn_prefill(const moe_packed* p, int dtype, const void* q, i
   if ((rc = check_rows(who, "out", out, out_stride, a.Hq, a.D)) != MOE_OK) return rc;
   if (!(scale > 0) || !isfinite(scale)) return bad(who, "scale must be positive and finite");
   if (!ws || !aligned16(ws)) return bad(who, "ws must be 16-byte aligned memory");
-  if (ws_bytes < kAlign)
-    return fail(MOE_ERR_WORKSPACE, std::string(who) + ": workspace too small (need " + std::to_string(kAlign) + ")");
+  const int n = attn_prefill_parts(a, n_cus());
+  const AttnWs w = prefill_ws(a, n);
+  if (ws_bytes < w.total)
+    return fail(MOE_ERR_WORKSPACE, std::string(who) + ": workspace too small (need " + std::to_string(w.total) + ")");
   a.q = q;
   a.k = k;
   a.v = v;
@@ -353,6 +365,7 @@ extern "C" int moe_attn_prefill(const moe_packed* p, int dtype, const void* q, i
   a.os = out_stride;
   a.c = scale * 1.4426950408889634f;
   a.causal = causal != 0;
-  hipError_t e = launch_attn_prefill(a, dtype, n_cus(), (hipStream_t)stream);
+  a.split = {(float*)((uint8_t*)ws + w.o), (float*)((uint8_t*)ws + w.ml), nullptr, n};
+  hipError_t e = launch_attn_prefill(a, dtype, (hipStream_t)stream);
   return e == hipSuccess ? MOE_OK : hip_fail(who, e);
 }

@@ -76,7 +76,9 @@ struct PrefillArgs {
   int64_t qs, ks, vs, os;
   float c;
   int causal;
+  SplitBuf split;           // parts [part][Tq][Hq] of the keys (where: unused)
 };
-hipError_t launch_attn_prefill(const PrefillArgs& a, int dtype, int cus, hipStream_t s);
+int attn_prefill_parts(const PrefillArgs& a, int cus);
+hipError_t launch_attn_prefill(const PrefillArgs& a, int dtype, hipStream_t s);
 
 }  // namespace qmoe

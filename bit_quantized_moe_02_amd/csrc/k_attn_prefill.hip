@@ -336,7 +336,7 @@ __device__ __forceinline__ bool step(Rows<T, D, CT>& R, Scores<CT>& S, Weights<C
 // that share keys share the staged tiles), all keys they see, tile by tile
 // in two LDS buffers: the next tile is on its way while one is computed.
 template <typename T, int D, int CT>
-__global__ __launch_bounds__(kThreads, CT == 1 && D <= 128 ? 2 : 1) void prefill_kernel(PrefillArgs a, int tiles) {
+__global__ __launch_bounds__(kThreads, CT > 1 || D > 128 ? 1 : D > 64 ? 2 : 3) void prefill_kernel(PrefillArgs a, int tiles) {
   constexpr int kRowsWg = 32 * CT * kWaves;
   constexpr int kBytes = kTile * D * 2;
   __shared__ __attribute__((aligned(1024))) uint8_t k0[kBytes], v0[kBytes], k1[kBytes], v1[kBytes];
@@ -392,37 +392,42 @@ __global__ __launch_bounds__(kThreads, CT == 1 && D <= 128 ? 2 : 1) void prefill
   const int any = a.causal ? shift + last_row / group : sk.n - 1;
   const int n_whole = all < 0 ? 0 : (all + 1) / kTile, n_tiles = any < 0 ? 0 : any / kTile + 1;
 
-  if (n_tiles > 0) {
+  // this part's tiles
+  const int per = (n_tiles + a.split.n - 1) / a.split.n;
+  const int t0 = blockIdx.y * per, t1 = min(t0 + per, n_tiles);
+
+  if (t0 < t1) {
     Keys<D> K;
     K.len = sk.n;
     K.k.init((const uint16_t*)a.k + (int64_t)sk.row0 * a.ks + (int64_t)hk * D, a.ks, wave, lane);
     K.v.init((const uint16_t*)a.v + (int64_t)sk.row0 * a.vs + (int64_t)hk * D, a.vs, wave, lane);
-    K.k.start(0, sk.n, k0, wave);
-    K.k.start(kTile, sk.n, k1, wave);
-    K.v.start(0, sk.n, v0, wave);
+    K.k.start(t0 * kTile, sk.n, k0, wave);
+    K.k.start((t0 + 1) * kTile, sk.n, k1, wave);
+    K.v.start(t0 * kTile, sk.n, v0, wave);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     Scores<CT> S;
     Weights<CT> W;
     scores<T, D, CT>(R, S, k0, lane);
-    step<true, true, T, D, CT>(R, S, W, K, 0, k0, k1, v0, v1, a.c, wave, lane);
-    int t = 1;
-    for (; t + 2 <= n_whole; t += 2) {
+    step<true, true, T, D, CT>(R, S, W, K, t0, k0, k1, v0, v1, a.c, wave, lane);
+    int t = t0 + 1;
+    const int t_whole = min(n_whole, t1);
+    for (; t + 2 <= t_whole; t += 2) {
       step<false, false, T, D, CT>(R, S, W, K, t, k1, k0, v1, v0, a.c, wave, lane);
       step<false, false, T, D, CT>(R, S, W, K, t + 1, k0, k1, v0, v1, a.c, wave, lane);
     }
     const int masked_from = t - 1;          // (its V is still to come)
     bool special = false;
-    for (; t < n_tiles; t += 2) {
+    for (; t < t1; t += 2) {
       special |= step<false, true, T, D, CT>(R, S, W, K, t, k1, k0, v1, v0, a.c, wave, lane);
-      if (t + 1 >= n_tiles) break;
+      if (t + 1 >= t1) break;
       special |= step<false, true, T, D, CT>(R, S, W, K, t + 1, k0, k1, v0, v1, a.c, wave, lane);
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    special |= add_values<true, T, D, CT>(R, W, n_tiles & 1 ? v0 : v1, lane);
+    special |= add_values<true, T, D, CT>(R, W, (t1 - t0) & 1 ? v0 : v1, lane);
     if (special)
-      add_special<T, D, CT>(R, K.v.base, K.v.row_bytes, masked_from * kTile, min(n_tiles * kTile, sk.n), lane);
+      add_special<T, D, CT>(R, K.v.base, K.v.row_bytes, masked_from * kTile, min(t1 * kTile, sk.n), lane);
   }
 #pragma unroll
   for (int t = 0; t < CT; ++t) {
@@ -430,8 +435,19 @@ __global__ __launch_bounds__(kThreads, CT == 1 && D <= 128 ? 2 : 1) void prefill
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const int r = w0 + 32 * t + col;
     if (r >= rows) continue;
-    const int tok = sq.row0 + r / group, h = hk * group + r % group;
-    uint16_t* p = (uint16_t*)a.out + (int64_t)tok * a.os + (int64_t)h * D + 4 * hh;
+    const int64_t row = sq.row0 + r / group, h = hk * group + r % group;
+    if (a.split.n > 1) {
+      const int64_t at = (blockIdx.y * (int64_t)a.Tq + row) * a.Hq + h;
+      float* p = a.split.o + at * D + 4 * hh;
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; e += 4)
+          *reinterpret_cast<f32x4*>(p + 32 * d + 2 * e) = f32x4{R.o[t][d][e], R.o[t][d][e + 1], R.o[t][d][e + 2], R.o[t][d][e + 3]};
+      if (hh == 0) *reinterpret_cast<float2*>(a.split.ml + 2 * at) = make_float2(R.m[t], sum);
+      continue;
+    }
+    uint16_t* p = (uint16_t*)a.out + row * a.os + h * D + 4 * hh;
 #pragma unroll
     for (int d = 0; d < D / 32; ++d)
 #pragma unroll
@@ -441,25 +457,68 @@ __global__ __launch_bounds__(kThreads, CT == 1 && D <= 128 ? 2 : 1) void prefill
         w.y = T::cvt2(R.o[t][d][e + 2] * inv, R.o[t][d][e + 3] * inv);
         *reinterpret_cast<u32x2*>(p + 32 * d + 2 * e) = w;
       }
-    if (hh == 0 && a.lse) a.lse[(int64_t)tok * a.Hq + h] = (R.m[t] + __builtin_amdgcn_logf(sum)) * kLn2;
+    if (hh == 0 && a.lse) a.lse[row * a.Hq + h] = (R.m[t] + __builtin_amdgcn_logf(sum)) * kLn2;
   }
 }
 
-template <typename T, int D, int CT>
+// Joins the parts of one row and head: a wave each, 4 columns a lane, as many
+// parts at once as a wave has lanes for.
+template <typename T, int D>
+__global__ __launch_bounds__(kThreads) void join_parts_kernel(PrefillArgs a) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int h = blockIdx.y * kWaves + wave, b = blockIdx.x / a.max_q, i = blockIdx.x % a.max_q;
+  const Seq sq = seq_rows(a.cu_q, a.per_q, a.Tq, b);
+  if (h >= a.Hq || i >= sq.n) return;
+  const int64_t row = sq.row0 + i, at = row * a.Hq + h, pitch = (int64_t)a.Tq * a.Hq;
+  constexpr int kCh = D / 4, kAtOnce = 64 / kCh;
+  const int ch = lane % kCh, p0 = lane / kCh;
+  float mx = kMinusInf;
+  for (int p = lane; p < a.split.n; p += 64) mx = fmaxf(mx, a.split.ml[2 * (at + p * pitch)]);
+  for (int o = 32; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
+  const float base = mx == kMinusInf ? 0.f : mx;
+  float sum = 0.f;
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int p = p0; p < a.split.n; p += kAtOnce) {
+    const float2 v = *reinterpret_cast<const float2*>(a.split.ml + 2 * (at + p * pitch));
+    const float e = exp2_fast(v.x - base);  // (a part that saw nothing: maximum -inf, zeros)
+    sum += e * v.y;
+    acc += *reinterpret_cast<const f32x4*>(a.split.o + (at + p * pitch) * D + 4 * ch) * e;
+  }
+#pragma unroll
+  for (int o = kCh; o < 64; o <<= 1) {
+    sum += __shfl_xor(sum, o);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] += __shfl_xor(acc[j], o);
+  }
+  if (p0 != 0) return;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  u32x2 w;
+  w.x = T::cvt2(acc[0] * inv, acc[1] * inv);
+  w.y = T::cvt2(acc[2] * inv, acc[3] * inv);
+  *reinterpret_cast<u32x2*>((uint16_t*)a.out + row * a.os + (int64_t)h * D + 4 * ch) = w;
+  if (ch == 0 && a.lse) a.lse[at] = (mx + __builtin_amdgcn_logf(sum)) * kLn2;
+}
+
+template <typename T, int D>
 hipError_t go(const PrefillArgs& a, hipStream_t s) {
   const int64_t rows = (int64_t)a.max_q * (a.Hq / a.Hk);
-  const int tiles = (int)((rows + 32 * CT * kWaves - 1) / (32 * CT * kWaves));
+  const int tiles = (int)((rows + 32 * kWaves - 1) / (32 * kWaves));
   const int64_t per_seq = ((int64_t)tiles * a.Hk + 7) / 8 * 8;   // whole rounds of the XCDs
-  hipLaunchKernelGGL((prefill_kernel<T, D, CT>), dim3((unsigned)(per_seq * a.B)), dim3(kThreads), 0, s, a, tiles);
+  hipLaunchKernelGGL((prefill_kernel<T, D, 1>), dim3((unsigned)(per_seq * a.B), (unsigned)a.split.n), dim3(kThreads), 0, s, a, tiles);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.split.n == 1) return e;
+  hipLaunchKernelGGL((join_parts_kernel<T, D>), dim3((unsigned)((int64_t)a.B * a.max_q), (unsigned)((a.Hq + kWaves - 1) / kWaves)),
+                     dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 
 template <typename T>
 hipError_t by_dim(const PrefillArgs& a, hipStream_t s) {
   switch (a.D) {
-    case 64: return go<T, 64, 1>(a, s);
-    case 128: return go<T, 128, 1>(a, s);
-    default: return go<T, 256, 1>(a, s);
+    case 64: return go<T, 64>(a, s);
+    case 128: return go<T, 128>(a, s);
+    default: return go<T, 256>(a, s);
   }
 }
 
@@ -467,8 +526,19 @@ hipError_t by_dim(const PrefillArgs& a, hipStream_t s) {
 
 namespace qmoe {
 
-hipError_t launch_attn_prefill(const PrefillArgs& a, int dtype, int cus, hipStream_t s) {
-  (void)cus;
+// Parts the keys are cut into where the rows alone would leave much of the
+// card idle: up to 4/3 workgroups a compute unit, each with 8 tiles of the
+// average context at least (fewer do not pay for the join).
+int attn_prefill_parts(const PrefillArgs& a, int cus) {
+  const int64_t rows = (int64_t)a.max_q * (a.Hq / a.Hk);
+  const int64_t wgs = (rows + 32 * kWaves - 1) / (32 * kWaves) * a.B * a.Hk;
+  const int64_t most = a.Tk / a.B / (8 * kTile);
+  int64_t n = 4ll * cus / 3 / wgs;
+  if (n > most) n = most;
+  return n < 1 ? 1 : (int)n;
+}
+
+hipError_t launch_attn_prefill(const PrefillArgs& a, int dtype, hipStream_t s) {
   return dtype == 0 ? by_dim<Bf16>(a, s) : by_dim<F16>(a, s);
 }
 

@@ -435,6 +435,11 @@ PREFILL = [  # query rows, key rows, query heads, key heads
     ([10, 4, 3], [200, 0, 1], 6, 2),                   # a chunk's end, no keys, more rows than keys
     ([130], [321], 8, 1),
     ([1, 1, 1, 1], [1, 63, 64, 65], 3, 1),
+    # enough heads to fill the card with row tiles of 128
+    ([5, 64, 127], [5, 64, 127], 64, 64),
+    ([3, 40, 100], [65, 300, 99], 128, 32),
+    ([129, 0, 9], [7, 3, 0], 48, 24),                  # (24 key heads on 8 XCDs)
+    ([60, 65], [60, 400], 99, 33),
 ]
 
 
@@ -449,8 +454,8 @@ def test_prefill(q, case, D, causal, dt):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
-@pytest.mark.parametrize("D", [64, 128])
-def test_prefill_special_values(q, D, dt):
+@pytest.mark.parametrize("D,heads", [(64, 1), (128, 1), (128, 64), (64, 64), (256, 1), (256, 64)])
+def test_prefill_special_values(q, D, heads, dt):
     """Infinities and NaN in keys and values reach the rows that see them, and no row before their token."""
     def spoil(k, v):
         v[60, 0, 3], v[61, 0, 9], v[90, 0, 33], v[100, 0, 0] = float("inf"), -float("inf"), float("nan"), float("nan")
@@ -458,19 +463,22 @@ def test_prefill_special_values(q, D, dt):
         k[110, 0, 7] = float("nan")
         v[139, 0, :] = float("nan")                    # the last key of the first sequence
     rng = np.random.default_rng(36)
-    _prefill(q, [140, 30], [140, 30], 2, 1, D, dt, True, rng, "special values", spoil=spoil)
+    _prefill(q, [140, 30], [140, 30], 2 * heads, heads, D, dt, True, rng, "special values", spoil=spoil)
 
 
 def test_prefill_longer(q):
     rng = np.random.default_rng(37)
     _prefill(q, [300, 700], [300, 1100], 4, 1, 128, "bf16", True, rng, "longer", sigma=3.0)
     _prefill(q, [513], [513], 4, 4, 64, "fp16", True, rng, "longer, narrow", sigma=3.0, max_q=2000)
+    _prefill(q, [300, 517], [300, 800], 32, 32, 128, "bf16", True, rng, "longer, many heads", sigma=3.0)
+    _prefill(q, [200, 333], [700, 800], 48, 16, 64, "fp16", False, rng, "longer, many heads, all keys", sigma=3.0)
 
 
 def test_prefill_few_rows_many_keys(q):
     rng = np.random.default_rng(38)
     _prefill(q, [3, 20], [2500, 3333], 4, 2, 128, "bf16", True, rng, "few rows", sigma=2.0)
     _prefill(q, [9], [2049], 2, 2, 64, "fp16", False, rng, "few rows, narrow")
+    _prefill(q, [1, 2, 0], [700, 5, 40], 2, 1, 256, "bf16", True, rng, "few rows, wide heads")
 
 
 def test_prefill_no_keys_at_all(q):
