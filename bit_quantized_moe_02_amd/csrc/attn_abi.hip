@@ -18,11 +18,13 @@ namespace {
 constexpr size_t kAlign = 256;
 constexpr int64_t kMaxRows = 1 << 24;       // rows of a call
 constexpr int64_t kMaxStride = 1 << 24;     // elements: a tile's offsets then fit 32 bits
-constexpr int64_t kMaxGrid = 0x7FFFFFFF;
+constexpr int64_t kMaxGrid = (1 << 24) - 1; // workgroups of 256 threads: 32-bit thread numbers
+constexpr int64_t kMaxBatch = 1 << 20;
 
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 
 int bad(const char* who, const std::string& what) { return fail(MOE_ERR_INVALID_ARG, std::string(who) + ": " + what); }
 
@@ -75,9 +77,11 @@ int check_cache(const char* who, const moe_kv_cache* c, const moe_kv_batch* b, K
   if (!dim_ok(c->head_dim)) return fail(MOE_ERR_UNSUPPORTED, std::string(who) + ": head_dim must be 64, 128 or 256");
   if (!c->codes || !c->scales) return bad(who, "the cache's codes or scales are NULL");
   if (!aligned16(c->codes) || !aligned16(c->scales)) return bad(who, "the cache must be 16-byte aligned");
-  if (b->batch < 1 || b->rows < 1 || b->rows > kMaxRows || b->max_new < 1 || b->pages_per_seq < 1)
-    return bad(who, "need batch, rows, max_new and pages_per_seq >= 1, rows <= 2^24");
+  if (b->batch < 1 || b->batch > kMaxBatch || b->rows < 1 || b->rows > kMaxRows || b->max_new < 1 || b->pages_per_seq < 1)
+    return bad(who, "need batch, rows, max_new and pages_per_seq >= 1, batch <= 2^20, rows <= 2^24");
   if (!b->page_table || !b->kv_lens) return bad(who, "page_table or kv_lens is NULL");
+  if (!aligned4(b->page_table) || !aligned4(b->kv_lens) || !aligned4(b->cu_rows))
+    return bad(who, "page_table, kv_lens and cu_rows must be 4-byte aligned");
   if (b->table_stride < b->pages_per_seq) return bad(who, "table_stride must be at least pages_per_seq");
   if ((int64_t)b->pages_per_seq * c->page_tokens > (1 << 30)) return bad(who, "more than 2^30 positions a sequence");
   if (!b->cu_rows && b->rows % b->batch != 0) return bad(who, "without cu_rows rows must be a multiple of batch");
@@ -108,9 +112,11 @@ int check_heads(const char* who, int q_heads, int kv_heads) {
 }
 
 // Grids of the attention kernels: 16-row tiles in the third dimension, a join for each row.
-int check_attn_grid(const char* who, int64_t batch, int64_t max_new, int64_t q_heads, int64_t kv_heads) {
-  if (batch > (1 << 20) || (max_new * (q_heads / kv_heads) + 15) / 16 > 65535 || batch * max_new > kMaxGrid)
+int check_attn_grid(const char* who, int64_t batch, int64_t max_new, int64_t max_len, int64_t q_heads, int64_t kv_heads) {
+  if ((max_new * (q_heads / kv_heads) + 15) / 16 > 65535 || batch * max_new > kMaxGrid)
     return bad(who, "batch, max_new or heads too large");
+  // the kernels number the steps of 32 positions of all sequences in 32 bits
+  if (batch * ((max_len + 31) / 32) > 0x7FFFFFFF - (1 << 20)) return bad(who, "batch * pages_per_seq * page_tokens too large");
   return MOE_OK;
 }
 
@@ -242,7 +248,7 @@ int check_decode_args(const char* who, const moe_kv_cache* cache, const moe_kv_b
   int rc = check_cache(who, cache, batch, kv);
   if (rc != MOE_OK) return rc;
   if ((rc = check_heads(who, q_heads, kv->Hk)) != MOE_OK) return rc;
-  return check_attn_grid(who, kv->B, kv->max_new, q_heads, kv->Hk);
+  return check_attn_grid(who, kv->B, kv->max_new, kv->max_len, q_heads, kv->Hk);
 }
 
 }  // namespace
@@ -267,6 +273,7 @@ extern "C" int moe_attn_decode(const moe_kv_cache* cache, const moe_kv_batch* ba
   if ((rc = check_rows(who, "q", q, q_stride, q_heads, a.kv.D)) != MOE_OK) return rc;
   if ((rc = check_rows(who, "out", out, out_stride, q_heads, a.kv.D)) != MOE_OK) return rc;
   if (!(scale > 0) || !isfinite(scale)) return bad(who, "scale must be positive and finite");
+  if (!aligned4(lse)) return bad(who, "lse must be 4-byte aligned");
   if (!ws || !aligned16(ws)) return bad(who, "ws must be 16-byte aligned memory");
   const int n = attn_decode_workers(a.kv, q_heads, n_cus());
   const AttnWs w = attn_ws(n, a.kv, q_heads);
@@ -288,12 +295,13 @@ namespace {
 
 int check_packed(const char* who, const moe_packed* p, PrefillArgs* a) {
   if (!p) return bad(who, "the packed description is NULL");
-  if (p->batch < 1 || p->rows_q < 1 || p->rows_q > kMaxRows || p->rows_k < 0 || p->rows_k > kMaxRows || p->max_q < 1)
-    return bad(who, "need batch, rows_q and max_q >= 1, rows_k >= 0, rows <= 2^24");
+  if (p->batch < 1 || p->batch > kMaxBatch || p->rows_q < 1 || p->rows_q > kMaxRows || p->rows_k < 0 || p->rows_k > kMaxRows || p->max_q < 1)
+    return bad(who, "need batch, rows_q and max_q >= 1, rows_k >= 0, batch <= 2^20, rows <= 2^24");
   if (p->kv_heads < 1 || p->kv_heads > 256) return bad(who, "need 1 <= kv_heads <= 256");
   int rc = check_heads(who, p->q_heads, p->kv_heads);
   if (rc != MOE_OK) return rc;
   if (!dim_ok(p->head_dim)) return fail(MOE_ERR_UNSUPPORTED, std::string(who) + ": head_dim must be 64, 128 or 256");
+  if (!aligned4(p->cu_q) || !aligned4(p->cu_k)) return bad(who, "cu_q and cu_k must be 4-byte aligned");
   if (!p->cu_q && p->rows_q % p->batch != 0) return bad(who, "without cu_q rows_q must be a multiple of batch");
   if (!p->cu_k && p->rows_k % p->batch != 0) return bad(who, "without cu_k rows_k must be a multiple of batch");
   if (!p->cu_q && p->rows_q / p->batch > p->max_q) return bad(who, "max_q is smaller than rows_q / batch");
@@ -308,8 +316,9 @@ int check_packed(const char* who, const moe_packed* p, PrefillArgs* a) {
   a->Hq = p->q_heads;
   a->Hk = p->kv_heads;
   a->D = p->head_dim;
+  // (row tiles of 128, whole rounds of 8 XCDs)
   if ((int64_t)a->max_q * (a->Hq / a->Hk) > (1 << 30) ||
-      ((int64_t)a->max_q * (a->Hq / a->Hk) / 32 + 1) * a->B * a->Hk > kMaxGrid)
+      ((((int64_t)a->max_q * (a->Hq / a->Hk) + 127) / 128) * a->Hk + 7) * a->B > kMaxGrid)
     return bad(who, "batch, max_q or heads too large");
   return MOE_OK;
 }
@@ -349,6 +358,7 @@ extern "C" int moe_attn_prefill(const moe_packed* p, int dtype, const void* q, i
   }
   if ((rc = check_rows(who, "out", out, out_stride, a.Hq, a.D)) != MOE_OK) return rc;
   if (!(scale > 0) || !isfinite(scale)) return bad(who, "scale must be positive and finite");
+  if (!aligned4(lse)) return bad(who, "lse must be 4-byte aligned");
   if (!ws || !aligned16(ws)) return bad(who, "ws must be 16-byte aligned memory");
   const int n = attn_prefill_parts(a, n_cus());
   const AttnWs w = prefill_ws(a, n);

@@ -190,7 +190,7 @@ __global__ __launch_bounds__(64 * (Short ? kShortWaves : kWaves), Short ? 1 : oc
       a.split.where[b] = make_int2(worker, (first + cost - 1) / cut.per - worker + 1);
     first += cost;
     pos = Short ? end : min(first, end);
-    const int rows = s.n * group;
+    const int rows = min(s.n, a.kv.max_new) * group;
     if (r0 >= rows) continue;               // (the same for the whole workgroup)
 
     // this lane's row of each row tile: its q (the second operand) and the

@@ -167,11 +167,14 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int nb) 
     if (p < half) {
       const double w = a.freqs[p] * 0.15915494309189535;       // turns a position
       for (int n = f + (threadIdx.x / 128); n < e; n += kThreads / 128) {
-        double t = (double)(blk * 16 + n) * w;
-        t -= floor(t);
+        // the nearest quarter turn off in 64 bits, the rest (an eighth at most,
+        // so exact to 2^-28 turns) in 32, and the quarters by exchange
+        const double t = 4.0 * (double)(blk * 16 + n) * w, quarters = rint(t);
         float sn, cs;
-        sincospif(2.0f * (float)t, &sn, &cs);
-        turn[n][p] = make_float2(cs * a.rscale, sn * a.rscale);
+        sincospif(0.5f * (float)(t - quarters), &sn, &cs);
+        const int k = (int)(quarters - 4.0 * floor(0.25 * quarters));
+        const float s4 = k & 1 ? cs : sn, c4 = k & 1 ? sn : cs;
+        turn[n][p] = make_float2((k == 1 || k == 2 ? -c4 : c4) * a.rscale, (k >= 2 ? -s4 : s4) * a.rscale);
       }
     }
     __syncthreads();

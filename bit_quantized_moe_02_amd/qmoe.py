@@ -676,7 +676,7 @@ def moe_attn_decode(cache, batch, q, out, ws, scale, lse=None, stream=None):
 def moe_attn_prefill_workspace_bytes(rows_q: int, batch: int, max_q: int, rows_k: int, q_heads: int, kv_heads: int,
                                      head_dim: int) -> int:
     # (which rows belong to which sequence does not matter here: any offsets stand for them)
-    p = MoePacked(batch, rows_q, rows_k, max_q, 1, 1, q_heads, kv_heads, head_dim)
+    p = MoePacked(batch, rows_q, rows_k, max_q, 16, 16, q_heads, kv_heads, head_dim)
     return int(lib.moe_attn_prefill_workspace_bytes(ctypes.byref(p)))
 
 

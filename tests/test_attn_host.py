@@ -77,7 +77,8 @@ def _batch(q, **kw):
 BAD_CACHE = [dict(n_pages=0), dict(page_tokens=24), dict(page_tokens=2048), dict(kv_heads=0), dict(kv_heads=300), dict(head_dim=80),
              dict(codes=None), dict(scales=None), dict(codes=P + 8), dict(scales=P + 4)]
 BAD_BATCH = [dict(batch=0), dict(rows=0), dict(rows=(1 << 24) + 2), dict(max_new=0), dict(max_new=2), dict(rows=7), dict(pages_per_seq=0),
-             dict(page_table=None), dict(kv_lens=None), dict(table_stride=3), dict(pages_per_seq=1 << 25, table_stride=1 << 25)]
+             dict(page_table=None), dict(kv_lens=None), dict(page_table=P + 2), dict(kv_lens=P + 1), dict(cu_rows=P + 2),
+             dict(batch=(1 << 20) + 1, rows=1 << 21, max_new=1 << 21, cu_rows=P), dict(table_stride=3), dict(pages_per_seq=1 << 25, table_stride=1 << 25)]
 
 
 def _calls(q, c, b):
@@ -137,13 +138,15 @@ def test_decode_rows_refused(q):
 
     assert call(dtype=7) == q.MOE_ERR_UNSUPPORTED
     for kw in (dict(q=None), dict(out=None), dict(hq=3), dict(hq=0), dict(hq=4098), dict(qs=128), dict(os=252), dict(scale=0.0), dict(scale=-1.0),
-               dict(scale=float("nan")), dict(scale=float("inf")), dict(ws=None), dict(ws=P + 8)):
+               dict(scale=float("nan")), dict(scale=float("inf")), dict(ws=None), dict(ws=P + 8), dict(lse=P + 2)):
         assert call(**kw) == q.MOE_ERR_INVALID_ARG, kw
     need = lib.moe_attn_decode_workspace_bytes(R(c), R(b), 4)
     assert need >= 256
     assert call(wsb=need - 1) == q.MOE_ERR_WORKSPACE and str(need) in q.moe_last_error()
-    huge = _batch(q, batch=1 << 24, rows=1 << 24, max_new=1 << 24, cu_rows=P)
-    assert lib.moe_attn_decode_workspace_bytes(R(c), R(huge), 4) == 0
+    # more workgroups than a launch numbers; more steps of positions than 32 bits number
+    for huge in (_batch(q, batch=1 << 10, rows=1 << 24, max_new=1 << 24, cu_rows=P),
+                 _batch(q, batch=1 << 20, rows=1 << 20, max_new=1, pages_per_seq=1 << 12, table_stride=1 << 12, cu_rows=P)):
+        assert lib.moe_attn_decode_workspace_bytes(R(c), R(huge), 4) == 0 and "too large" in q.moe_last_error()
 
 
 def test_prefill_refused(q):
@@ -156,7 +159,8 @@ def test_prefill_refused(q):
 
     for s in (dict(batch=0), dict(rows_q=0), dict(rows_k=-1), dict(max_q=0), dict(q_heads=5), dict(q_heads=0), dict(kv_heads=0),
               dict(kv_heads=300), dict(rows_q=(1 << 24) + 1), dict(rows_k=(1 << 24) + 1), dict(cu_q=None, rows_q=7), dict(cu_k=None, rows_k=7),
-              dict(cu_q=None, max_q=3), dict(batch=1 << 30, max_q=8)):
+              dict(cu_q=None, max_q=3), dict(batch=(1 << 20) + 1),
+              dict(cu_q=P + 1), dict(cu_k=P + 2), dict(batch=1 << 20, rows_q=1 << 24, max_q=1 << 24, q_heads=256, kv_heads=256)):
         assert call(s) == q.MOE_ERR_INVALID_ARG, s
         assert lib.moe_attn_prefill_workspace_bytes(R(q.MoePacked(*{**shape, **s}.values()))) == 0
     assert call(dict(head_dim=32)) == q.MOE_ERR_UNSUPPORTED and call(dtype=3) == q.MOE_ERR_UNSUPPORTED

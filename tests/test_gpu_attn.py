@@ -352,6 +352,28 @@ def test_lengths_are_clamped(q):
     q.moe_kv_append(dev, batch, back, back)
 
 
+def test_more_rows_than_max_new(q):
+    """A sequence with more rows than max_new says: the first max_new are right, and nothing else is written."""
+    rng = np.random.default_rng(44)
+    Hk, D, page, Hq, lens, ns = 2, 128, 16, 2, [1500, 300], [9, 3]
+    table, n_pages = page_table(rng, lens, page)
+    cache = A.Cache(*random_cache(rng, n_pages, page, Hk, D), page, Hk, D)
+    dev = to_device(q, cache)
+    qt, qv = rows_in(rng, 12, Hq, D, torch.bfloat16)
+    batch = q.KvBatch(i32(table), i32(lens), 12, 3, i32(cu_of(ns)))
+    need = q.moe_attn_decode_workspace_bytes(dev, batch, Hq)
+    ws = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    out, lse = torch.full_like(qt, 9.0), torch.full((12, Hq), 9.0, device="cuda")
+    q.moe_attn_decode(dev, batch, qt, out, ws[:need], 0.09, lse)
+    assert torch.all(ws[need:] == 0x5A)
+    assert torch.all(out[3:9] == 9.0) and torch.all(lse[3:9] == 9.0)
+    for b, rows in ((0, slice(0, 3)), (1, slice(9, 12))):
+        K, V, _ = cache.read(table[b], 0, lens[b])
+        seen = np.arange(lens[b])[None] <= (lens[b] - ns[b] + np.arange(3))[:, None]
+        ref, rl, mag, smag = A.attention(qv[rows], K, V, seen, 0.09)
+        check_attention(out[rows], lse[rows], ref, rl, *attention_bounds(torch.bfloat16, D, V, ref, mag, smag, lens[b]), f"sequence {b}")
+
+
 def test_decode_is_repeatable_and_needs_no_clean_workspace(q):
     rng = np.random.default_rng(34)
     Hk, D, page, lens = 2, 128, 64, [5000, 300, 4097]
