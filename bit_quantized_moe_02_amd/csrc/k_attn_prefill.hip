@@ -126,9 +126,10 @@ struct Weights {
 // raised when a score exceeds it by 2^8 (or a row has none yet): the weights
 // are then at most 2^8, which costs no precision, and the sums are hardly ever
 // rescaled.
-// Masked: some row of the wave does not see some key of the tile.
+// Masked, partly: some row of the workgroup does not see some key of the tile.
 template <bool Masked, typename T, int D, int CT>
-__device__ __forceinline__ bool exponents(const Rows<T, D, CT>& R, Scores<CT>& S, float* mx, int j0, float c, int lane) {
+__device__ __forceinline__ bool exponents(const Rows<T, D, CT>& R, Scores<CT>& S, float* mx, int j0, bool partly, float c,
+                                          int lane) {
   const int hh = lane >> 5;
   bool raise = false;
 #pragma unroll
@@ -136,7 +137,7 @@ __device__ __forceinline__ bool exponents(const Rows<T, D, CT>& R, Scores<CT>& S
     const float base = R.m[t] == kMinusInf ? 0.f : R.m[t];
 #pragma unroll
     for (int e = 0; e < 32; ++e) S.s[t][e >> 4][e & 15] = __builtin_fmaf(S.s[t][e >> 4][e & 15], c, -base);
-    if (Masked) {
+    if (Masked && partly) {
       const int seen = only_here(R.last[t] - j0 - 4 * hh);
 #pragma unroll
       for (int e = 0; e < 32; ++e)
@@ -219,17 +220,17 @@ __device__ __forceinline__ void take_special(u32x4& v) {
   }
 }
 
-// Says whether it met such values (Masked; a sum of squares finds them, and
-// very large ones).
+// Says whether it met such values (Masked, partly as above; a sum of squares
+// finds them, and very large ones).
 template <bool Masked, typename T, int D, int CT>
-__device__ __forceinline__ bool add_values(Rows<T, D, CT>& R, const Weights<CT>& W, const uint8_t* vt, int lane) {
+__device__ __forceinline__ bool add_values(Rows<T, D, CT>& R, const Weights<CT>& W, const uint8_t* vt, bool partly, int lane) {
   bool special = false;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     u32x4 v[D / 32];
 #pragma unroll
     for (int d = 0; d < D / 32; ++d) v[d] = value_operand<D>(vt, k, d, lane);
-    if (Masked) {
+    if (Masked && partly) {
       float sq[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int d = 0; d < D / 32; ++d)
@@ -289,17 +290,17 @@ struct Keys {
 // zeros, so nothing here asks which is the last.
 template <bool First, bool Masked, typename T, int D, int CT>
 __device__ __forceinline__ bool step(Rows<T, D, CT>& R, Scores<CT>& S, Weights<CT>& W, const Keys<D>& K, int t,
-                                     uint8_t* k_this, uint8_t* k_next, uint8_t* v_this, uint8_t* v_last, float c, int wave,
-                                     int lane) {
+                                     uint8_t* k_this, uint8_t* k_next, uint8_t* v_this, uint8_t* v_last, int n_whole,
+                                     float c, int wave, int lane) {
   const int j0 = t * kTile;
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
   K.k.start(j0 + 2 * kTile, K.len, k_this, wave);
   if (!First) K.v.start(j0, K.len, v_this, wave);
   float mx[CT];
-  const bool raise = exponents<Masked, T, D, CT>(R, S, mx, j0, c, lane);
+  const bool raise = exponents<Masked, T, D, CT>(R, S, mx, j0, t >= n_whole, c, lane);
   bool special = false;
-  if (!First) special = add_values<Masked, T, D, CT>(R, W, v_last, lane);
+  if (!First) special = add_values<Masked, T, D, CT>(R, W, v_last, t > n_whole, lane);
   if (!First && !Masked) {
     __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
 #pragma unroll
@@ -409,23 +410,23 @@ __global__ __launch_bounds__(kThreads, CT > 1 || D > 128 ? 1 : D > 64 ? 2 : 3) v
     Scores<CT> S;
     Weights<CT> W;
     scores<T, D, CT>(R, S, k0, lane);
-    step<true, true, T, D, CT>(R, S, W, K, t0, k0, k1, v0, v1, a.c, wave, lane);
+    step<true, true, T, D, CT>(R, S, W, K, t0, k0, k1, v0, v1, n_whole, a.c, wave, lane);
     int t = t0 + 1;
     const int t_whole = min(n_whole, t1);
     for (; t + 2 <= t_whole; t += 2) {
-      step<false, false, T, D, CT>(R, S, W, K, t, k1, k0, v1, v0, a.c, wave, lane);
-      step<false, false, T, D, CT>(R, S, W, K, t + 1, k0, k1, v0, v1, a.c, wave, lane);
+      step<false, false, T, D, CT>(R, S, W, K, t, k1, k0, v1, v0, n_whole, a.c, wave, lane);
+      step<false, false, T, D, CT>(R, S, W, K, t + 1, k0, k1, v0, v1, n_whole, a.c, wave, lane);
     }
     const int masked_from = t - 1;          // (its V is still to come)
     bool special = false;
     for (; t < t1; t += 2) {
-      special |= step<false, true, T, D, CT>(R, S, W, K, t, k1, k0, v1, v0, a.c, wave, lane);
+      special |= step<false, true, T, D, CT>(R, S, W, K, t, k1, k0, v1, v0, n_whole, a.c, wave, lane);
       if (t + 1 >= t1) break;
-      special |= step<false, true, T, D, CT>(R, S, W, K, t + 1, k0, k1, v0, v1, a.c, wave, lane);
+      special |= step<false, true, T, D, CT>(R, S, W, K, t + 1, k0, k1, v0, v1, n_whole, a.c, wave, lane);
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    special |= add_values<true, T, D, CT>(R, W, (t1 - t0) & 1 ? v0 : v1, lane);
+    special |= add_values<true, T, D, CT>(R, W, (t1 - t0) & 1 ? v0 : v1, t1 > n_whole, lane);
     if (special)
       add_special<T, D, CT>(R, K.v.base, K.v.row_bytes, masked_from * kTile, min(t1 * kTile, sk.n), lane);
   }
