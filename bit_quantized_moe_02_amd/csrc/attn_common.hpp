@@ -155,4 +155,40 @@ __device__ __forceinline__ float sum_halves(float x) {
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// One wave joins the n parts of one row and head, 4 columns a lane, as many
+// parts at once as it has lanes for: part p's un-normalised output at
+// o + p * pitch * D, its (maximum, sum) at ml + 2 * p * pitch; lse may be null.
+template <typename T, int D>
+__device__ __forceinline__ void join_row(const float* o, const float* ml, int n, int64_t pitch, uint16_t* out, float* lse,
+                                         int lane) {
+  constexpr int kCh = D / 4, kAtOnce = 64 / kCh;
+  const int ch = lane % kCh, p0 = lane / kCh;
+  float mx = kMinusInf;
+  for (int p = lane; p < n; p += 64) mx = fmaxf(mx, ml[2 * p * pitch]);
+  for (int s = 32; s >= 1; s >>= 1) mx = fmaxf(mx, __shfl_xor(mx, s));
+  const float base = mx == kMinusInf ? 0.f : mx;
+  float sum = 0.f;
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int p = p0; p < n; p += kAtOnce) {
+    const float2 v = *reinterpret_cast<const float2*>(ml + 2 * p * pitch);
+    const float e = exp2_fast(v.x - base);  // (a part that saw nothing: maximum -inf, zeros)
+    sum += e * v.y;
+    acc += *reinterpret_cast<const f32x4*>(o + p * pitch * D + 4 * ch) * e;
+  }
+#pragma unroll
+  for (int s = kCh; s < 64; s <<= 1) {
+    sum += __shfl_xor(sum, s);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] += __shfl_xor(acc[j], s);
+  }
+  if (p0 != 0) return;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  u32x2 w;
+  w.x = T::cvt2(acc[0] * inv, acc[1] * inv);
+  w.y = T::cvt2(acc[2] * inv, acc[3] * inv);
+  *reinterpret_cast<u32x2*>(out + 4 * ch) = w;
+  if (ch == 0 && lse) *lse = (mx + __builtin_amdgcn_logf(sum)) * kLn2;
+}
+
 }  // namespace qmoe_dev

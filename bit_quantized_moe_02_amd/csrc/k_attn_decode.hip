@@ -486,6 +486,18 @@ __global__ __launch_bounds__(kThreads) void join_kernel(DecodeArgs a) {
   if (ch == 0 && a.lse) a.lse[row * a.Hq + h] = (mx + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
+// The same by a wave each, four heads a workgroup: a few parts.
+template <typename T, int D>
+__global__ __launch_bounds__(kThreads) void join_few_kernel(DecodeArgs a) {
+  const int b = blockIdx.x / a.kv.max_new, i = blockIdx.x % a.kv.max_new, h = blockIdx.y * (kThreads / 64) + (threadIdx.x >> 6);
+  const int2 where = a.split.where[b];
+  const Seq s = seq_rows(a.kv.cu, a.kv.per_seq, a.kv.T, b);
+  if (h >= a.Hq || i >= s.n || where.y == 1) return;
+  const int64_t pitch = (int64_t)a.kv.max_new * a.Hq, at = (where.x + b) * pitch + (int64_t)i * a.Hq + h, row = s.row0 + i;
+  join_row<T, D>(a.split.o + at * D, a.split.ml + 2 * at, where.y, pitch, (uint16_t*)a.out + row * a.os + (int64_t)h * D,
+                 a.lse ? a.lse + row * a.Hq + h : nullptr, threadIdx.x & 63);
+}
+
 int rows_of(const KvArgs& kv, int Hq) { return kv.max_new * (Hq / kv.Hk); }
 
 // Row tiles of 16 a workgroup takes: as many as the step needs, up to 4 (64
@@ -514,6 +526,13 @@ void (*pick_dim(int dim, int nr, bool shrt))(DecodeArgs) {
   return dim == 64 ? pick<T, 64>(nr, shrt) : dim == 128 ? pick<T, 128>(nr, shrt) : pick<T, 256>(nr, shrt);
 }
 
+template <typename T>
+void (*pick_join(int dim, bool few))(DecodeArgs) {
+  if (dim == 64) return few ? join_few_kernel<T, 64> : join_kernel<T, 64>;
+  if (dim == 128) return few ? join_few_kernel<T, 128> : join_kernel<T, 128>;
+  return few ? join_few_kernel<T, 256> : join_kernel<T, 256>;
+}
+
 }  // namespace
 
 namespace qmoe {
@@ -532,18 +551,17 @@ hipError_t launch_attn_decode(const DecodeArgs& a, int dtype, hipStream_t s) {
   const int nr = row_tiles(a.kv, a.Hq);
   const bool bf = dtype == 0, shrt = is_short(a.kv, nr);
   auto fn = bf ? pick_dim<Bf16>(a.kv.D, nr, shrt) : pick_dim<F16>(a.kv.D, nr, shrt);
-  void (*join)(DecodeArgs) = nullptr;
-  switch (a.kv.D) {
-    case 64: join = bf ? join_kernel<Bf16, 64> : join_kernel<F16, 64>; break;
-    case 128: join = bf ? join_kernel<Bf16, 128> : join_kernel<F16, 128>; break;
-    default: join = bf ? join_kernel<Bf16, 256> : join_kernel<F16, 256>; break;
-  }
   hipLaunchKernelGGL(fn, dim3((unsigned)a.kv.Hk, (unsigned)(shrt ? a.kv.B : a.split.n),
                               (unsigned)((rows_of(a.kv, a.Hq) + 16 * nr - 1) / (16 * nr))),
                      dim3(64 * (shrt ? kShortWaves : kWaves)), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.split.n == 1) return e;
-  hipLaunchKernelGGL(join, dim3((unsigned)(a.kv.B * (int64_t)a.kv.max_new), (unsigned)a.Hq), dim3(kThreads), 0, s, a);
+  // a wave a row where the ranges make at most 16 parts a sequence (16 users'
+  // drafts of 3, 64 heads, 4 parts: 3.9 us, a workgroup a row 5.5)
+  const bool few = a.split.n <= 16 * a.kv.B;
+  auto join = bf ? pick_join<Bf16>(a.kv.D, few) : pick_join<F16>(a.kv.D, few);
+  hipLaunchKernelGGL(join, dim3((unsigned)(a.kv.B * (int64_t)a.kv.max_new), (unsigned)(few ? (a.Hq + 3) / 4 : a.Hq)),
+                     dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 

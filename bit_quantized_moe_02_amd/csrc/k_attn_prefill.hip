@@ -462,43 +462,15 @@ __global__ __launch_bounds__(kThreads, CT > 1 || D > 128 ? 1 : D > 64 ? 2 : 3) v
   }
 }
 
-// Joins the parts of one row and head: a wave each, 4 columns a lane, as many
-// parts at once as a wave has lanes for.
+// Joins the parts of one row and head: a wave each.
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void join_parts_kernel(PrefillArgs a) {
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int h = blockIdx.y * kWaves + wave, b = blockIdx.x / a.max_q, i = blockIdx.x % a.max_q;
+  const int h = blockIdx.y * kWaves + (threadIdx.x >> 6), b = blockIdx.x / a.max_q, i = blockIdx.x % a.max_q;
   const Seq sq = seq_rows(a.cu_q, a.per_q, a.Tq, b);
   if (h >= a.Hq || i >= sq.n) return;
-  const int64_t row = sq.row0 + i, at = row * a.Hq + h, pitch = (int64_t)a.Tq * a.Hq;
-  constexpr int kCh = D / 4, kAtOnce = 64 / kCh;
-  const int ch = lane % kCh, p0 = lane / kCh;
-  float mx = kMinusInf;
-  for (int p = lane; p < a.split.n; p += 64) mx = fmaxf(mx, a.split.ml[2 * (at + p * pitch)]);
-  for (int o = 32; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
-  const float base = mx == kMinusInf ? 0.f : mx;
-  float sum = 0.f;
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int p = p0; p < a.split.n; p += kAtOnce) {
-    const float2 v = *reinterpret_cast<const float2*>(a.split.ml + 2 * (at + p * pitch));
-    const float e = exp2_fast(v.x - base);  // (a part that saw nothing: maximum -inf, zeros)
-    sum += e * v.y;
-    acc += *reinterpret_cast<const f32x4*>(a.split.o + (at + p * pitch) * D + 4 * ch) * e;
-  }
-#pragma unroll
-  for (int o = kCh; o < 64; o <<= 1) {
-    sum += __shfl_xor(sum, o);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[j] += __shfl_xor(acc[j], o);
-  }
-  if (p0 != 0) return;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  u32x2 w;
-  w.x = T::cvt2(acc[0] * inv, acc[1] * inv);
-  w.y = T::cvt2(acc[2] * inv, acc[3] * inv);
-  *reinterpret_cast<u32x2*>((uint16_t*)a.out + row * a.os + (int64_t)h * D + 4 * ch) = w;
-  if (ch == 0 && a.lse) a.lse[at] = (mx + __builtin_amdgcn_logf(sum)) * kLn2;
+  const int64_t row = sq.row0 + i, at = row * a.Hq + h;
+  join_row<T, D>(a.split.o + at * D, a.split.ml + 2 * at, a.split.n, (int64_t)a.Tq * a.Hq,
+                 (uint16_t*)a.out + row * a.os + (int64_t)h * D, a.lse ? a.lse + at : nullptr, threadIdx.x & 63);
 }
 
 template <typename T, int D>
