@@ -78,47 +78,42 @@ __device__ __forceinline__ u32x2 lds_tr(const uint8_t* p) {
   return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p));
 }
 
-// A wave's state: 32*CT rows, row lane % 32 of each group of 32.
-template <typename T, int D, int CT>
+// A wave's state: 32 rows, row lane % 32.
+template <typename T, int D>
 struct Rows {
-  u32x4 q[CT][D / 16];
-  f32x16 o[CT][D / 32];
-  float m[CT], l[CT];
-  int last[CT];                             // last key the row sees, -1: none
+  u32x4 q[D / 16];
+  f32x16 o[D / 32];
+  float m, l;
+  int last;                                 // last key the row sees, -1: none
 };
 
 // Scores of a tile.  With K as the first operand of a 32x32x16 product a lane
 // gets 16 of 32 keys of one query row (column lane % 32): maximum and sum are
 // nearly all inside a lane, and the weights are already the second operand
 // of the product with V.
-template <int CT>
 struct Scores {
-  f32x16 s[CT][2];                          // key 32 i + 8 (e / 4) + 4 hh + e % 4 in s[.][i][e]
+  f32x16 s[2];                              // key 32 i + 8 (e / 4) + 4 hh + e % 4 in s[i][e]
 };
 
-template <typename T, int D, int CT>
-__device__ __forceinline__ void scores(const Rows<T, D, CT>& R, Scores<CT>& S, const uint8_t* kt, int lane) {
+template <typename T, int D>
+__device__ __forceinline__ void scores(const Rows<T, D>& R, Scores& S, const uint8_t* kt, int lane) {
   const int col = lane & 31, hh = lane >> 5;
 #pragma unroll
   for (int kb = 0; kb < D / 16; ++kb) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const u32x4 k = *reinterpret_cast<const u32x4*>(kt + ((32 * i + col) * (2 * D) + 16 * k_piece<D>(32 * i + col, 2 * kb + hh)));
-#pragma unroll
-      for (int t = 0; t < CT; ++t) {
-        if (kb == 0)
-          S.s[t][i] = T::mma32(k, R.q[t][kb], f32x16{});
-        else
-          S.s[t][i] = T::mma32(k, R.q[t][kb], S.s[t][i]);
-      }
+      if (kb == 0)
+        S.s[i] = T::mma32(k, R.q[kb], f32x16{});
+      else
+        S.s[i] = T::mma32(k, R.q[kb], S.s[i]);
     }
   }
 }
 
 // Weights of a tile's 64 keys, as operands: four groups of 16 keys.
-template <int CT>
 struct Weights {
-  u32x4 p[CT][4];
+  u32x4 p[4];
 };
 
 // Scores as powers of two under the running maximum, in place; says whether
@@ -127,69 +122,58 @@ struct Weights {
 // are then at most 2^8, which costs no precision, and the sums are hardly ever
 // rescaled.
 // Masked, partly: some row of the workgroup does not see some key of the tile.
-template <bool Masked, typename T, int D, int CT>
-__device__ __forceinline__ bool exponents(const Rows<T, D, CT>& R, Scores<CT>& S, float* mx, int j0, bool partly, float c,
+template <bool Masked, typename T, int D>
+__device__ __forceinline__ bool exponents(const Rows<T, D>& R, Scores& S, float& mx, int j0, bool partly, float c,
                                           int lane) {
   const int hh = lane >> 5;
-  bool raise = false;
+  const float base = R.m == kMinusInf ? 0.f : R.m;
 #pragma unroll
-  for (int t = 0; t < CT; ++t) {
-    const float base = R.m[t] == kMinusInf ? 0.f : R.m[t];
+  for (int e = 0; e < 32; ++e) S.s[e >> 4][e & 15] = __builtin_fmaf(S.s[e >> 4][e & 15], c, -base);
+  if (Masked && partly) {
+    const int seen = only_here(R.last - j0 - 4 * hh);
 #pragma unroll
-    for (int e = 0; e < 32; ++e) S.s[t][e >> 4][e & 15] = __builtin_fmaf(S.s[t][e >> 4][e & 15], c, -base);
-    if (Masked && partly) {
-      const int seen = only_here(R.last[t] - j0 - 4 * hh);
-#pragma unroll
-      for (int e = 0; e < 32; ++e)
-        if (32 * (e >> 4) + 8 * ((e & 15) >> 2) + (e & 3) > seen) S.s[t][e >> 4][e & 15] = kMinusInf;
-    }
-    float m[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      m[i] = fmaxf(fmaxf(S.s[t][i][0], S.s[t][i][1]), S.s[t][i][2]);
-#pragma unroll
-      for (int e = 3; e < 15; e += 2) m[i] = fmaxf(fmaxf(m[i], S.s[t][i][e]), S.s[t][i][e + 1]);
-      m[i] = fmaxf(m[i], S.s[t][i][15]);
-    }
-    mx[t] = max_halves(fmaxf(m[0], m[1]));
-    raise |= mx[t] > kLazy || (R.m[t] == kMinusInf && mx[t] > kMinusInf);
+    for (int e = 0; e < 32; ++e)
+      if (32 * (e >> 4) + 8 * ((e & 15) >> 2) + (e & 3) > seen) S.s[e >> 4][e & 15] = kMinusInf;
   }
-  return __any(raise);
+  float m[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    m[i] = fmaxf(fmaxf(S.s[i][0], S.s[i][1]), S.s[i][2]);
+#pragma unroll
+    for (int e = 3; e < 15; e += 2) m[i] = fmaxf(fmaxf(m[i], S.s[i][e]), S.s[i][e + 1]);
+    m[i] = fmaxf(m[i], S.s[i][15]);
+  }
+  mx = max_halves(fmaxf(m[0], m[1]));
+  return __any(mx > kLazy || (R.m == kMinusInf && mx > kMinusInf));
 }
 
-template <typename T, int D, int CT>
-__device__ __forceinline__ void raise_maximum(Rows<T, D, CT>& R, Scores<CT>& S, const float* mx) {
+template <typename T, int D>
+__device__ __forceinline__ void raise_maximum(Rows<T, D>& R, Scores& S, float mx) {
+  const bool raise = mx > kLazy || (R.m == kMinusInf && mx > kMinusInf);
+  const float d = raise ? mx : 0.f;
+  const float r = !raise ? 1.f : R.m == kMinusInf ? 0.f : exp2_fast(-d);
+  if (raise) R.m = (R.m == kMinusInf ? 0.f : R.m) + d;
+  R.l *= r;
 #pragma unroll
-  for (int t = 0; t < CT; ++t) {
-    const bool raise = mx[t] > kLazy || (R.m[t] == kMinusInf && mx[t] > kMinusInf);
-    const float d = raise ? mx[t] : 0.f;
-    const float r = !raise ? 1.f : R.m[t] == kMinusInf ? 0.f : exp2_fast(-d);
-    if (raise) R.m[t] = (R.m[t] == kMinusInf ? 0.f : R.m[t]) + d;
-    R.l[t] *= r;
+  for (int k = 0; k < D / 32; ++k) R.o[k] *= r;
 #pragma unroll
-    for (int k = 0; k < D / 32; ++k) R.o[t][k] *= r;
-#pragma unroll
-    for (int e = 0; e < 32; ++e) S.s[t][e >> 4][e & 15] -= d;
-  }
+  for (int e = 0; e < 32; ++e) S.s[e >> 4][e & 15] -= d;
 }
 
-template <typename T, int D, int CT>
-__device__ __forceinline__ void weights(Rows<T, D, CT>& R, const Scores<CT>& S, Weights<CT>& W) {
+template <typename T, int D>
+__device__ __forceinline__ void weights(Rows<T, D>& R, const Scores& S, Weights& W) {
+  float sum[4] = {R.l, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int t = 0; t < CT; ++t) {
-    float sum[4] = {R.l[t], 0.f, 0.f, 0.f};
+  for (int w = 0; w < 4; ++w) {
+    float y[8];
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      float y[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        y[e] = exp2_fast(S.s[t][w >> 1][8 * (w & 1) + e]);
-        sum[e & 3] += y[e];                 // (before they are rounded: the sum is an output)
-      }
-      W.p[t][w] = u32x4{T::cvt2(y[0], y[1]), T::cvt2(y[2], y[3]), T::cvt2(y[4], y[5]), T::cvt2(y[6], y[7])};
+    for (int e = 0; e < 8; ++e) {
+      y[e] = exp2_fast(S.s[w >> 1][8 * (w & 1) + e]);
+      sum[e & 3] += y[e];                   // (before they are rounded: the sum is an output)
     }
-    R.l[t] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    W.p[w] = u32x4{T::cvt2(y[0], y[1]), T::cvt2(y[2], y[3]), T::cvt2(y[4], y[5]), T::cvt2(y[6], y[7])};
   }
+  R.l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
 }
 
 // The product with V, 32 columns x 16 keys an operand: transposing reads in
@@ -222,8 +206,8 @@ __device__ __forceinline__ void take_special(u32x4& v) {
 
 // Says whether it met such values (Masked, partly as above; a sum of squares
 // finds them, and very large ones).
-template <bool Masked, typename T, int D, int CT>
-__device__ __forceinline__ bool add_values(Rows<T, D, CT>& R, const Weights<CT>& W, const uint8_t* vt, bool partly, int lane) {
+template <bool Masked, typename T, int D>
+__device__ __forceinline__ bool add_values(Rows<T, D>& R, const Weights& W, const uint8_t* vt, bool partly, int lane) {
   bool special = false;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -243,16 +227,14 @@ __device__ __forceinline__ bool add_values(Rows<T, D, CT>& R, const Weights<CT>&
       }
     }
 #pragma unroll
-    for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-      for (int t = 0; t < CT; ++t) R.o[t][d] = T::mma32(v[d], W.p[t][k], R.o[t][d]);
+    for (int d = 0; d < D / 32; ++d) R.o[d] = T::mma32(v[d], W.p[k], R.o[d]);
   }
   return special;
 }
 
 // Keys j0..j1-1 once more, for their values that are not finite.
-template <typename T, int D, int CT>
-__device__ void add_special(Rows<T, D, CT>& R, const uint8_t* v, int64_t row_bytes, int j0, int j1, int lane) {
+template <typename T, int D>
+__device__ void add_special(Rows<T, D>& R, const uint8_t* v, int64_t row_bytes, int j0, int j1, int lane) {
   const int hh = lane >> 5;
   for (int j = j0; j < j1; ++j) {
     const uint8_t* row = v + j * row_bytes + 8 * hh;
@@ -265,9 +247,7 @@ __device__ void add_special(Rows<T, D, CT>& R, const uint8_t* v, int64_t row_byt
         for (int i = 0; i < 4; ++i) {
           const uint32_t bits = (i & 2 ? w.y : w.x) >> (16 * (i & 1)) & 0xFFFFu;
           const float x = (bits & T::kExpOne) == T::kExpOne ? T::lo(bits) : 0.f;
-#pragma unroll
-          for (int t = 0; t < CT; ++t)
-            if (j <= R.last[t]) R.o[t][d][e + i] += x;
+          if (j <= R.last) R.o[d][e + i] += x;
         }
       }
   }
@@ -288,8 +268,8 @@ struct Keys {
 // the next but one K and of this tile's V start; they have a whole step's
 // time, and there is one barrier a step.  Tiles behind the last come as
 // zeros, so nothing here asks which is the last.
-template <bool First, bool Masked, typename T, int D, int CT>
-__device__ __forceinline__ bool step(Rows<T, D, CT>& R, Scores<CT>& S, Weights<CT>& W, const Keys<D>& K, int t,
+template <bool First, bool Masked, typename T, int D>
+__device__ __forceinline__ bool step(Rows<T, D>& R, Scores& S, Weights& W, const Keys<D>& K, int t,
                                      uint8_t* k_this, uint8_t* k_next, uint8_t* v_this, uint8_t* v_last, int n_whole,
                                      float c, int wave, int lane) {
   const int j0 = t * kTile;
@@ -297,48 +277,45 @@ __device__ __forceinline__ bool step(Rows<T, D, CT>& R, Scores<CT>& S, Weights<C
   __syncthreads();
   K.k.start(j0 + 2 * kTile, K.len, k_this, wave);
   if (!First) K.v.start(j0, K.len, v_this, wave);
-  float mx[CT];
-  const bool raise = exponents<Masked, T, D, CT>(R, S, mx, j0, t >= n_whole, c, lane);
+  float mx;
+  const bool raise = exponents<Masked, T, D>(R, S, mx, j0, t >= n_whole, c, lane);
   bool special = false;
-  if (!First) special = add_values<Masked, T, D, CT>(R, W, v_last, t > n_whole, lane);
+  if (!First) special = add_values<Masked, T, D>(R, W, v_last, t > n_whole, lane);
   if (!First && !Masked) {
     __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) {       // block A: D/8 products, 32 multiplications, 20 maxima
       __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-      __builtin_amdgcn_sched_group_barrier(0x008, CT, 0);
-      __builtin_amdgcn_sched_group_barrier(0x002, (D == 64 ? 7 : 4) * CT, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, D == 64 ? 7 : 4, 0);
     }
   }
-  if (raise) raise_maximum<T, D, CT>(R, S, mx);
-  weights<T, D, CT>(R, S, W);
-  scores<T, D, CT>(R, S, k_next, lane);
+  if (raise) raise_maximum<T, D>(R, S, mx);
+  weights<T, D>(R, S, W);
+  scores<T, D>(R, S, k_next, lane);
   // (the weights are made here, among the products, not where they are used)
 #pragma unroll
-  for (int u = 0; u < CT; ++u)
-#pragma unroll
-    for (int w = 0; w < 4; ++w) asm volatile("" : "+v"(W.p[u][w]));
-#pragma unroll
-  for (int u = 0; u < CT; ++u) asm volatile("" : "+v"(R.l[u]));
+  for (int w = 0; w < 4; ++w) asm volatile("" : "+v"(W.p[w]));
+  asm volatile("" : "+v"(R.l));
   if (!Masked) {
     __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) {       // block B: D/8 products, 32 exponentials, 32 additions, 16 conversions
       __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x008, CT, 0);
-      __builtin_amdgcn_sched_group_barrier(0x402, (D == 64 ? 10 : 5) * CT, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x402, D == 64 ? 10 : 5, 0);
     }
   }
   return special;
 }
 
-// Workgroup: 32*CT*kWaves rows of one sequence and key head (row r = token
+// Workgroup: 32*kWaves rows of one sequence and key head (row r = token
 // r / group, query head r % group of the key head's group, so that the heads
 // that share keys share the staged tiles), all keys they see, tile by tile
 // in two LDS buffers: the next tile is on its way while one is computed.
-template <typename T, int D, int CT>
-__global__ __launch_bounds__(kThreads, CT > 1 || D > 128 ? 1 : D > 64 ? 2 : 3) void prefill_kernel(PrefillArgs a, int tiles) {
-  constexpr int kRowsWg = 32 * CT * kWaves;
+template <typename T, int D>
+__global__ __launch_bounds__(kThreads, D > 128 ? 1 : D > 64 ? 2 : 3) void prefill_kernel(PrefillArgs a, int tiles) {
+  constexpr int kRowsWg = 32 * kWaves;
   constexpr int kBytes = kTile * D * 2;
   __shared__ __attribute__((aligned(1024))) uint8_t k0[kBytes], v0[kBytes], k1[kBytes], v1[kBytes];
 
@@ -361,32 +338,28 @@ __global__ __launch_bounds__(kThreads, CT > 1 || D > 128 ? 1 : D > 64 ? 2 : 3) v
   if (qt < 0) return;                       // the whole workgroup
   const int group = a.Hq / a.Hk;
   const Seq sq = seq_rows(a.cu_q, a.per_q, a.Tq, b), sk = seq_rows(a.cu_k, a.per_k, a.Tk, b);
-  const int rows = sq.n * group, r0 = qt * kRowsWg;
+  const int rows = min(sq.n, a.max_q) * group, r0 = qt * kRowsWg;
   if (r0 >= rows) return;                   // the whole workgroup
 
   const int col = lane & 31, hh = lane >> 5;
   const int shift = sk.n - sq.n;            // key index of query row 0's own position
-  const int w0 = r0 + wave * 32 * CT;       // this wave's first row
-  Rows<T, D, CT> R;
+  Rows<T, D> R;
+  const int r = r0 + wave * 32 + col;       // this lane's row
+  const int token = r / group, h = hk * group + r % group;
+  R.last = r >= rows ? -1 : a.causal ? min(shift + token, sk.n - 1) : sk.n - 1;
+  R.m = kMinusInf;
+  R.l = 0.f;
 #pragma unroll
-  for (int t = 0; t < CT; ++t) {
-    const int r = w0 + 32 * t + col;
-    const int i = r / group, h = hk * group + r % group;
-    R.last[t] = r >= rows ? -1 : a.causal ? min(shift + i, sk.n - 1) : sk.n - 1;
-    R.m[t] = kMinusInf;
-    R.l[t] = 0.f;
+  for (int k = 0; k < D / 16; ++k) R.q[k] = u32x4{0, 0, 0, 0};
+  if (r < rows) {
+    const uint16_t* p = (const uint16_t*)a.q + (int64_t)(sq.row0 + token) * a.qs + (int64_t)h * D + 8 * hh;
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k) R.q[t][k] = u32x4{0, 0, 0, 0};
-    if (r < rows) {
-      const uint16_t* p = (const uint16_t*)a.q + (int64_t)(sq.row0 + i) * a.qs + (int64_t)h * D + 8 * hh;
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) R.q[t][k] = *reinterpret_cast<const u32x4*>(p + 16 * k);
-    }
-#pragma unroll
-    for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) R.o[t][d][e] = 0.f;
+    for (int k = 0; k < D / 16; ++k) R.q[k] = *reinterpret_cast<const u32x4*>(p + 16 * k);
   }
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) R.o[d][e] = 0.f;
   // tiles that all of the workgroup's rows see whole, and that any row sees
   const int last_row = min(r0 + kRowsWg, rows) - 1;
   const int all = a.causal ? min(shift + r0 / group, sk.n - 1) : sk.n - 1;
@@ -407,59 +380,55 @@ __global__ __launch_bounds__(kThreads, CT > 1 || D > 128 ? 1 : D > 64 ? 2 : 3) v
     K.v.start(t0 * kTile, sk.n, v0, wave);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    Scores<CT> S;
-    Weights<CT> W;
-    scores<T, D, CT>(R, S, k0, lane);
-    step<true, true, T, D, CT>(R, S, W, K, t0, k0, k1, v0, v1, n_whole, a.c, wave, lane);
+    Scores S;
+    Weights W;
+    scores<T, D>(R, S, k0, lane);
+    step<true, true, T, D>(R, S, W, K, t0, k0, k1, v0, v1, n_whole, a.c, wave, lane);
     int t = t0 + 1;
     const int t_whole = min(n_whole, t1);
     for (; t + 2 <= t_whole; t += 2) {
-      step<false, false, T, D, CT>(R, S, W, K, t, k1, k0, v1, v0, n_whole, a.c, wave, lane);
-      step<false, false, T, D, CT>(R, S, W, K, t + 1, k0, k1, v0, v1, n_whole, a.c, wave, lane);
+      step<false, false, T, D>(R, S, W, K, t, k1, k0, v1, v0, n_whole, a.c, wave, lane);
+      step<false, false, T, D>(R, S, W, K, t + 1, k0, k1, v0, v1, n_whole, a.c, wave, lane);
     }
     const int masked_from = t - 1;          // (its V is still to come)
     bool special = false;
     for (; t < t1; t += 2) {
-      special |= step<false, true, T, D, CT>(R, S, W, K, t, k1, k0, v1, v0, n_whole, a.c, wave, lane);
+      special |= step<false, true, T, D>(R, S, W, K, t, k1, k0, v1, v0, n_whole, a.c, wave, lane);
       if (t + 1 >= t1) break;
-      special |= step<false, true, T, D, CT>(R, S, W, K, t + 1, k0, k1, v0, v1, n_whole, a.c, wave, lane);
+      special |= step<false, true, T, D>(R, S, W, K, t + 1, k0, k1, v0, v1, n_whole, a.c, wave, lane);
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    special |= add_values<true, T, D, CT>(R, W, (t1 - t0) & 1 ? v0 : v1, t1 > n_whole, lane);
+    special |= add_values<true, T, D>(R, W, (t1 - t0) & 1 ? v0 : v1, t1 > n_whole, lane);
     if (special)
-      add_special<T, D, CT>(R, K.v.base, K.v.row_bytes, masked_from * kTile, min(t1 * kTile, sk.n), lane);
+      add_special<T, D>(R, K.v.base, K.v.row_bytes, masked_from * kTile, min(t1 * kTile, sk.n), lane);
   }
-#pragma unroll
-  for (int t = 0; t < CT; ++t) {
-    const float sum = sum_halves(R.l[t]);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int r = w0 + 32 * t + col;
-    if (r >= rows) continue;
-    const int64_t row = sq.row0 + r / group, h = hk * group + r % group;
-    if (a.split.n > 1) {
-      const int64_t at = (blockIdx.y * (int64_t)a.Tq + row) * a.Hq + h;
-      float* p = a.split.o + at * D + 4 * hh;
-#pragma unroll
-      for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-        for (int e = 0; e < 16; e += 4)
-          *reinterpret_cast<f32x4*>(p + 32 * d + 2 * e) = f32x4{R.o[t][d][e], R.o[t][d][e + 1], R.o[t][d][e + 2], R.o[t][d][e + 3]};
-      if (hh == 0) *reinterpret_cast<float2*>(a.split.ml + 2 * at) = make_float2(R.m[t], sum);
-      continue;
-    }
-    uint16_t* p = (uint16_t*)a.out + row * a.os + h * D + 4 * hh;
+  const float sum = sum_halves(R.l);
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  if (r >= rows) return;
+  const int64_t row = sq.row0 + token;
+  if (a.split.n > 1) {
+    const int64_t at = (blockIdx.y * (int64_t)a.Tq + row) * a.Hq + h;
+    float* p = a.split.o + at * D + 4 * hh;
 #pragma unroll
     for (int d = 0; d < D / 32; ++d)
 #pragma unroll
-      for (int e = 0; e < 16; e += 4) {
-        u32x2 w;
-        w.x = T::cvt2(R.o[t][d][e] * inv, R.o[t][d][e + 1] * inv);
-        w.y = T::cvt2(R.o[t][d][e + 2] * inv, R.o[t][d][e + 3] * inv);
-        *reinterpret_cast<u32x2*>(p + 32 * d + 2 * e) = w;
-      }
-    if (hh == 0 && a.lse) a.lse[row * a.Hq + h] = (R.m[t] + __builtin_amdgcn_logf(sum)) * kLn2;
+      for (int e = 0; e < 16; e += 4)
+        *reinterpret_cast<f32x4*>(p + 32 * d + 2 * e) = f32x4{R.o[d][e], R.o[d][e + 1], R.o[d][e + 2], R.o[d][e + 3]};
+    if (hh == 0) *reinterpret_cast<float2*>(a.split.ml + 2 * at) = make_float2(R.m, sum);
+    return;
   }
+  uint16_t* p = (uint16_t*)a.out + row * a.os + (int64_t)h * D + 4 * hh;
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) {
+      u32x2 w;
+      w.x = T::cvt2(R.o[d][e] * inv, R.o[d][e + 1] * inv);
+      w.y = T::cvt2(R.o[d][e + 2] * inv, R.o[d][e + 3] * inv);
+      *reinterpret_cast<u32x2*>(p + 32 * d + 2 * e) = w;
+    }
+  if (hh == 0 && a.lse) a.lse[row * a.Hq + h] = (R.m + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
 // Joins the parts of one row and head: a wave each.
@@ -478,7 +447,7 @@ hipError_t go(const PrefillArgs& a, hipStream_t s) {
   const int64_t rows = (int64_t)a.max_q * (a.Hq / a.Hk);
   const int tiles = (int)((rows + 32 * kWaves - 1) / (32 * kWaves));
   const int64_t per_seq = ((int64_t)tiles * a.Hk + 7) / 8 * 8;   // whole rounds of the XCDs
-  hipLaunchKernelGGL((prefill_kernel<T, D, 1>), dim3((unsigned)(per_seq * a.B), (unsigned)a.split.n), dim3(kThreads), 0, s, a, tiles);
+  hipLaunchKernelGGL((prefill_kernel<T, D>), dim3((unsigned)(per_seq * a.B), (unsigned)a.split.n), dim3(kThreads), 0, s, a, tiles);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.split.n == 1) return e;
   hipLaunchKernelGGL((join_parts_kernel<T, D>), dim3((unsigned)((int64_t)a.B * a.max_q), (unsigned)((a.Hq + kWaves - 1) / kWaves)),

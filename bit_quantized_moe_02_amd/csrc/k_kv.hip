@@ -79,7 +79,7 @@ __device__ __forceinline__ u32x4 pack8(const float* x) {
 
 __device__ __forceinline__ u32x4 ldg16(const uint16_t* p) { return *reinterpret_cast<const u32x4*>(p); }
 
-// Scales and codes of a block of one head that an append has to know.
+// Index in the cache of block `blk` of head hk, on page `page`.
 __device__ __forceinline__ int64_t block_in(const KvArgs& a, int page, int blk, int hk) {
   return ((((int64_t)page * a.Hk + hk) << a.lb) + (blk & ((1 << a.lb) - 1)));
 }

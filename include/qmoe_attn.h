@@ -76,8 +76,9 @@ size_t moe_kv_scale_bytes(int32_t n_pages, int32_t page_tokens, int32_t kv_heads
  *               this step's rows included.
  *   cu_rows     device int32 [batch+1]: sequence b has rows cu_rows[b] to
  *               cu_rows[b+1]-1; NULL: rows/batch each.
- *   max_new     at least the largest number of rows of one sequence (rows
- *               past it are not processed).
+ *   max_new     at least the largest number of rows of one sequence
+ *               (attention leaves rows past it as they are, appending and
+ *               reading may).
  * Row i of the n rows of sequence b is position kv_lens[b] - n + i: the
  * step's rows are the sequence's last.  Rows behind cu_rows[batch] are left
  * as they are. */
@@ -174,15 +175,16 @@ size_t moe_attn_decode_workspace_bytes(const moe_kv_cache* cache, const moe_kv_b
  * (codes times scales as rows of the row type; the weights p of one tile
  * rounded to it), 32-bit sums.  Meant for few rows a sequence (1..16 in
  * decoding and draft verification; any number works).  ws: device scratch,
- * no initialization needed; calls that overlap in time need one each. */
+ * no initialization needed; calls that overlap in time need one each.  out
+ * and lse must not overlap the inputs. */
 int moe_attn_decode(const moe_kv_cache* cache, const moe_kv_batch* batch, int dtype, const void* q,
                     int64_t q_stride, int32_t q_heads, float scale, void* out, int64_t out_stride, float* lse,
                     void* ws, size_t ws_bytes, void* stream);
 
 /* Packed prompts: sequence b has query rows cu_q[b]..cu_q[b+1]-1 of rows_q
  * and key rows cu_k[b]..cu_k[b+1]-1 of rows_k (device int32 [batch+1];
- * NULL: rows/batch each). max_q: at least the largest number of query rows
- * of one sequence (rows past it are not processed). */
+ * NULL: rows/batch each).  max_q: at least the largest number of query rows
+ * of one sequence (rows past it are left as they are). */
 typedef struct moe_packed {
   int32_t batch;
   int32_t rows_q;
@@ -203,7 +205,7 @@ size_t moe_attn_prefill_workspace_bytes(const moe_packed* p);
  * place of the cache.  causal != 0: query row i of n sees key rows
  * j <= m - n + i of the sequence's m (aligned at the end: a chunk's rows come
  * last; with n > m the first n - m rows see nothing); else all m.  rows_k may
- * be 0 (k and v are not read then). */
+ * be 0 (k and v are not read then).  out, lse and ws as above. */
 int moe_attn_prefill(const moe_packed* p, int dtype, const void* q, int64_t q_stride, const void* k,
                      int64_t k_stride, const void* v, int64_t v_stride, float scale, int causal, void* out,
                      int64_t out_stride, float* lse, void* ws, size_t ws_bytes, void* stream);

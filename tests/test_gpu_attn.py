@@ -503,6 +503,28 @@ def test_prefill_few_rows_many_keys(q):
     _prefill(q, [1, 2, 0], [700, 5, 40], 2, 1, 256, "bf16", True, rng, "few rows, wide heads")
 
 
+@pytest.mark.parametrize("n_keys", [70, 9000])
+def test_prefill_more_rows_than_max_q(q, n_keys):
+    """A sequence with more rows than max_q says, whole and cut into parts: the first max_q are right, the others untouched."""
+    rng = np.random.default_rng(46)
+    Hk, D, Hq, ns, ms, most = 2, 128, 4, [41, 7], [n_keys, 50], 9
+    qt, qv = rows_in(rng, sum(ns), Hq, D, torch.bfloat16)
+    kt, kv = rows_in(rng, sum(ms), Hk, D, torch.bfloat16)
+    vt, vv = rows_in(rng, sum(ms), Hk, D, torch.bfloat16)
+    need = q.moe_attn_prefill_workspace_bytes(sum(ns), 2, most, sum(ms), Hq, Hk, D)
+    assert (need > 256) == (n_keys == 9000)
+    ws = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    out, lse = torch.full_like(qt, 9.0), torch.full((sum(ns), Hq), 9.0, device="cuda")
+    q.moe_attn_prefill(qt, kt, vt, i32(cu_of(ns)), i32(cu_of(ms)), most, out, ws[:need], 0.09, True, lse)
+    assert torch.all(ws[need:] == 0x5A)
+    assert torch.all(out[most:41] == 9.0) and torch.all(lse[most:41] == 9.0)
+    for b, (rows, keys) in enumerate(((slice(0, most), slice(0, n_keys)), (slice(41, 48), slice(n_keys, n_keys + 50)))):
+        seen = np.arange(ms[b])[None] <= (ms[b] - ns[b] + np.arange(rows.stop - rows.start))[:, None]
+        K, V = kv[keys], vv[keys]
+        ref, rl, mag, smag = A.attention(qv[rows], K, V, seen, 0.09)
+        check_attention(out[rows], lse[rows], ref, rl, *attention_bounds(torch.bfloat16, D, V, ref, mag, smag, ms[b]), f"sequence {b}")
+
+
 def test_prefill_no_keys_at_all(q):
     x = torch.zeros((3, 2, 64), dtype=torch.bfloat16, device="cuda")
     k = torch.zeros((0, 2, 64), dtype=torch.bfloat16, device="cuda")
