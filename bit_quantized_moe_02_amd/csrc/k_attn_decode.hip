@@ -14,6 +14,7 @@ constexpr int kWaves = 4;                   // of a workgroup that takes a range
 constexpr int kShortWaves = 8;              // of one that takes a whole short context
 constexpr int kThreads = 256;               // of the join
 constexpr int kStep = 32;                   // positions a wave takes at once: two blocks
+constexpr float kLazy = 8.f;                // how far a score may exceed the running maximum, in powers of 2
 
 // Shares.  The contexts of all sequences, in steps of 32 positions one after
 // the other (a sequence with rows and no context counts as one step), are
@@ -132,7 +133,7 @@ __device__ __forceinline__ u32x4 load_codes(const uint8_t* p) {
 }
 
 // Workgroups of a compute unit that the registers leave room for.
-constexpr int occupancy(int dim, int nr) { return nr == 1 && dim <= 128 ? 3 : nr == 2 && dim <= 128 ? 2 : 1; }
+constexpr int occupancy(int dim, int nr) { return dim > 128 ? 1 : nr == 1 ? 3 : 2; }
 
 // Workgroup: one range, one key head, up to 16*NR rows of each of its
 // sequences (row r = token r / group, query head r % group of the key head's
@@ -309,22 +310,31 @@ __global__ __launch_bounds__(64 * (Short ? kShortWaves : kWaves), Short ? 1 : oc
         u32x4 pk[NR];
 #pragma unroll
         for (int t = 0; t < NR; ++t) {
+          // powers of two under the running maximum, which is raised only when a
+          // score exceeds it by 2^8 (or a row has none yet): weights up to 2^8
+          // cost no precision, and the sums are hardly ever rescaled
+          const float base = m[t] == kMinusInf ? 0.f : m[t];
           float x[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = sc[t][j >> 2][j & 3] * a.c;
-          float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-          mx = fmaxf(m[t], max_rows4(mx));
-          if (__any(mx > m[t])) {
-            const float r = m[t] == kMinusInf ? 0.f : exp2_fast(m[t] - mx);
+          for (int j = 0; j < 8; ++j) x[j] = __builtin_fmaf(sc[t][j >> 2][j & 3], a.c, -base);
+          float mx = fmaxf(fmaxf(x[0], x[1]), x[2]);
+          mx = fmaxf(fmaxf(mx, x[3]), x[4]);
+          mx = fmaxf(fmaxf(mx, x[5]), x[6]);
+          mx = max_rows4(fmaxf(mx, x[7]));
+          const bool raise = mx > kLazy || (m[t] == kMinusInf && mx > kMinusInf);
+          if (__any(raise)) {
+            const float d = raise ? mx : 0.f;
+            const float r = !raise ? 1.f : m[t] == kMinusInf ? 0.f : exp2_fast(-d);
+            if (raise) m[t] = base + d;
             l[t] *= r;
 #pragma unroll
-            for (int d = 0; d < kDt; ++d) o[t][d] *= r;
-            m[t] = mx;
+            for (int k = 0; k < kDt; ++k) o[t][k] *= r;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] -= d;
           }
-          const float base = mx == kMinusInf ? 0.f : mx;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            x[j] = exp2_fast(x[j] - base);
+            x[j] = exp2_fast(x[j]);
             l[t] += x[j];
           }
           pk[t].x = T::cvt2(x[0], x[1]);
@@ -500,25 +510,27 @@ __global__ __launch_bounds__(kThreads) void join_few_kernel(DecodeArgs a) {
 
 int rows_of(const KvArgs& kv, int Hq) { return kv.max_new * (Hq / kv.Hk); }
 
-// Row tiles of 16 a workgroup takes: as many as the step needs, up to 4 (64
-// rows; 2 for the widest heads), so that the context is read once for all.
-int row_tiles(const KvArgs& kv, int Hq) {
-  const int rows = rows_of(kv, Hq);
-  return rows <= 16 ? 1 : rows <= 32 || kv.D > 128 ? 2 : 4;
-}
+// Row tiles of 16 a workgroup takes: two serve up to 32 rows with one read of
+// the codes and leave room for two workgroups a compute unit.  More rows go to
+// neighbours in the grid's third dimension, which find the codes in the
+// caches: 8 contexts of 16384, 32 tokens each, 32 + 8 heads of 64, 91 us (one
+// tile a workgroup 116, four, at one workgroup a compute unit, 110); heads of
+// 128 133 us (249, 131).
+int row_tiles(const KvArgs& kv, int Hq) { return rows_of(kv, Hq) <= 16 ? 1 : 2; }
 
-// Whether contexts (by the page table) are taken whole: four rounds of a
-// workgroup's waves; the join would cost more than the rounds it saves.  The
-// widest row tiles do not fit the registers of 8 waves.
+// Whether contexts (by the page table) are taken whole: up to six rounds of a
+// workgroup's waves, where even one sequence alone loses nothing by it (1536
+// positions, 32 + 8 heads of 128: 9.2 us, parts and join 9.4; 16 sequences
+// 11.5 and 14.1).  Two tiles of the widest rows do not fit the registers of 8
+// waves.
 bool is_short(const KvArgs& kv, int nr) {
-  return kv.max_len <= 4 * kShortWaves * kStep && nr * kv.D <= 256 && kv.B <= 65535;
+  return kv.max_len <= 6 * kShortWaves * kStep && nr * kv.D <= 256 && kv.B <= 65535;
 }
 
 template <typename T, int D>
 void (*pick(int nr, bool shrt))(DecodeArgs) {
   if (nr == 1) return shrt ? decode_kernel<T, D, 1, true> : decode_kernel<T, D, 1, false>;
-  if (nr == 2) return shrt ? decode_kernel<T, D, (D > 128 ? 1 : 2), true> : decode_kernel<T, D, 2, false>;
-  return shrt ? decode_kernel<T, D, (D > 64 ? 1 : 4), true> : decode_kernel<T, D, (D > 128 ? 2 : 4), false>;
+  return shrt ? decode_kernel<T, D, (D > 128 ? 1 : 2), true> : decode_kernel<T, D, 2, false>;
 }
 
 template <typename T>

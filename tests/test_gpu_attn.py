@@ -270,6 +270,28 @@ def test_decode(q, case, D, dt):
         _decode(q, cache, dev, table, lens, ns, Hq, DT[dt], rng, f"case {case}, uniform", uniform=True)
 
 
+LONG = [  # rows, lengths, page, query heads, key heads: contexts cut into ranges
+    ([1, 1, 1, 1], [3000, 1, 0, 1700], 64, 8, 2),
+    ([4, 1, 0, 5, 2], [2100, 300, 9, 4, 1601], 16, 16, 2),             # two row tiles
+    ([9, 3], [40, 2500], 128, 30, 3),                  # several workgroups of row tiles
+    ([33, 1], [1999, 33], 32, 8, 1),                   # 264 rows of a key head
+]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("case", range(len(DECODE) + len(LONG)))
+def test_decode_ranges(q, case, D, dt):
+    """Page tables wide enough that contexts are cut into ranges, short contexts among them."""
+    ns, lens, page, Hq, Hk = (DECODE + LONG)[case]
+    rng = np.random.default_rng(260 + case)
+    table, n_pages = page_table(rng, lens, page, width=4096 // page)
+    cache = A.Cache(*random_cache(rng, n_pages, page, Hk, D), page, Hk, D)
+    spoil_tails(cache, table, lens)
+    dev = to_device(q, cache)
+    _decode(q, cache, dev, table, lens, ns, Hq, DT[dt], rng, f"case {case}", sigma=2.0, extra=2, pad=8)
+
+
 @pytest.mark.parametrize("width", [1, 40, 4000])
 def test_decode_parts(q, width):
     """One context, page tables of several widths: from one part to one for each 128 positions, most of them empty."""
@@ -296,6 +318,8 @@ def test_decode_special_values(q, dt):
         cache.codes[at[0], h, at[1], part, cache.at[part][pos % 16][d]] = 0xFF if d % 2 else 0x7F
     cache.scales[int(table[0, 1]), 1, 0, 1] = 2.0 ** -12
     _decode(q, cache, to_device(q, cache), table, lens, ns, 4, dt, rng, "special values", sigma=6.0)
+    wide = np.concatenate([table, np.full((2, 200), -1)], axis=1)       # (the same cut into ranges)
+    _decode(q, cache, to_device(q, cache), wide, lens, ns, 4, dt, rng, "special values, ranges", sigma=6.0)
 
 
 @pytest.mark.parametrize("pad", [0, 60])
