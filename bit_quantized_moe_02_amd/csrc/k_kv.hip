@@ -93,6 +93,10 @@ __device__ __forceinline__ int64_t block_in(const KvArgs& a, int page, int blk, 
 // first job's loads are asked for before the angles: with one token it is
 // latency that counts.  (With many, asking for each next job's loads while one
 // is worked on costs registers and 4% at 2048 tokens of 32 + 8 + 8 heads.)
+//
+// Bound by memory: 2048 tokens, heads of 128: 50 MB in 14.4 us, 3.5 TB/s (a
+// copy of 4 GB reaches 4.7).  One token 4.6 us, 64 users of up to 3 tokens 6.4:
+// a launch and three loads that wait for one another (length, page, scale).
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int nb) {
   constexpr int kLanes = D / 16;            // lanes of a row of q or k, 16 columns each
@@ -321,7 +325,9 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int nb) 
 
 // One wave takes one block of one sequence and head: the K codes go out as
 // they lie (a lane holds 8 consecutive columns of one token), the V codes
-// through a transposing tile in LDS.
+// through a transposing tile in LDS, so that rows are written 16 bytes a lane.
+// Bound by memory: 7 contexts of up to 8191, 8 heads of 64: 75 MB in 13.5 us,
+// 5.6 TB/s; 2048 positions, 8 heads of 128 (12.6 MB) in 4.9 us.
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a, int nb) {
   constexpr int kPad = 8;
@@ -400,7 +406,8 @@ hipError_t launch_kv_append(const AppendArgs& a, int dtype, int cus, hipStream_t
   const int64_t items = (int64_t)a.kv.B * nb;
   const int jobs = a.Hq + 2 * a.kv.Hk;
   // few tokens: a wave per job, so that the heads' latencies overlap; many:
-  // a workgroup takes all heads and its angles serve them all
+  // a workgroup takes all heads and its angles serve them all.  4 workgroups a
+  // compute unit: 2048 tokens 18.0 us a call (1: 22.2, 2: 19.0, 3: 18.5, 8: 20.2)
   int64_t gy = (4ll * cus + items - 1) / items;
   const int most = (jobs + kWaves - 1) / kWaves;
   if (gy > most) gy = most;

@@ -618,12 +618,13 @@ def test_prompt_in_chunks_then_steps(q):
             check_attention(out[r], lse[r], ref, rl, *attention_bounds(dt, D, V, ref, mag, smag, lens[b]), f"step, sequence {b}")
 
 
-def test_steps_in_a_graph_on_a_side_stream(q):
+@pytest.mark.parametrize("width", [None, 200])
+def test_steps_in_a_graph_on_a_side_stream(q, width):
     """A captured step (append, attend) replayed with lengths and rows that the program moves on between replays equals
-    the eager steps, to the bit."""
+    the eager steps, to the bit; contexts whole, and cut into ranges (a wide page table)."""
     rng = np.random.default_rng(41)
     Hq, Hk, D, page, dt, steps = 8, 2, 128, 16, torch.bfloat16, 20
-    table, n_pages = page_table(rng, [60, 90], page)
+    table, n_pages = page_table(rng, [60, 90], page, width=width)
     codes, scales = random_cache(rng, n_pages, page, Hk, D)
     rows = torch.from_numpy(rng.standard_normal((steps, 2, Hq + 2 * Hk, D))).to(dt).cuda()
     rope = q.Rope(torch.from_numpy(q.moe_rope_freqs(D)).cuda(), D)
@@ -663,6 +664,62 @@ def test_steps_in_a_graph_on_a_side_stream(q):
     for (a, la), (b, lb) in zip(got["eager"][0], got["graph"][0]):
         assert torch.equal(a, b) and torch.equal(la, lb)
     assert torch.equal(got["eager"][1], got["graph"][1]) and torch.equal(got["eager"][2], got["graph"][2])
+
+
+@pytest.mark.parametrize("width", [None, 400])
+def test_layer_steps_in_a_graph(q, width):
+    """Attention and the routed experts as one captured step: rows in, turned and appended, attended to, and through
+    the layer that takes the heads' outputs as its input.  Replays equal the eager steps to the bit, and the experts'
+    output is the oracle's for the attention's."""
+    import synth
+    from layer_fixture import device_layer, oracle_layer, rel_err
+    wl = synth.WORKLOADS["tiny"]
+    layer = device_layer(wl)
+    rng = np.random.default_rng(47)
+    H, E, k = wl.hidden, wl.n_experts, wl.top_k
+    Hq, Hk, D, page, dt, steps, B = 4, 2, H // 4, 16, torch.bfloat16, 8, 3
+    table, _ = page_table(rng, [40, 60, 300], page, width=width)
+    n_pages = int(table.max()) + 1
+    codes, scales = random_cache(rng, n_pages, page, Hk, D)
+    rows = torch.from_numpy(rng.standard_normal((steps, B, Hq + 2 * Hk, D)) * 3).to(dt).cuda()
+    rope = q.Rope(torch.from_numpy(q.moe_rope_freqs(D)).cuda(), D)
+    got = {}
+    for mode in ("eager", "graph"):
+        dev = to_device(q, A.Cache(codes, scales, page, Hk, D))
+        lens = i32([20, 47, 280])
+        batch = q.KvBatch(i32(table), lens, B)
+        x = torch.zeros_like(rows[0])
+        q_out, out = torch.zeros((B, Hq, D), dtype=dt, device="cuda"), torch.zeros((B, Hq, D), dtype=dt, device="cuda")
+        idx, w = torch.zeros((B, k), dtype=torch.int32, device="cuda"), torch.zeros((B, k), device="cuda")
+        y = torch.zeros((B, H), device="cuda")
+        ws = torch.empty(q.moe_attn_decode_workspace_bytes(dev, batch, Hq), dtype=torch.uint8, device="cuda")
+        lws = torch.empty(q.moe_layer_decode_workspace_bytes(layer.w, B, k), dtype=torch.uint8, device="cuda")
+
+        def step():
+            q.moe_kv_append(dev, batch, x[:, Hq:Hq + Hk], x[:, Hq + Hk:], rope, x[:, :Hq], q_out)
+            q.moe_attn_decode(dev, batch, q_out, out, ws, 0.3)
+            q.moe_layer_decode(layer.w, layer.router, None, out.view(B, H), B, k, idx, w, y, lws)
+
+        graph = None
+        if mode == "graph":
+            graph = torch.cuda.CUDAGraph()
+            torch.cuda.synchronize()
+            with torch.cuda.graph(graph):
+                step()
+        outs = []
+        for i in range(steps):
+            x.copy_(rows[i])
+            lens += 1
+            graph.replay() if graph else step()
+            outs.append([t.clone() for t in (out, idx, w, y)])
+        torch.cuda.synchronize()
+        got[mode] = outs
+    for e, g in zip(got["eager"], got["graph"]):
+        assert all(torch.equal(a, b) for a, b in zip(e, g))
+    for e in got["eager"][::3]:
+        ref, ref_idx, _ = oracle_layer(wl, f64(e[0]).reshape(B, H))
+        assert np.array_equal(e[1].cpu().numpy(), ref_idx)
+        assert rel_err(e[3].cpu().numpy(), ref).max() <= 2e-3
 
 
 def test_two_streams_at_once(q):
