@@ -147,7 +147,8 @@ int moe_rope_freqs(int32_t rot_dim, double base, int rule, double factor, double
  * behind the new tokens are left as they are.
  * Rows at negative positions (more rows than kv_lens) are turned but not
  * appended.  Two sequences of one step must not append to the same page
- * (they may share pages that neither appends to).  q_out, k_out and the
+ * (they may share pages that neither appends to), nor one sequence to a page
+ * that its table names twice.  q_out, k_out and the
  * inputs must not overlap otherwise. */
 int moe_kv_append(const moe_kv_cache* cache, const moe_kv_batch* batch, const moe_rope* rope, int dtype,
                   const void* q, int64_t q_stride, int32_t q_heads, const void* k, int64_t k_stride,

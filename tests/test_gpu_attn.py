@@ -100,6 +100,29 @@ def test_append(q, case, D, dt):
         assert np.all(np.abs(a - b) <= 0.125 * np.maximum(np.abs(a), np.abs(b)) + 2.0 ** -9)
 
 
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("D,rot", [(64, 48), (128, 112), (256, 16), (256, 240)])
+def test_append_turns_part_of_a_head(q, D, rot, inter):
+    """Numbers of turned columns that are no power of two, over a border between blocks of a large page."""
+    rng = np.random.default_rng(48)
+    Hq, Hk, page, dt, lens, ns = 3, 1, 1024, torch.bfloat16, [1030, 18], [20, 5]
+    table, n_pages = page_table(rng, lens, page)
+    codes, scales = random_cache(rng, n_pages, page, Hk, D)
+    dev = to_device(q, A.Cache(codes, scales, page, Hk, D))
+    qt, qv = rows_in(rng, 25, Hq, D, dt)
+    kt, kv = rows_in(rng, 25, Hk, D, dt)
+    vt, _ = rows_in(rng, 25, Hk, D, dt)
+    q_out, k_out = torch.full_like(qt, 3.0), torch.full_like(kt, 3.0)
+    freqs = q.moe_rope_freqs(rot, 500.0, "base", 2.0)
+    q.moe_kv_append(dev, _batch(q, table, lens, ns), kt, vt, q.Rope(torch.from_numpy(freqs).cuda(), rot, inter), qt, q_out, k_out)
+    for x, got in ((qv, f64(q_out)), (kv, f64(k_out))):
+        for b, rows in enumerate((slice(0, 20), slice(20, 25))):
+            want = A.rotate(x[rows], np.arange(lens[b] - ns[b], lens[b]), freqs, inter)
+            tol = half_step(dt) * np.abs(want) + 2.0 ** -20 * 2 * np.abs(x[rows]).max()
+            assert np.all(np.abs(got[rows] - want) <= tol), np.abs(got[rows] - want).max()
+            assert np.array_equal(got[rows][:, :, rot:], x[rows][:, :, rot:])
+
+
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
 def test_append_token_by_token_equals_oracle(q, dt):
     """40 single-token steps whose values grow and shrink, V and unturned K: every byte equal, the growth of a block's
@@ -525,6 +548,44 @@ def test_prefill_few_rows_many_keys(q):
     _prefill(q, [3, 20], [2500, 3333], 4, 2, 128, "bf16", True, rng, "few rows", sigma=2.0)
     _prefill(q, [9], [2049], 2, 2, 64, "fp16", False, rng, "few rows, narrow")
     _prefill(q, [1, 2, 0], [700, 5, 40], 2, 1, 256, "bf16", True, rng, "few rows, wide heads")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_prefill_parts(q, D, dt):
+    """Keys cut into parts: of unequal contexts, so that a sequence's last parts have no tiles, with empty sequences."""
+    rng = np.random.default_rng(49)
+    Hq, Hk, ns, ms = 4, 1, [5, 0, 40], [3500, 700, 90]
+    assert q.moe_attn_prefill_workspace_bytes(45, 3, 40, sum(ms), Hq, Hk, D) > 256
+    _prefill(q, ns, ms, Hq, Hk, D, dt, True, rng, "parts", sigma=2.0)
+    _prefill(q, ns, ms, Hq, Hk, D, dt, False, rng, "parts, all keys", sigma=2.0, pad=8)
+
+
+@pytest.mark.parametrize("Tk", [300, 6000])
+def test_prefill_in_a_graph(q, Tk):
+    """A captured call, whole and cut into parts, replayed with other rows and another cut into sequences: the eager
+    call's bits."""
+    rng = np.random.default_rng(50)
+    Hq, Hk, D, Tq, dt = 4, 2, 128, 60, torch.bfloat16
+    xs = [[rows_in(rng, n, h, D, dt)[0] for n, h in ((Tq, Hq), (Tk, Hk), (Tk, Hk))] for _ in range(4)]
+    cus = [(i32([0, a, Tq]), i32([0, b, Tk])) for a, b in ((30, Tk // 2), (1, Tk - 7), (59, 3), (20, Tk // 3))]
+    ws = [torch.empty(q.moe_attn_prefill_workspace_bytes(Tq, 2, Tq, Tk, Hq, Hk, D), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    assert (ws[0].numel() > 256) == (Tk == 6000)
+    x, cu = [t.clone() for t in xs[0]], [t.clone() for t in cus[0]]
+    out, lse = torch.zeros((Tq, Hq, D), dtype=dt, device="cuda"), torch.zeros((Tq, Hq), device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        q.moe_attn_prefill(*x, *cu, Tq, out, ws[0], 0.09, True, lse)
+    for i in range(12):
+        for dst, src in zip(x + cu, xs[i % 4] + list(cus[i % 4])):
+            dst.copy_(src)
+        graph.replay()
+        o, l = torch.zeros_like(out), torch.zeros_like(lse)
+        q.moe_attn_prefill(*xs[i % 4], *cus[i % 4], Tq, o, ws[1], 0.09, True, l)
+        if i % 3 == 2:
+            torch.cuda.synchronize()
+        assert torch.equal(o, out) and torch.equal(l, lse)
 
 
 @pytest.mark.parametrize("n_keys", [70, 9000])
