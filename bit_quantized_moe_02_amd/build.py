@@ -1,4 +1,5 @@
-"""Builds libqmoe.so in this package directory (gfx950).
+"""Builds libqmoe.so (gfx950) and _attn.so, the attention calls' tensor
+arguments from Python, in this package directory.
 
 The host translation unit (quantizer / packer, no HIP) is compiled by the
 host C++ compiler with -ffp-contract=off so its fp64 quantization decisions
@@ -9,10 +10,12 @@ compiled by hipcc for gfx950 with packed fp32 instructions disabled.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +24,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libqmoe.so")
+PY_ATTN = os.path.join(HERE, "_attn.so")
 
 ARCH = os.environ.get("QMOE_ARCH", "gfx950")
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
@@ -69,7 +73,18 @@ def build(verbose: bool = False) -> str:
     tmp = LIB + ".tmp"
     _run([HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", "-o", tmp] + objs + ["-lpthread"])
     os.replace(tmp, LIB)
+    build_py_attn()
     return LIB
+
+
+def build_py_attn() -> str:
+    """Compiles the Python module that hands the attention calls' tensors to the library (host code only)."""
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    _run([CXX, "-O2", "-fPIC", "-std=c++17", "-Wall", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+          "-I", os.path.join(torch_dir, "include"), "-shared", os.path.join(CSRC, "py_attn.cpp"), "-o", PY_ATTN + ".tmp",
+          "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"])
+    os.replace(PY_ATTN + ".tmp", PY_ATTN)
+    return PY_ATTN
 
 
 # Host-code sanitizer build: AddressSanitizer and UndefinedBehaviorSanitizer

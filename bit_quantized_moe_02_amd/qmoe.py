@@ -5,17 +5,21 @@ becomes a QmoeError carrying moe_last_error().  Every computation happens in
 the library's kernels or its host quantizer.
 
 Import torch before this module (the library then shares torch's HIP
-runtime); a missing libqmoe.so raises at import time.
+runtime); a missing libqmoe.so or _attn.so raises at import time.
 """
 from __future__ import annotations
 
 import ctypes
 import os
-import struct
 
 import numpy as np
 
 import torch
+
+try:
+    from . import _attn
+except ImportError as e:
+    raise ImportError("_attn.so is not built; run `python -m bit_quantized_moe_02_amd.build`") from e
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # QMOE_LIB names another build of the same library (the host-sanitizer build
@@ -475,9 +479,9 @@ class ExpertCache:
 
 
 _DTYPE = {torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16}
-_PACKED = struct.Struct("@4i2P3i0P")        # struct moe_packed
-assert _PACKED.size == ctypes.sizeof(MoePacked)
 
+_attn.use(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
+            for f in ("moe_kv_append", "moe_kv_read", "moe_attn_decode", "moe_attn_prefill")))
 
 # index of the current device, where the library launches
 _device = torch._C._cuda_getDevice
@@ -488,43 +492,38 @@ def _here(t, name, dev):
         raise ValueError(f"{name} is on {t.device}, not on the current device")
 
 
-def _rows(t, name, heads, dim, n, dtype, dev):
-    """(address, row stride) of a row tensor [>= n, heads, dim] of `dtype` on device `dev`, its heads back to back."""
-    try:
-        (r, h, d), stride = t.shape, t.stride()
-        if (h == heads and d == dim and r >= n and t.dtype is dtype and t.get_device() == dev and stride[2] == 1 and
-                (stride[1] == dim or h == 1)):
-            return t.data_ptr(), stride[0] if r > 1 else h * d
-    except (AttributeError, ValueError):
-        pass
-    # what of it was wrong
+def _look_rows(t, name, heads, dim, n, dtype, dev):
+    """Raises unless t is a row tensor [>= n, heads, dim] of `dtype` on device `dev`, its heads back to back."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.dtype not in _DTYPE or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype if dtype in _DTYPE else 'torch.bfloat16 or torch.float16'}, not {t.dtype}")
     if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or t.shape[0] < n:
         raise ValueError(f"{name} has shape {tuple(t.shape)}; the call needs [{n}, {heads}, {dim}]")
     _here(t, name, dev)
-    raise ValueError(f"{name}'s heads must lie back to back")
+    if t.layout != torch.strided or t.stride(2) != 1 or (t.stride(1) != dim and heads != 1):
+        raise ValueError(f"{name}'s heads must lie back to back")
 
 
-def _type(t, name):
-    """Library code of a row tensor's type."""
-    code = _DTYPE.get(getattr(t, "dtype", None))
-    if code is None or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor of torch.bfloat16 or torch.float16")
-    return code
+def _look_vec(t, name, dtype, n, dev, optional=False):
+    """Raises unless t is a contiguous tensor of at least n elements of `dtype` on device `dev`."""
+    if _dev(t, name, dtype, n, optional) is not None:
+        _here(t, name, dev)
 
 
-def _vec(t, name, dtype, n, dev):
-    """Address of a contiguous tensor of at least n elements of `dtype` on device `dev`."""
-    try:
-        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.numel() >= n:
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    _dev(t, name, dtype, n)                 # raises, unless only the device is wrong
-    _here(t, name, dev)
+def _refused(rc, rows, vecs=()):
+    """Raises what is wrong with a call: the library's error, or the tensor that is not what the call needs."""
+    if rc > 0:
+        _check(rc)
+    for r in rows:
+        _look_rows(*r)
+    for v in vecs:
+        _look_vec(*v)
+    raise ValueError("an argument is out of range")
+
+
+def _heads(t):
+    return t.shape[1] if isinstance(t, torch.Tensor) and t.dim() == 3 else 0
 
 
 def _stream_on(stream, dev):
@@ -570,7 +569,7 @@ class KvCache:
                             _dev(scales, "scales", torch.float32, ns // 4))
         self.device = codes.get_device()
         _here(scales, "scales", self.device)
-        self.ref = ctypes.byref(self.c)
+        self.ref, self.at = ctypes.byref(self.c), ctypes.addressof(self.c)
 
 
 class KvBatch:
@@ -598,7 +597,7 @@ class KvBatch:
         for t, name in ((kv_lens, "kv_lens"), (cu_rows, "cu_rows")):
             if t is not None:
                 _here(t, name, self.device)
-        self.ref = ctypes.byref(self.c)
+        self.ref, self.at = ctypes.byref(self.c), ctypes.addressof(self.c)
 
 
 class Rope:
@@ -609,7 +608,7 @@ class Rope:
         self.c = MoeRope(rot_dim, int(bool(interleaved)), scale,
                          _dev(freqs, "freqs", torch.float64, rot_dim // 2, optional=rot_dim == 0))
         self.device = None if freqs is None else freqs.get_device()
-        self.ref = ctypes.byref(self.c)
+        self.ref, self.at = ctypes.byref(self.c), ctypes.addressof(self.c)
 
 
 def _step(cache, batch):
@@ -623,36 +622,28 @@ def _step(cache, batch):
 def moe_kv_append(cache, batch, k, v, rope=None, q=None, q_out=None, k_out=None, stream=None):
     """k, v (and q) [rows, heads, head_dim], any row stride; q turned into q_out (may be q), k_out (may be k or None)."""
     H, D, n = cache.kv_heads, cache.head_dim, batch.rows
-    dev, code, dt = _step(cache, batch), _type(k, "k"), k.dtype
+    dev = _step(cache, batch)
     if rope is not None and rope.device not in (None, dev):
         raise ValueError(f"rope is on device {rope.device}, the current one is {dev}")
-    kp, ks = _rows(k, "k", H, D, n, dt, dev)
-    vp, vs = _rows(v, "v", H, D, n, dt, dev)
-    qp = qop = kop = None
-    qs = hq = qos = kos = 0
-    if q is not None:
-        hq = q.shape[1] if q.dim() == 3 else 0
-        qp, qs = _rows(q, "q", hq, D, n, dt, dev)
-        qop, qos = _rows(q_out, "q_out", hq, D, n, dt, dev)
-    elif q_out is not None:
+    if q is None and q_out is not None:
         raise ValueError("q_out without q")
-    if k_out is not None:
-        kop, kos = _rows(k_out, "k_out", H, D, n, dt, dev)
-    rc = lib.moe_kv_append(cache.ref, batch.ref, rope.ref if rope is not None else None, code, qp, qs, hq, kp, ks, vp, vs,
-                           qop, qos, kop, kos, _stream_on(stream, dev))
+    rc = _attn.append(cache.at, batch.at, 0 if rope is None else rope.at, H, D, n, dev, _stream_on(stream, dev), k, v, q, q_out,
+                      k_out)
     if rc:
-        _check(rc)
+        dt, hq = getattr(k, "dtype", None), _heads(q)
+        _refused(rc, [(k, "k", H, D, n, dt, dev), (v, "v", H, D, n, dt, dev)] +
+                 ([] if q is None else [(q, "q", hq, D, n, dt, dev), (q_out, "q_out", hq, D, n, dt, dev)]) +
+                 ([] if k_out is None else [(k_out, "k_out", H, D, n, dt, dev)]))
 
 
 def moe_kv_read(cache, batch, k_out, v_out, stream=None):
     """Rows of the batch's last positions into k_out, v_out [rows, kv_heads, head_dim]."""
     H, D, n = cache.kv_heads, cache.head_dim, batch.rows
-    dev, code, dt = _step(cache, batch), _type(k_out, "k_out"), k_out.dtype
-    kp, ks = _rows(k_out, "k_out", H, D, n, dt, dev)
-    vp, vs = _rows(v_out, "v_out", H, D, n, dt, dev)
-    rc = lib.moe_kv_read(cache.ref, batch.ref, code, kp, ks, vp, vs, _stream_on(stream, dev))
+    dev = _step(cache, batch)
+    rc = _attn.read(cache.at, batch.at, H, D, n, dev, _stream_on(stream, dev), k_out, v_out)
     if rc:
-        _check(rc)
+        dt = getattr(k_out, "dtype", None)
+        _refused(rc, [(k_out, "k_out", H, D, n, dt, dev), (v_out, "v_out", H, D, n, dt, dev)])
 
 
 def moe_attn_decode_workspace_bytes(cache, batch, q_heads: int) -> int:
@@ -662,15 +653,12 @@ def moe_attn_decode_workspace_bytes(cache, batch, q_heads: int) -> int:
 def moe_attn_decode(cache, batch, q, out, ws, scale, lse=None, stream=None):
     """q, out [rows, q_heads, head_dim]; lse fp32 [rows, q_heads] or None."""
     D, n = cache.head_dim, batch.rows
-    dev, code, dt = _step(cache, batch), _type(q, "q"), q.dtype
-    hq = q.shape[1] if q.dim() == 3 else 0
-    qp, qs = _rows(q, "q", hq, D, n, dt, dev)
-    op, os_ = _rows(out, "out", hq, D, n, dt, dev)
-    rc = lib.moe_attn_decode(cache.ref, batch.ref, code, qp, qs, hq, scale, op, os_,
-                             None if lse is None else _vec(lse, "lse", torch.float32, n * hq, dev),
-                             _vec(ws, "ws", torch.uint8, 0, dev), ws.numel(), _stream_on(stream, dev))
+    dev = _step(cache, batch)
+    rc = _attn.decode(cache.at, batch.at, D, n, dev, _stream_on(stream, dev), q, out, ws, scale, lse)
     if rc:
-        _check(rc)
+        dt, hq = getattr(q, "dtype", None), _heads(q)
+        _refused(rc, [(q, "q", hq, D, n, dt, dev), (out, "out", hq, D, n, dt, dev)],
+                 [(ws, "ws", torch.uint8, 0, dev), (lse, "lse", torch.float32, n * hq, dev, True)])
 
 
 def moe_attn_prefill_workspace_bytes(rows_q: int, batch: int, max_q: int, rows_k: int, q_heads: int, kv_heads: int,
@@ -682,20 +670,16 @@ def moe_attn_prefill_workspace_bytes(rows_q: int, batch: int, max_q: int, rows_k
 
 def moe_attn_prefill(q, k, v, cu_q, cu_k, max_q, out, ws, scale, causal=True, lse=None, stream=None):
     """q, out [rows_q, q_heads, head_dim]; k, v [rows_k, kv_heads, head_dim]; cu_q, cu_k int32 [batch+1]."""
-    code, dt, dev = _type(q, "q"), q.dtype, _device()
-    if q.dim() != 3 or _type(k, "k") != code or k.dim() != 3:
-        raise ValueError("q and k must be [rows, heads, head_dim] of one type")
-    nq, hq, D = q.shape
-    nk, hk = k.shape[:2]
-    qp, qs = _rows(q, "q", hq, D, nq, dt, dev)
-    kp, ks = _rows(k, "k", hk, D, nk, dt, dev)
-    vp, vs = _rows(v, "v", hk, D, nk, dt, dev)
-    op, os_ = _rows(out, "out", hq, D, nq, dt, dev)
-    cq = _vec(cu_q, "cu_q", torch.int32, 2, dev)
-    batch = cu_q.numel() - 1
-    p = _PACKED.pack(batch, nq, nk, max_q, cq, _vec(cu_k, "cu_k", torch.int32, batch + 1, dev), hq, hk, D)
-    rc = lib.moe_attn_prefill(p, code, qp, qs, kp, ks, vp, vs, scale, 1 if causal else 0, op, os_,
-                              None if lse is None else _vec(lse, "lse", torch.float32, nq * hq, dev),
-                              _vec(ws, "ws", torch.uint8, 0, dev), ws.numel(), _stream_on(stream, dev))
+    if not getattr(q, "is_cuda", False):
+        raise ValueError("q must be a CUDA tensor")
+    dev = _device()
+    rc = _attn.prefill(dev, _stream_on(stream, dev), q, k, v, cu_q, cu_k, max_q, out, ws, scale, causal, lse)
     if rc:
-        _check(rc)
+        if rc < 0 and any(not isinstance(t, torch.Tensor) or t.dim() != 3 for t in (q, k)):
+            raise ValueError("q and k must be CUDA tensors [rows, heads, head_dim]")
+        dt, (nq, hq, D), (nk, hk, _) = q.dtype, q.shape, k.shape
+        _refused(rc, [(q, "q", hq, D, nq, dt, dev), (k, "k", hk, D, nk, dt, dev), (v, "v", hk, D, nk, dt, dev),
+                      (out, "out", hq, D, nq, dt, dev)],
+                 [(cu_q, "cu_q", torch.int32, 2, dev), (cu_k, "cu_k", torch.int32, getattr(cu_q, "numel", int)(), dev),
+                  (ws, "ws", torch.uint8, 0, dev), (lse, "lse", torch.float32, nq * hq, dev, True)])
+

@@ -808,23 +808,73 @@ def test_two_streams_at_once(q):
 
 
 def test_binding_refusals(q):
+    """Each argument the binding looks at, wrong in each way: refused with its name, and nothing written."""
     x = torch.zeros((2, 4, 64), dtype=torch.bfloat16, device="cuda")
-    dev = q.KvCache(None, None, 16, 2, 64, 4)
+    kv = x[:, :2]
+    dev = q.KvCache(torch.zeros(4 * 2 * 16 * 2 * 64, dtype=torch.uint8, device="cuda"), torch.zeros(16, device="cuda"), 16, 2, 64)
     batch = q.KvBatch(i32([[0], [1]]), i32([1, 1]), 2)
     ws = torch.empty(q.moe_attn_decode_workspace_bytes(dev, batch, 4), dtype=torch.uint8, device="cuda")
-    bad = [lambda: q.moe_attn_decode(dev, batch, x[:1], x, ws, 0.1),                        # too few rows
-           lambda: q.moe_attn_decode(dev, batch, x.float(), x, ws, 0.1),                    # a type it has not
-           lambda: q.moe_attn_decode(dev, batch, x, x.half(), ws, 0.1),
-           lambda: q.moe_attn_decode(dev, batch, x.transpose(1, 2).contiguous().transpose(1, 2), x, ws, 0.1),
-           lambda: q.moe_attn_decode(dev, batch, x, torch.empty_like(x), ws, 0.1, torch.zeros(3, device="cuda")),
-           lambda: q.moe_attn_decode(dev, batch, x[:, :3], x[:, :3], ws, 0.1),              # heads that do not divide
-           lambda: q.moe_kv_append(dev, batch, x[:, :2], x[:, :2], None, x, None),          # q without q_out
-           lambda: q.moe_kv_append(dev, batch, x, x),                                       # another number of heads
-           lambda: q.moe_kv_read(dev, batch, x[:, :2], None),
-           lambda: q.KvBatch(i32([[0, 1], [1, 2]]).t(), i32([1, 1]), 2),
-           lambda: q.KvBatch(i32([[0], [1]]), i32([1, 1]), 2, None, i32([0, 1, 2])),
-           lambda: q.KvCache(torch.zeros(100, dtype=torch.uint8, device="cuda"), None, 16, 2, 64)]
-    for i, call in enumerate(bad):
-        with pytest.raises((ValueError, q.QmoeError)):
+    out = torch.full_like(x, 7.0)
+    turned = x.transpose(1, 2).contiguous().transpose(1, 2)                        # heads not back to back
+    wrong = {"too few rows": x[:1], "another type": x.float(), "not its q's type": x.half(), "on the host": x.cpu(), "no tensor": 3,
+             "two dimensions": x[0], "heads apart": turned, "another dimension": x[:, :, :32]}
+    f32 = torch.zeros((2, 4), device="cuda")
+    cu = i32([0, 1, 2])
+
+    def refuses(call, name, what):
+        with pytest.raises((ValueError, q.QmoeError), match=name if isinstance(name, str) else None):
             call()
-            pytest.fail(f"call {i} was not refused")
+            pytest.fail(f"{what} was not refused")
+
+    for what, bad in wrong.items():
+        b2 = bad if not isinstance(bad, torch.Tensor) or bad.dim() != 3 else bad[:, :2]
+        if what != "not its q's type":
+            refuses(lambda: q.moe_attn_decode(dev, batch, bad, out, ws, 0.1), "q", f"decode q {what}")
+            refuses(lambda: q.moe_kv_append(dev, batch, b2, kv), "k", f"append k {what}")
+            refuses(lambda: q.moe_kv_read(dev, batch, b2, out[:, :2]), "k_out", f"read k_out {what}")
+        if what not in ("too few rows", "another dimension", "not its q's type"):
+            refuses(lambda: q.moe_attn_prefill(bad, kv, kv, cu, cu, 1, out, ws, 0.1), "q", f"prefill q {what}")
+        if what != "too few rows":
+            refuses(lambda: q.moe_attn_prefill(x, b2, kv, cu, cu, 1, out, ws, 0.1), "k|v", f"prefill k {what}")
+        refuses(lambda: q.moe_attn_decode(dev, batch, x, bad, ws, 0.1), "out", f"decode out {what}")
+        refuses(lambda: q.moe_attn_prefill(x, kv, kv, cu, cu, 1, bad, ws, 0.1), "out", f"prefill out {what}")
+        refuses(lambda: q.moe_attn_prefill(x, kv, b2, cu, cu, 1, out, ws, 0.1), "v", f"prefill v {what}")
+        refuses(lambda: q.moe_kv_append(dev, batch, kv, b2), "v", f"append v {what}")
+        refuses(lambda: q.moe_kv_append(dev, batch, kv, kv, None, bad, out), "q|q_out", f"append q {what}")
+        refuses(lambda: q.moe_kv_append(dev, batch, kv, kv, None, x, bad), "q_out", f"append q_out {what}")
+        refuses(lambda: q.moe_kv_append(dev, batch, kv, kv, None, None, None, b2), "k_out", f"append k_out {what}")
+        refuses(lambda: q.moe_kv_read(dev, batch, out[:, :2], b2), "v_out", f"read v_out {what}")
+    for what, bad in {"too small": f32[0], "another type": f32.half(), "on the host": f32.cpu(), "strided": torch.zeros((4, 4), device="cuda")[:, :2]}.items():
+        refuses(lambda: q.moe_attn_decode(dev, batch, x, out, ws, 0.1, bad), "lse", f"decode lse {what}")
+        refuses(lambda: q.moe_attn_prefill(x, kv, kv, cu, cu, 1, out, ws, 0.1, True, bad), "lse", f"prefill lse {what}")
+    for bad in (None, f32, ws.cpu(), ws[::2]):
+        refuses(lambda: q.moe_attn_decode(dev, batch, x, out, bad, 0.1), "ws", "decode ws")
+        refuses(lambda: q.moe_attn_prefill(x, kv, kv, cu, cu, 1, out, bad, 0.1), "ws", "prefill ws")
+    for bad in (None, cu.long(), cu.cpu(), cu[:1]):
+        refuses(lambda: q.moe_attn_prefill(x, kv, kv, bad, cu, 1, out, ws, 0.1), "cu_q", "cu_q")
+        refuses(lambda: q.moe_attn_prefill(x, kv, kv, cu, bad, 1, out, ws, 0.1), "cu_k", "cu_k")
+    for call in (lambda: q.moe_attn_decode(dev, batch, x, out, ws[:100], 0.1),       # too small a workspace
+                 lambda: q.moe_attn_decode(dev, batch, x, out, ws, float("nan")),
+                 lambda: q.moe_attn_decode(dev, batch, x[:, :3], out[:, :3], ws, 0.1),   # heads that do not divide
+                 lambda: q.moe_attn_prefill(x, kv, kv, cu, cu, 0, out, ws, 0.1),
+                 lambda: q.moe_attn_prefill(x, kv, kv, cu, cu, 1 << 40, out, ws, 0.1),
+                 lambda: q.moe_attn_prefill(x[:, :0], kv, kv, cu, cu, 1, out[:, :0], ws, 0.1),
+                 lambda: q.moe_kv_append(dev, batch, kv, kv, None, x, None),         # q without q_out
+                 lambda: q.moe_kv_append(dev, batch, kv, kv, None, None, out),
+                 lambda: q.moe_kv_append(dev, batch, x, x),                          # another number of heads
+                 lambda: q.moe_kv_read(dev, batch, kv, None),
+                 lambda: q.KvBatch(i32([[0, 1], [1, 2]]).t(), i32([1, 1]), 2),
+                 lambda: q.KvBatch(i32([[0], [1]]), i32([1, 1]), 2, None, i32([0, 1, 2])),
+                 lambda: q.KvCache(torch.zeros(100, dtype=torch.uint8, device="cuda"), None, 16, 2, 64)):
+        refuses(call, None, "call")
+    for call in (lambda: q.moe_attn_decode(dev, batch, x, out, ws, "0.1"), lambda: q.moe_attn_prefill(x, kv, kv, cu, cu, 1.5, out, ws, 0.1)):
+        with pytest.raises(TypeError):
+            call()
+    torch.cuda.synchronize()
+    assert torch.all(out == 7.0) and not dev.codes.any() and not dev.scales.any()
+    # and what is not wrong: more rows than the step has, one head of a row with odd strides
+    q.moe_attn_decode(dev, batch, torch.cat([x, x]), torch.cat([out, out]), ws, 1, f32)
+    one = q.KvCache(dev.codes, dev.scales, 16, 1, 64)
+    y = torch.zeros((2, 24, 64), dtype=torch.bfloat16, device="cuda")[:, 5:6]
+    q.moe_kv_append(one, batch, y, y, None, y, y)
+    torch.cuda.synchronize()
