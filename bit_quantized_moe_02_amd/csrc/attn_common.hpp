@@ -92,23 +92,23 @@ struct Seq {
   int len, n, row0;
 };
 
-__device__ __forceinline__ Seq seq_rows(const int32_t* cu, int per_seq, int T, int b) {
+// `some`: an address of 8 bytes that may be read, for where there is no cu (no
+// branch then keeps this load from going with others).
+__device__ __forceinline__ Seq seq_rows(const int32_t* cu, int per_seq, int T, int b, const void* some) {
+  const int32_t* p = cu ? cu + b : (const int32_t*)some;
+  const int first = p[0], past = p[1];
+  const int c0 = min(max(first, 0), T), c1 = min(max(past, c0), T);
   Seq s;
   s.len = 0;
-  if (cu) {
-    const int c0 = min(max(cu[b], 0), T), c1 = min(max(cu[b + 1], c0), T);
-    s.row0 = c0;
-    s.n = c1 - c0;
-  } else {
-    s.row0 = b * per_seq;
-    s.n = per_seq;
-  }
+  s.row0 = cu ? c0 : b * per_seq;
+  s.n = cu ? c1 - c0 : per_seq;
   return s;
 }
 
 __device__ __forceinline__ Seq seq_of(const qmoe::KvArgs& a, int b) {
-  Seq s = seq_rows(a.cu, a.per_seq, a.T, b);
-  s.len = min(max(a.lens[b], 0), a.max_len);
+  const int len = a.lens[b];
+  Seq s = seq_rows(a.cu, a.per_seq, a.T, b, a.codes);
+  s.len = min(max(len, 0), a.max_len);
   return s;
 }
 

@@ -467,7 +467,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(DecodeArgs a) {
   const int lane = threadIdx.x & 63;
   const int b = blockIdx.x / a.kv.max_new, i = blockIdx.x % a.kv.max_new, h = blockIdx.y;
   const int2 where = a.split.where[b];      // (nothing was written for a sequence without rows)
-  const Seq s = seq_rows(a.kv.cu, a.kv.per_seq, a.kv.T, b);
+  const Seq s = seq_rows(a.kv.cu, a.kv.per_seq, a.kv.T, b, a.kv.codes);
   if (i >= s.n) return;
   const int w0 = where.x, n = where.y;
   if (n == 1) return;                       // written by the range that holds it
@@ -510,7 +510,7 @@ template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void join_few_kernel(DecodeArgs a) {
   const int b = blockIdx.x / a.kv.max_new, i = blockIdx.x % a.kv.max_new, h = blockIdx.y * (kThreads / 64) + (threadIdx.x >> 6);
   const int2 where = a.split.where[b];
-  const Seq s = seq_rows(a.kv.cu, a.kv.per_seq, a.kv.T, b);
+  const Seq s = seq_rows(a.kv.cu, a.kv.per_seq, a.kv.T, b, a.kv.codes);
   if (h >= a.Hq || i >= s.n || where.y == 1) return;
   const int64_t pitch = (int64_t)a.kv.max_new * a.Hq, at = (where.x + b) * pitch + (int64_t)i * a.Hq + h, row = s.row0 + i;
   join_row<T, D>(a.split.o + at * D, a.split.ml + 2 * at, where.y, pitch, (uint16_t*)a.out + row * a.os + (int64_t)h * D,

@@ -267,11 +267,12 @@ struct Keys {
 // with step t-1, and the next K and the previous V have come, the copies of
 // the next but one K and of this tile's V start; they have a whole step's
 // time, and there is one barrier a step.  Tiles behind the last come as
-// zeros, so nothing here asks which is the last.
+// zeros, so only the scores ask which is the last (where tiles are masked: a
+// short prompt's time is mostly one or two tiles').
 template <bool First, bool Masked, typename T, int D>
 __device__ __forceinline__ bool step(Rows<T, D>& R, Scores& S, Weights& W, const Keys<D>& K, int t,
                                      uint8_t* k_this, uint8_t* k_next, uint8_t* v_this, uint8_t* v_last, int n_whole,
-                                     float c, int wave, int lane) {
+                                     int t1, float c, int wave, int lane) {
   const int j0 = t * kTile;
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
@@ -292,7 +293,7 @@ __device__ __forceinline__ bool step(Rows<T, D>& R, Scores& S, Weights& W, const
   }
   if (raise) raise_maximum<T, D>(R, S, mx);
   weights<T, D>(R, S, W);
-  scores<T, D>(R, S, k_next, lane);
+  if (!Masked || t + 1 < t1) scores<T, D>(R, S, k_next, lane);
   // (the weights are made here, among the products, not where they are used)
 #pragma unroll
   for (int w = 0; w < 4; ++w) asm volatile("" : "+v"(W.p[w]));
@@ -328,6 +329,11 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : D > 64 ? 2 : 3) void prefil
   constexpr int kBytes = kTile * D * 2;
   __shared__ __attribute__((aligned(1024))) uint8_t k0[kBytes], v0[kBytes], k1[kBytes], v1[kBytes];
 
+  // (all arguments are asked for at once: fetched where they are used, each
+  // line of them costs a short prompt a wait of its own)
+  asm volatile("" ::"s"(a.cu_q), "s"(a.cu_k), "s"(a.B), "s"(a.Tq), "s"(a.Tk), "s"(a.max_q), "s"(a.per_q), "s"(a.per_k), "s"(a.Hq),
+               "s"(a.Hk), "s"(a.q), "s"(a.k), "s"(a.v), "s"(a.out), "s"(a.lse), "s"(a.qs), "s"(a.ks), "s"(a.vs), "s"(a.os),
+               "s"(a.c), "s"(a.causal), "s"(a.split.n));
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // Workgroups go round robin over the 8 XCDs.  A key head's workgroups stay
   // on one of them, where its keys stay in the L2 (with fewer than 8 key heads
@@ -346,7 +352,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : D > 64 ? 2 : 3) void prefil
   }
   if (qt < 0) return;                       // the whole workgroup
   const int group = a.Hq / a.Hk;
-  const Seq sq = seq_rows(a.cu_q, a.per_q, a.Tq, b), sk = seq_rows(a.cu_k, a.per_k, a.Tk, b);
+  const Seq sq = seq_rows(a.cu_q, a.per_q, a.Tq, b, a.q), sk = seq_rows(a.cu_k, a.per_k, a.Tk, b, a.q);
   const int rows = min(sq.n, a.max_q) * group, r0 = qt * kRowsWg;
   if (r0 >= rows) return;                   // the whole workgroup
 
@@ -358,10 +364,10 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : D > 64 ? 2 : 3) void prefil
   R.last = r >= rows ? -1 : a.causal ? min(shift + token, sk.n - 1) : sk.n - 1;
   R.m = kMinusInf;
   R.l = 0.f;
-#pragma unroll
-  for (int k = 0; k < D / 16; ++k) R.q[k] = u32x4{0, 0, 0, 0};
-  if (r < rows) {
-    const uint16_t* p = (const uint16_t*)a.q + (int64_t)(sq.row0 + token) * a.qs + (int64_t)h * D + 8 * hh;
+  {
+    // (lanes behind the last row take it again: they see no key and write nothing)
+    const int rc = min(r, rows - 1), hc = hk * group + rc % group;
+    const uint16_t* p = (const uint16_t*)a.q + (int64_t)(sq.row0 + rc / group) * a.qs + (int64_t)hc * D + 8 * hh;
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) R.q[k] = *reinterpret_cast<const u32x4*>(p + 16 * k);
   }
@@ -392,19 +398,19 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : D > 64 ? 2 : 3) void prefil
     Scores S;
     Weights W;
     scores<T, D>(R, S, k0, lane);
-    step<true, true, T, D>(R, S, W, K, t0, k0, k1, v0, v1, n_whole, a.c, wave, lane);
+    step<true, true, T, D>(R, S, W, K, t0, k0, k1, v0, v1, n_whole, t1, a.c, wave, lane);
     int t = t0 + 1;
     const int t_whole = min(n_whole, t1);
     for (; t + 2 <= t_whole; t += 2) {
-      step<false, false, T, D>(R, S, W, K, t, k1, k0, v1, v0, n_whole, a.c, wave, lane);
-      step<false, false, T, D>(R, S, W, K, t + 1, k0, k1, v0, v1, n_whole, a.c, wave, lane);
+      step<false, false, T, D>(R, S, W, K, t, k1, k0, v1, v0, n_whole, t1, a.c, wave, lane);
+      step<false, false, T, D>(R, S, W, K, t + 1, k0, k1, v0, v1, n_whole, t1, a.c, wave, lane);
     }
     const int masked_from = t - 1;          // (its V is still to come)
     bool special = false;
     for (; t < t1; t += 2) {
-      special |= step<false, true, T, D>(R, S, W, K, t, k1, k0, v1, v0, n_whole, a.c, wave, lane);
+      special |= step<false, true, T, D>(R, S, W, K, t, k1, k0, v1, v0, n_whole, t1, a.c, wave, lane);
       if (t + 1 >= t1) break;
-      special |= step<false, true, T, D>(R, S, W, K, t + 1, k0, k1, v0, v1, n_whole, a.c, wave, lane);
+      special |= step<false, true, T, D>(R, S, W, K, t + 1, k0, k1, v0, v1, n_whole, t1, a.c, wave, lane);
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
@@ -444,7 +450,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : D > 64 ? 2 : 3) void prefil
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void join_parts_kernel(PrefillArgs a) {
   const int h = blockIdx.y * kWaves + (threadIdx.x >> 6), b = blockIdx.x / a.max_q, i = blockIdx.x % a.max_q;
-  const Seq sq = seq_rows(a.cu_q, a.per_q, a.Tq, b);
+  const Seq sq = seq_rows(a.cu_q, a.per_q, a.Tq, b, a.q);
   if (h >= a.Hq || i >= sq.n) return;
   const int64_t row = sq.row0 + i, at = row * a.Hq + h;
   join_row<T, D>(a.split.o + at * D, a.split.ml + 2 * at, a.split.n, (int64_t)a.Tq * a.Hq,
