@@ -321,8 +321,10 @@ __device__ __forceinline__ bool step(Rows<T, D>& R, Scores& S, Weights& W, const
 // product: 1.34 and 1.80 PFLOP/s).  With heads of 64 the vector unit does as
 // much for half the products: 8 prompts of up to 2048, 32 + 4 heads, 104 us,
 // 666 TFLOP/s, vector unit busy 61%, matrix core 33%.  A short prompt waits: one
-// tile 6.3 us, each one more about 1.1.
-// (64 rows a wave, one wave a SIMD: 278 and 154 us; 8 waves: 221 and 121.)
+// tile 6.0 us, each one more about 1 (2100 cycles for a wave alone on its SIMD,
+// half of them the matrix core's).
+// (64 rows a wave, one wave a SIMD: 278 and 154 us; 8 waves: 221 and 121; three
+// buffers: 112 with heads of 64, and 309 rows, heads of 128, 12.9 for 12.2.)
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads, D > 128 ? 1 : D > 64 ? 2 : 3) void prefill_kernel(PrefillArgs a, int tiles) {
   constexpr int kRowsWg = 32 * kWaves;
