@@ -32,6 +32,31 @@ __device__ __forceinline__ float inverse_pow2(float s) {
 
 __device__ __forceinline__ bool finite(float x) { return (__builtin_bit_cast(uint32_t, x) & 0x7F800000u) != 0x7F800000u; }
 
+// Sine and cosine of |x| <= pi/4 by their series: the first terms left out are
+// below 2^-36 of the sine and 2^-33.
+__device__ __forceinline__ void sine_cosine(double x, double* sn, double* cs) {
+  const double y = x * x;
+  const double s = 1.0 + y * (-1.0 / 6 + y * (1.0 / 120 + y * (-1.0 / 5040 + y * (1.0 / 362880 - y * (1.0 / 39916800)))));
+  const double c = 1.0 + y * (-0.5 + y * (1.0 / 24 + y * (-1.0 / 720 + y * (1.0 / 40320 - y * (1.0 / 3628800)))));
+  *sn = x * s;
+  *cs = c;
+}
+
+// 32 bits of x that rounded again to fewer (12 of mantissa at most: a row's, a
+// code's) give what x itself rounds to.  That is the nearest 32 bits, but for
+// those that look like a border between two shorter numbers: there x is cut
+// off and the last bit set in place of the bits lost.
+__device__ __forceinline__ float to_round_again(double x) {
+  const float f = (float)x;
+  uint32_t u = __builtin_bit_cast(uint32_t, f);
+  if ((u & 0xFFFu) == 0 && finite(f)) {
+    if (fabs((double)f) > fabs(x)) --u;
+    if ((double)f != x) u |= 1;
+  }
+  return __builtin_bit_cast(float, u);
+}
+
+
 __device__ __forceinline__ float amax_of(float m, float x) { return finite(x) ? fmaxf(m, fabsf(x)) : m; }
 
 // Code of x (already divided by the scale); not finite -> not a number.
@@ -86,7 +111,8 @@ __device__ __forceinline__ int64_t block_in(const KvArgs& a, int page, int blk, 
 
 // One workgroup takes the tokens that one block of one sequence gets, and a
 // share (blockIdx.y) of the heads.  Its threads compute the angles of those
-// tokens once into LDS (64-bit reduction, then 32-bit sine and cosine); then
+// tokens once into LDS, in 64 bits for k, whose codes then fall at the borders
+// between them as in 64-bit arithmetic, and rounded to 32 for q; then
 // each wave takes one job at a time: a q head (turn), a K head (turn, scale,
 // codes) or a V head (scale, codes).  A wave holds 16 tokens of one head in
 // registers, so each input is read once and each output written once.  The
@@ -106,6 +132,8 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int nb) 
   constexpr int kSt = kCh * 4 > 64 ? kCh * 4 / 64 : 1;
   constexpr int kRaw = 2 * kSteps > 4 * kSt ? 2 * kSteps : 4 * kSt;
   __shared__ __attribute__((aligned(16))) float2 turn[16][D / 2 + 1];
+  constexpr int kPitch = kLanes + 1;        // (so that neither writes nor reads meet in a bank)
+  __shared__ __attribute__((aligned(16))) double2 exact[16][8 * kPitch];   // pair 8 c + j at j * kPitch + c
 
   const int b = nb == 1 ? blockIdx.x : blockIdx.x / nb, ib = nb == 1 ? 0 : blockIdx.x % nb;
   const Seq s = seq_of(a.kv, b);
@@ -166,19 +194,22 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int nb) 
   load(job);
 
   if (half > 0) {
+    bool has_k = false;                     // whether a K head is among this workgroup's jobs
+    for (int j = blockIdx.y * kWaves; j < a.Hq + a.kv.Hk; j += kWaves * gridDim.y) has_k |= j + kWaves > a.Hq;
     // pair threadIdx.x % 128 of new tokens f + threadIdx.x / 128, ...
     const int p = threadIdx.x % 128;
     if (p < half) {
       const double w = a.freqs[p] * 0.15915494309189535;       // turns a position
       for (int n = f + (threadIdx.x / 128); n < e; n += kThreads / 128) {
-        // the nearest quarter turn off in 64 bits, the rest (an eighth at most,
-        // so exact to 2^-28 turns) in 32, and the quarters by exchange
+        // whole quarter turns off, and sine and cosine of the rest
         const double t = 4.0 * (double)(blk * 16 + n) * w, quarters = rint(t);
-        float sn, cs;
-        sincospif(0.5f * (float)(t - quarters), &sn, &cs);
+        double sn, cs;
+        sine_cosine((t - quarters) * 1.5707963267948966, &sn, &cs);
         const int k = (int)(quarters - 4.0 * floor(0.25 * quarters));
-        const float s4 = k & 1 ? cs : sn, c4 = k & 1 ? sn : cs;
-        turn[n][p] = make_float2((k == 1 || k == 2 ? -c4 : c4) * a.rscale, (k >= 2 ? -s4 : s4) * a.rscale);
+        const double s4 = k & 1 ? cs : sn, c4 = k & 1 ? sn : cs;
+        const double2 u = make_double2(k == 1 || k == 2 ? -c4 : c4, k >= 2 ? -s4 : s4);
+        if (has_k) exact[n][(p & 7) * kPitch + (p >> 3)] = make_double2(u.x * a.rscale, u.y * a.rscale);
+        turn[n][p] = make_float2((float)(u.x * a.rscale), (float)(u.y * a.rscale));
       }
     }
     __syncthreads();
@@ -201,7 +232,19 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int nb) 
         float* B = x[st] + 8;
         unpack8<T>(raw[2 * st], A);
         unpack8<T>(raw[2 * st + 1], B);
-        if (turned && on) {
+        if (turned && on && !is_q) {
+          const double2* t = &exact[n][c];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            // (pair j of the lane's: columns j and 8 + j of its 16, or 2 j and 2 j + 1)
+            const double2 u = t[j * kPitch];
+            float* pa = a.inter ? &x[st][2 * j] : A + j;
+            float* pb = a.inter ? &x[st][2 * j + 1] : B + j;
+            const double va = *pa, vb = *pb;
+            *pa = to_round_again(va * u.x - vb * u.y);
+            *pb = to_round_again(va * u.y + vb * u.x);
+          }
+        } else if (turned && on) {
           const float2* t = &turn[n][8 * c];
           if (a.inter) {
 #pragma unroll

@@ -136,8 +136,8 @@ int moe_rope_freqs(int32_t rot_dim, double base, int rule, double factor, double
  *           no q.
  *   k_out   the turned k rows, rounded once to the row type (may be k
  *           itself); NULL: not wanted.
- * Sums are 32-bit; the codes come from the 32-bit turned values, rounded
- * once (nearest, ties to even).  Scale of a block's K (or V): the least power
+ * q is turned in 32 bits, k in 64; k_out and the codes are the turned values
+ * rounded once (nearest, ties to even).  Scale of a block's K (or V): the least power
  * of two s with |x| <= 448 s for every finite x of the block's tokens so far,
  * not below 2^-64.  A token that needs a larger scale than its block has
  * makes the earlier tokens' codes of that block be divided by the growth
