@@ -33,11 +33,11 @@ __device__ __forceinline__ float inverse_pow2(float s) {
 __device__ __forceinline__ bool finite(float x) { return (__builtin_bit_cast(uint32_t, x) & 0x7F800000u) != 0x7F800000u; }
 
 // Sine and cosine of |x| <= pi/4 by their series: the first terms left out are
-// below 2^-36 of the sine and 2^-33.
+// below 2^-45 of the sine and 2^-40.
 __device__ __forceinline__ void sine_cosine(double x, double* sn, double* cs) {
   const double y = x * x;
-  const double s = 1.0 + y * (-1.0 / 6 + y * (1.0 / 120 + y * (-1.0 / 5040 + y * (1.0 / 362880 - y * (1.0 / 39916800)))));
-  const double c = 1.0 + y * (-0.5 + y * (1.0 / 24 + y * (-1.0 / 720 + y * (1.0 / 40320 - y * (1.0 / 3628800)))));
+  const double s = 1.0 + y * (-1.0 / 6 + y * (1.0 / 120 + y * (-1.0 / 5040 + y * (1.0 / 362880 + y * (-1.0 / 39916800 + y * (1.0 / 6227020800))))));
+  const double c = 1.0 + y * (-0.5 + y * (1.0 / 24 + y * (-1.0 / 720 + y * (1.0 / 40320 + y * (-1.0 / 3628800 + y * (1.0 / 479001600))))));
   *sn = x * s;
   *cs = c;
 }
@@ -120,9 +120,10 @@ __device__ __forceinline__ int64_t block_in(const KvArgs& a, int page, int blk, 
 // latency that counts.  (With many, asking for each next job's loads while one
 // is worked on costs registers and 4% at 2048 tokens of 32 + 8 + 8 heads.)
 //
-// Bound by memory: 2048 tokens, heads of 128: 50 MB in 14.4 us, 3.5 TB/s (a
-// copy of 4 GB reaches 4.7).  One token 4.6 us, 64 users of up to 3 tokens 6.4:
-// a launch and three loads that wait for one another (length, page, scale).
+// Bound by memory: 2048 tokens, heads of 128: 50 MB in 13.7 us, 3.7 TB/s (a
+// copy of 4 GB reaches 4.7); without a turn 12.5, with all of it in 32 bits 12.9.
+// One token 4.6 us, 64 users of up to 3 tokens 6.0: a launch and three loads
+// that wait for one another (length, page, scale).
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int nb) {
   constexpr int kLanes = D / 16;            // lanes of a row of q or k, 16 columns each
@@ -196,11 +197,11 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int nb) 
   if (half > 0) {
     bool has_k = false;                     // whether a K head is among this workgroup's jobs
     for (int j = blockIdx.y * kWaves; j < a.Hq + a.kv.Hk; j += kWaves * gridDim.y) has_k |= j + kWaves > a.Hq;
-    // pair threadIdx.x % 128 of new tokens f + threadIdx.x / 128, ...
-    const int p = threadIdx.x % 128;
+    // a thread takes one pair of every (256 / 2^sh)th new token
+    const int sh = half <= 32 ? 5 : half <= 64 ? 6 : 7, p = threadIdx.x & ((1 << sh) - 1);
     if (p < half) {
       const double w = a.freqs[p] * 0.15915494309189535;       // turns a position
-      for (int n = f + (threadIdx.x / 128); n < e; n += kThreads / 128) {
+      for (int n = f + (threadIdx.x >> sh); n < e; n += kThreads >> sh) {
         // whole quarter turns off, and sine and cosine of the rest
         const double t = 4.0 * (double)(blk * 16 + n) * w, quarters = rint(t);
         double sn, cs;

@@ -92,6 +92,13 @@ def in_type(x, dt):
     return torch.from_numpy(x).to(dt).to(torch.float64).numpy()
 
 
+def rounded(x, dt):
+    """fp64 values rounded once to the row type (torch rounds them to 32 bits on the way)."""
+    bits, least = (8, -125) if dt == torch.bfloat16 else (11, -13)
+    quantum = np.ldexp(1.0, np.maximum(np.frexp(x)[1], least) - bits)
+    return np.rint(x / quantum) * quantum
+
+
 def attention_bounds(dt, dim, v, out, mag, smag, n_keys):
     """How far outputs and log sums may be from the oracle's, from the arithmetic alone.
 
