@@ -42,18 +42,28 @@ __device__ __forceinline__ void sine_cosine(double x, double* sn, double* cs) {
   *cs = c;
 }
 
-// 32 bits of x that rounded again to fewer (12 of mantissa at most: a row's, a
-// code's) give what x itself rounds to.  That is the nearest 32 bits, but for
-// those that look like a border between two shorter numbers: there x is cut
-// off and the last bit set in place of the bits lost.
-__device__ __forceinline__ float to_round_again(double x) {
-  const float f = (float)x;
-  uint32_t u = __builtin_bit_cast(uint32_t, f);
-  if ((u & 0xFFFu) == 0 && finite(f)) {
-    if (fabs((double)f) > fabs(x)) --u;
-    if ((double)f != x) u |= 1;
+// 32 bits of each x that rounded again to fewer (12 of mantissa at most: a
+// row's, a code's) give what x itself rounds to.  Those are the nearest 32
+// bits, but for those that look like a border between two shorter numbers:
+// there x is cut off and the last bit set in place of the bits lost.
+template <int N>
+__device__ __forceinline__ void to_round_again(const double* x, float* f) {
+  uint32_t low = 0xFFFu;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    f[i] = (float)x[i];
+    low = min(low, __builtin_bit_cast(uint32_t, f[i]) & 0xFFFu);
   }
-  return __builtin_bit_cast(float, u);
+  if (low != 0) return;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    uint32_t u = __builtin_bit_cast(uint32_t, f[i]);
+    if ((u & 0xFFFu) == 0 && finite(f[i])) {
+      if (fabs((double)f[i]) > fabs(x[i])) --u;
+      if ((double)f[i] != x[i]) u |= 1;
+      f[i] = __builtin_bit_cast(float, u);
+    }
+  }
 }
 
 
@@ -122,7 +132,7 @@ __device__ __forceinline__ int64_t block_in(const KvArgs& a, int page, int blk, 
 //
 // Bound by memory: 2048 tokens, heads of 128: 50 MB in 13.7 us, 3.7 TB/s (a
 // copy of 4 GB reaches 4.7); without a turn 12.5, with all of it in 32 bits 12.9.
-// One token 4.6 us, 64 users of up to 3 tokens 6.0: a launch and three loads
+// One token 4.9 us, 64 users of up to 3 tokens 6.0: a launch and three loads
 // that wait for one another (length, page, scale).
 template <typename T, int D>
 __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int nb) {
@@ -236,14 +246,28 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int nb) 
         if (turned && on && !is_q) {
           const double2* t = &exact[n][c];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
+          for (int j0 = 0; j0 < 8; j0 += 2) {
             // (pair j of the lane's: columns j and 8 + j of its 16, or 2 j and 2 j + 1)
-            const double2 u = t[j * kPitch];
-            float* pa = a.inter ? &x[st][2 * j] : A + j;
-            float* pb = a.inter ? &x[st][2 * j + 1] : B + j;
-            const double va = *pa, vb = *pb;
-            *pa = to_round_again(va * u.x - vb * u.y);
-            *pb = to_round_again(va * u.y + vb * u.x);
+            double v[4];
+            float y[4];
+#pragma unroll
+            for (int j = j0; j < j0 + 2; ++j) {
+              const double2 u = t[j * kPitch];
+              const double va = a.inter ? x[st][2 * j] : A[j], vb = a.inter ? x[st][2 * j + 1] : B[j];
+              v[2 * (j - j0)] = va * u.x - vb * u.y;
+              v[2 * (j - j0) + 1] = va * u.y + vb * u.x;
+            }
+            to_round_again<4>(v, y);
+#pragma unroll
+            for (int j = j0; j < j0 + 2; ++j) {
+              if (a.inter) {
+                x[st][2 * j] = y[2 * (j - j0)];
+                x[st][2 * j + 1] = y[2 * (j - j0) + 1];
+              } else {
+                A[j] = y[2 * (j - j0)];
+                B[j] = y[2 * (j - j0) + 1];
+              }
+            }
           }
         } else if (turned && on) {
           const float2* t = &turn[n][8 * c];
