@@ -157,10 +157,11 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 
 // One wave joins the n parts of one row and head, 4 columns a lane, as many
 // parts at once as it has lanes for: part p's un-normalised output at
-// o + p * pitch * D, its (maximum, sum) at ml + 2 * p * pitch; lse may be null.
+// o + p * pitch * D (1 / up times its size), its (maximum, sum) at ml + 2 * p *
+// pitch; lse may be null.
 template <typename T, int D>
 __device__ __forceinline__ void join_row(const float* o, const float* ml, int n, int64_t pitch, uint16_t* out, float* lse,
-                                         int lane) {
+                                         float up, int lane) {
   constexpr int kCh = D / 4, kAtOnce = 64 / kCh;
   const int ch = lane % kCh, p0 = lane / kCh;
   float mx = kMinusInf;
@@ -183,7 +184,7 @@ __device__ __forceinline__ void join_row(const float* o, const float* ml, int n,
     for (int j = 0; j < 4; ++j) acc[j] += __shfl_xor(acc[j], s);
   }
   if (p0 != 0) return;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const float inv = sum == 0.f ? 0.f : up / sum;
   u32x2 w;
   w.x = T::cvt2(acc[0] * inv, acc[1] * inv);
   w.y = T::cvt2(acc[2] * inv, acc[3] * inv);

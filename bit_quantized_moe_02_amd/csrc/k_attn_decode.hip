@@ -127,6 +127,13 @@ __device__ __forceinline__ uint32_t word_of(const u32x4& v, int w) {
   return w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w;
 }
 
+// A score's factor: scale * log2(e) times the block's scale, by its exponent,
+// kept finite and above zero (0 * inf and inf * 0 are no scores).
+__device__ __forceinline__ float score_factor(float c, float block_scale) {
+  const float e = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, block_scale) & 0x7F800000u);
+  return fminf(fmaxf(c * e, 0x1p-126f), 0x1.fffffep127f);
+}
+
 // Codes are read once, so they need not displace what the caches hold.
 __device__ __forceinline__ u32x4 load_codes(const uint8_t* p) {
   return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
@@ -134,6 +141,11 @@ __device__ __forceinline__ u32x4 load_codes(const uint8_t* p) {
 
 // Workgroups of a compute unit that the registers leave room for.
 constexpr int occupancy(int dim, int nr) { return dim > 128 ? 1 : nr == 1 ? 3 : 2; }
+
+// Outputs are summed 2^-32 times their size: a block's largest value, 448 *
+// 2^121, lies outside of 32-bit and bf16 numbers, and where its token is
+// masked 0 * inf would spoil the row.
+constexpr float kVDown = 0x1p-32f, kVUp = 0x1p32f;
 
 // Workgroup: one range, one key head, up to 16*NR rows of each of its
 // sequences (row r = token r / group, query head r % group of the key head's
@@ -143,7 +155,12 @@ constexpr int occupancy(int dim, int nr) { return dim > 128 ? 1 : nr == 1 ? 3 : 
 // With K as the first operand a 16x16x32 product gives a lane 4 positions of
 // one row (column lane % 16), which is what the second product takes as its
 // operand after exp, so the weights never leave the registers; the cache's
-// layout gives K and V codes in operand order by 16-byte loads.  HBM bounds
+// layout gives K and V codes in operand order by 16-byte loads.  The operands
+// are exact: K's are the codes themselves, their scale in the score's factor,
+// V's are bf16 numbers whatever the row type is (fp16 ends at 65504, and a code
+// times its scale does not), and a weight is the sum of two bf16 numbers, its
+// rounded value and what that leaves, good to 2^-16: the second products are
+// hidden by the loads.  HBM bounds
 // it, so a wave's loads never stop: the next step's K codes are asked for as
 // soon as this step's are in the first product, its V codes after the second.
 // (Two steps ahead holds twice the registers and gains nothing: 16 drafts of
@@ -253,20 +270,20 @@ __global__ __launch_bounds__(64 * (Short ? kShortWaves : kWaves), Short ? 1 : oc
         for (int k = 0; k < kP; ++k) vr[i][k] = load_codes(p + 16 * D + 1024 * k);
       }
       for (; st < s1; st += NW) {
-        // scores: position 32 st + 16 i + 4 g + j in sc[t][i][j]
+        // scores (of codes, without the scales): position 32 st + 16 i + 4 g + j in sc[t][i][j]
         f32x4 sc[NR][2];
-        float sv[2];
+        float ck[2], sv[2];
         int valid[2];
 #pragma unroll
         for (int t = 0; t < NR; ++t) sc[t][0] = sc[t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           valid[i] = cur[i].valid;
-          const float sk = valid[i] ? sc2[i].x : 1.f;
-          sv[i] = valid[i] ? sc2[i].y : 1.f;
+          ck[i] = score_factor(a.c, valid[i] ? sc2[i].x : 1.f);
+          sv[i] = valid[i] ? sc2[i].y * kVDown : 1.f;
 #pragma unroll
           for (int p = 0; p < kP; ++p) {
-            const u32x4 ka = dec8<T>(kr[i][p].x, kr[i][p].y, sk), kb = dec8<T>(kr[i][p].z, kr[i][p].w, sk);
+            const u32x4 ka = dec8<T>(kr[i][p].x, kr[i][p].y, 1.f), kb = dec8<T>(kr[i][p].z, kr[i][p].w, 1.f);
 #pragma unroll
             for (int t = 0; t < NR; ++t) {
               sc[t][i] = T::mma16(ka, q[t][2 * p], sc[t][i]);
@@ -315,16 +332,17 @@ __global__ __launch_bounds__(64 * (Short ? kShortWaves : kWaves), Short ? 1 : oc
           }
           bad_v = __any(bad_v);
         }
-        u32x4 pk[NR];
+        u32x4 hi[NR], lo[NR];
 #pragma unroll
         for (int t = 0; t < NR; ++t) {
           // powers of two under the running maximum, which is raised only when a
-          // score exceeds it by 2^8 (or a row has none yet): weights up to 2^8
-          // cost no precision, and the sums are hardly ever rescaled
+          // score exceeds it by 2^8 (or a row has none yet), so that the sums are
+          // hardly ever rescaled; the weights are then up to 2^8, and their two
+          // roundings relative to themselves
           const float base = m[t] == kMinusInf ? 0.f : m[t];
           float x[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = __builtin_fmaf(sc[t][j >> 2][j & 3], a.c, -base);
+          for (int j = 0; j < 8; ++j) x[j] = __builtin_fmaf(sc[t][j >> 2][j & 3], ck[j >> 2], -base);
           float mx = fmaxf(fmaxf(x[0], x[1]), x[2]);
           mx = fmaxf(fmaxf(mx, x[3]), x[4]);
           mx = fmaxf(fmaxf(mx, x[5]), x[6]);
@@ -345,10 +363,12 @@ __global__ __launch_bounds__(64 * (Short ? kShortWaves : kWaves), Short ? 1 : oc
             x[j] = exp2_fast(x[j]);
             l[t] += x[j];
           }
-          pk[t].x = T::cvt2(x[0], x[1]);
-          pk[t].y = T::cvt2(x[2], x[3]);
-          pk[t].z = T::cvt2(x[4], x[5]);
-          pk[t].w = T::cvt2(x[6], x[7]);
+#pragma unroll
+          for (int j = 0; j < 8; j += 2) {
+            const uint32_t h = Bf16::cvt2(x[j], x[j + 1]);
+            hi[t][j >> 1] = h;
+            lo[t][j >> 1] = Bf16::cvt2(x[j] - Bf16::lo(h), x[j + 1] - Bf16::hi(h));
+          }
         }
         // a valid V that is not a number, behind some rows' last position: take
         // it out of the product, and give it to the rows that see it
@@ -386,17 +406,21 @@ __global__ __launch_bounds__(64 * (Short ? kShortWaves : kWaves), Short ? 1 : oc
         }
 #pragma unroll
         for (int p = 0; p < kP; ++p) {
+          u32x4 v[4];
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             const uint32_t w0 = word_of(vr[0][p], w), w1 = word_of(vr[1][p], w);
-            u32x4 v;
-            v.x = T::dec2(w0, sv[0], false);
-            v.y = T::dec2(w0, sv[0], true);
-            v.z = T::dec2(w1, sv[1], false);
-            v.w = T::dec2(w1, sv[1], true);
+            v[w].x = Bf16::dec2(w0, sv[0], false);
+            v[w].y = Bf16::dec2(w0, sv[0], true);
+            v[w].z = Bf16::dec2(w1, sv[1], false);
+            v[w].w = Bf16::dec2(w1, sv[1], true);
 #pragma unroll
-            for (int t = 0; t < NR; ++t) o[t][4 * p + w] = T::mma16(v, pk[t], o[t][4 * p + w]);
+            for (int t = 0; t < NR; ++t) o[t][4 * p + w] = Bf16::mma16(v[w], hi[t], o[t][4 * p + w]);
           }
+#pragma unroll
+          for (int t = 0; t < NR; ++t)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) o[t][4 * p + w] = Bf16::mma16(v[w], lo[t], o[t][4 * p + w]);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -443,7 +467,7 @@ __global__ __launch_bounds__(64 * (Short ? kShortWaves : kWaves), Short ? 1 : oc
           *reinterpret_cast<f32x4*>(a.split.o + at * D + 4 * ch) = acc;
           if (ch == 0) *reinterpret_cast<float2*>(a.split.ml + 2 * at) = make_float2(mx, sum);
         } else {
-          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          const float inv = sum == 0.f ? 0.f : kVUp / sum;
           u32x2 w;
           w.x = T::cvt2(acc[0] * inv, acc[1] * inv);
           w.y = T::cvt2(acc[2] * inv, acc[3] * inv);
@@ -496,7 +520,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(DecodeArgs a) {
     acc += acc_s[p][ch];
     sum += sum_s[p];
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const float inv = sum == 0.f ? 0.f : kVUp / sum;
   u32x2 w;
   w.x = T::cvt2(acc[0] * inv, acc[1] * inv);
   w.y = T::cvt2(acc[2] * inv, acc[3] * inv);
@@ -514,7 +538,7 @@ __global__ __launch_bounds__(kThreads) void join_few_kernel(DecodeArgs a) {
   if (h >= a.Hq || i >= s.n || where.y == 1) return;
   const int64_t pitch = (int64_t)a.kv.max_new * a.Hq, at = (where.x + b) * pitch + (int64_t)i * a.Hq + h, row = s.row0 + i;
   join_row<T, D>(a.split.o + at * D, a.split.ml + 2 * at, where.y, pitch, (uint16_t*)a.out + row * a.os + (int64_t)h * D,
-                 a.lse ? a.lse + row * a.Hq + h : nullptr, threadIdx.x & 63);
+                 a.lse ? a.lse + row * a.Hq + h : nullptr, kVUp, threadIdx.x & 63);
 }
 
 int rows_of(const KvArgs& kv, int Hq) { return kv.max_new * (Hq / kv.Hk); }

@@ -456,7 +456,7 @@ __global__ __launch_bounds__(kThreads) void join_parts_kernel(PrefillArgs a) {
   if (h >= a.Hq || i >= sq.n) return;
   const int64_t row = sq.row0 + i, at = row * a.Hq + h;
   join_row<T, D>(a.split.o + at * D, a.split.ml + 2 * at, a.split.n, (int64_t)a.Tq * a.Hq,
-                 (uint16_t*)a.out + row * a.os + (int64_t)h * D, a.lse ? a.lse + at : nullptr, threadIdx.x & 63);
+                 (uint16_t*)a.out + row * a.os + (int64_t)h * D, a.lse ? a.lse + at : nullptr, 1.f, threadIdx.x & 63);
 }
 
 template <typename T, int D>

@@ -172,12 +172,14 @@ size_t moe_attn_decode_workspace_bytes(const moe_kv_cache* cache, const moe_kv_b
  *   out[r,h] = sum_j p_j V_j, p = softmax_j(scale q[r,h] . K_j), over the
  *   positions j <= the row's own; a row with none of them gives zeros.
  * lse (device float [rows][q_heads], NULL: not wanted): log sum_j
- * exp(scale q . K_j), -inf for an empty row.  Products of 16-bit operands
- * (codes times scales as rows of the row type; the weights p of one tile
- * rounded to it), 32-bit sums.  Meant for few rows a sequence (1..16 in
- * decoding and draft verification; any number works).  ws: device scratch,
- * no initialization needed; calls that overlap in time need one each.  out
- * and lse must not overlap the inputs. */
+ * exp(scale q . K_j), -inf for an empty row.  Codes and scales enter the
+ * products exactly, whatever the row type's range is; a weight p is held to
+ * 2^-16 of itself (a bf16 number and what its rounding leaves, as another);
+ * sums are 32-bit, and the output is rounded once to the row type (a sum outside
+ * its range gives infinity).  Meant for few rows a sequence
+ * (1..16 in decoding and draft verification; any number works).  ws: device
+ * scratch, no initialization needed; calls that overlap in time need one each.
+ * out and lse must not overlap the inputs. */
 int moe_attn_decode(const moe_kv_cache* cache, const moe_kv_batch* batch, int dtype, const void* q,
                     int64_t q_stride, int32_t q_heads, float scale, void* out, int64_t out_stride, float* lse,
                     void* ws, size_t ws_bytes, void* stream);
@@ -203,7 +205,8 @@ typedef struct moe_packed {
 size_t moe_attn_prefill_workspace_bytes(const moe_packed* p);
 
 /* Attention of packed sequences: as moe_attn_decode, with k and v rows in
- * place of the cache.  causal != 0: query row i of n sees key rows
+ * place of the cache, and the weights p of one tile rounded to the row type
+ * (half a step of each).  causal != 0: query row i of n sees key rows
  * j <= m - n + i of the sequence's m (aligned at the end: a chunk's rows come
  * last; with n > m the first n - m rows see nothing); else all m.  rows_k may
  * be 0 (k and v are not read then).  out, lse and ws as above. */

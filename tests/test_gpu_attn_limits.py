@@ -1,0 +1,129 @@
+"""GPU tests of the attention calls at the edges of their numbers: values next to the row type's largest, weights far
+below the largest, how many bits the weights keep."""
+import numpy as np
+import pytest
+
+from oracle import attn_oracle as A
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def q():
+    import torch
+    assert torch.cuda.is_available(), "GPU test needs a GPU"
+    from bit_quantized_moe_02_amd import qmoe
+    return qmoe
+
+
+import torch  # noqa: E402
+
+from attn_fixture import (DT, attention_bounds, check_attention, cu_of, f64, half_step, i32, page_table, random_cache, rows_in,  # noqa: E402
+                          subnormal_half, to_device)
+
+WIDTHS = [None, 4096]                                   # positions of a table: contexts whole, and cut into ranges
+
+
+def _table(rng, lens, page, width):
+    return page_table(rng, lens, page, width=None if width is None else width // page)
+
+
+def _decode(q, dev, table, lens, ns, qt, scale):
+    T, Hq, _ = qt.shape
+    batch = q.KvBatch(i32(table), i32(lens), T, max(ns), i32(cu_of(ns)))
+    out, lse = torch.full_like(qt, 9.0), torch.full((T, Hq), 9.0, device="cuda")
+    ws = torch.full((q.moe_attn_decode_workspace_bytes(dev, batch, Hq),), 0xFF, dtype=torch.uint8, device="cuda")
+    q.moe_attn_decode(dev, batch, qt, out, ws, scale, lse)
+    torch.cuda.synchronize()
+    return out, lse
+
+
+def _split_bounds(dt, dim, out, mag, smag, n_keys):
+    """As attention_bounds, for weights held as a 16-bit number and the rest of it as another (each rounding at most
+    half a step of bf16, 2^-8 of what it rounds), in products of exact values: 2^-16 of a weight."""
+    tol, tl = attention_bounds(dt, dim, np.zeros(1), out, mag, smag, n_keys)
+    smag = np.where(np.isfinite(smag), smag, 0)
+    e_s = (dim + 5) * 2.0 ** -24 * smag + 2.0 ** -21
+    rel = 2.0 ** -16 + 2 * e_s + (n_keys + 16) * 2.0 ** -23
+    return rel[..., None] * mag * (1 + 2 ** -6) + half_step(dt) * np.abs(out) + subnormal_half(dt), tl
+
+
+@pytest.mark.parametrize("width", WIDTHS)
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_decode_of_values_next_to_the_types_largest(q, D, dt, width):
+    """A draft's last token whose K and V round up past the row type's largest number: finite codes and scales, so the
+    tokens before it do not see it, and it has its finite part in its own row."""
+    dt = DT[dt]
+    rng = np.random.default_rng(60)
+    Hq, Hk, page, lens, ns = 4, 2, 16, [70, 37], [5, 3]
+    big = torch.finfo(dt).max
+    table, n_pages = _table(rng, lens, page, width)
+    cache = A.Cache(*random_cache(rng, n_pages, page, Hk, D), page, Hk, D)
+    dev = to_device(q, cache)
+    T = sum(ns)
+    qt, qv = rows_in(rng, T, Hq, D, dt, sigma=2.0)
+    kt, _ = rows_in(rng, T, Hk, D, dt)
+    vt, _ = rows_in(rng, T, Hk, D, dt)
+    vt[4, :, ::2], vt[7, 0, 1::2] = big, -big
+    kt[7, 1, 5] = big                                   # (its score is far below the others')
+    qt[5:, 2:, 5] = -2.0 ** -14 if dt == torch.float16 else -2.0 ** -120
+    qv = f64(qt)
+    q.moe_kv_append(dev, q.KvBatch(i32(table), i32(lens), T, 5, i32(cu_of(ns))), kt, vt)
+    cache = A.Cache(dev.codes.cpu().numpy(), f64(dev.scales), page, Hk, D)
+    out, lse = _decode(q, dev, table, lens, ns, qt, D ** -0.5)
+    cu = cu_of(ns)
+    for b, n in enumerate(ns):
+        K, V, _ = cache.read(table[b], 0, lens[b])
+        assert np.abs(V[-1]).max() > big and np.isfinite(V).all() and np.isfinite(K).all()
+        rows = slice(cu[b], cu[b + 1])
+        seen = np.arange(lens[b])[None] <= (lens[b] - n + np.arange(n))[:, None]
+        ref, rl, mag, smag = A.attention(qv[rows], K, V, seen, D ** -0.5)
+        assert np.abs(ref).max() < big
+        check_attention(out[rows], lse[rows], ref, rl, *_split_bounds(dt, D, ref, mag, smag, lens[b]), f"sequence {b}")
+
+
+@pytest.mark.parametrize("width", WIDTHS)
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_decode_weights_keep_16_bits(q, D, dt, width):
+    """Rows that a few keys dominate are as good as the output's own rounding."""
+    dt = DT[dt]
+    rng = np.random.default_rng(61)
+    Hq, Hk, page, lens, ns = 8, 2, 64, [777, 301], [2, 4]
+    table, n_pages = _table(rng, lens, page, width)
+    cache = A.Cache(*random_cache(rng, n_pages, page, Hk, D), page, Hk, D)
+    dev = to_device(q, cache)
+    qt, qv = rows_in(rng, 6, Hq, D, dt, sigma=3.0)
+    out, lse = _decode(q, dev, table, lens, ns, qt, D ** -0.5)
+    cu = cu_of(ns)
+    for b, n in enumerate(ns):
+        K, V, _ = cache.read(table[b], 0, lens[b])
+        rows = slice(cu[b], cu[b + 1])
+        seen = np.arange(lens[b])[None] <= (lens[b] - n + np.arange(n))[:, None]
+        ref, rl, mag, smag = A.attention(qv[rows], K, V, seen, D ** -0.5)
+        check_attention(out[rows], lse[rows], ref, rl, *_split_bounds(dt, D, ref, mag, smag, lens[b]), f"sequence {b}")
+
+
+@pytest.mark.parametrize("width", WIDTHS)
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_decode_many_small_weights_beside_a_large_one(q, dt, width):
+    """A first key that takes nearly all the weight and has no value, and 1400 others 2^-24.4 below it, whose values are
+    the whole output."""
+    dt = DT[dt]
+    rng = np.random.default_rng(63)
+    D, Hq, Hk, page, L = 64, 2, 1, 16, 1401
+    table, n_pages = _table(rng, [L], page, width)
+    cache = A.Cache(*random_cache(rng, n_pages, page, Hk, D), page, Hk, D)
+    dev = to_device(q, cache)
+    kt = torch.zeros((L, Hk, D), dtype=dt, device="cuda")
+    vt = torch.full((L, Hk, D), 40.0, dtype=dt, device="cuda")
+    qt = torch.zeros((1, Hq, D), dtype=dt, device="cuda")
+    kt[0, :, 0], vt[0], qt[:, :, 0] = 16.0, 0.0, 1.0
+    scale = 24.4 * np.log(2) / 16
+    q.moe_kv_append(dev, q.KvBatch(i32(table), i32([L]), L), kt, vt)
+    cache = A.Cache(dev.codes.cpu().numpy(), f64(dev.scales), page, Hk, D)
+    out, lse = _decode(q, dev, table, [L], [1], qt, scale)
+    K, V, _ = cache.read(table[0], 0, L)
+    ref, rl, mag, smag = A.attention(f64(qt), K, V, np.ones((1, L), bool), scale)
+    check_attention(out, lse, ref, rl, *_split_bounds(dt, D, ref, mag, smag, L), "small weights")
