@@ -349,14 +349,19 @@ __global__ __launch_bounds__(64 * (Short ? kShortWaves : kWaves), Short ? 1 : oc
           mx = max_rows4(fmaxf(mx, x[7]));
           const bool raise = mx > kLazy || (m[t] == kMinusInf && mx > kMinusInf);
           if (__any(raise)) {
-            const float d = raise ? mx : 0.f;
-            const float r = !raise ? 1.f : m[t] == kMinusInf ? 0.f : exp2_fast(-d);
-            if (raise) m[t] = base + d;
+            // from the scores again: under a maximum far below them x has lost bits
+            float top = kMinusInf;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) top = fmaxf(top, sc[t][j >> 2][j & 3] * ck[j >> 2]);
+            top = max_rows4(top);
+            const float r = !raise ? 1.f : m[t] == kMinusInf ? 0.f : exp2_fast(m[t] - top);
+            if (raise) m[t] = top;
             l[t] *= r;
 #pragma unroll
             for (int k = 0; k < kDt; ++k) o[t][k] *= r;
+            const float now = raise ? top : base;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] -= d;
+            for (int j = 0; j < 8; ++j) x[j] = __builtin_fmaf(sc[t][j >> 2][j & 3], ck[j >> 2], -now);
           }
 #pragma unroll
           for (int j = 0; j < 8; ++j) {

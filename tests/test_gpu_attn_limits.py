@@ -1,5 +1,5 @@
-"""GPU tests of the attention calls at the edges of their numbers: values next to the row type's largest, weights far
-below the largest, how many bits the weights keep."""
+"""GPU tests of the attention calls at the edges of their numbers: values next to the row type's largest, scores that
+jump between tiles, weights far below the largest, how many bits the weights keep."""
 import numpy as np
 import pytest
 
@@ -103,6 +103,32 @@ def test_decode_weights_keep_16_bits(q, D, dt, width):
         seen = np.arange(lens[b])[None] <= (lens[b] - n + np.arange(n))[:, None]
         ref, rl, mag, smag = A.attention(qv[rows], K, V, seen, D ** -0.5)
         check_attention(out[rows], lse[rows], ref, rl, *_split_bounds(dt, D, ref, mag, smag, lens[b]), f"sequence {b}")
+
+
+@pytest.mark.parametrize("width", WIDTHS)
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_decode_scores_that_jump(q, dt, width):
+    """Scores of some -30000 in the first half of the context and ordinary ones in the second: the first half has no
+    weight at all, and costs the second no bits."""
+    dt = DT[dt]
+    rng = np.random.default_rng(62)
+    D, Hq, Hk, page, L = 64, 16, 1, 16, 1024
+    table, n_pages = _table(rng, [L], page, width)
+    cache = A.Cache(*random_cache(rng, n_pages, page, Hk, D), page, Hk, D)
+    dev = to_device(q, cache)
+    kt, _ = rows_in(rng, L, Hk, D, dt)
+    vt, _ = rows_in(rng, L, Hk, D, dt)
+    qt, _ = rows_in(rng, 1, Hq, D, dt)
+    kt[:L // 2, :, 0], kt[L // 2:, :, 0], qt[:, :, 0] = -30000.0, 0.0, 8.0
+    kt[-10, :, 1], qt[:, :, 1] = 8.0, 8.0               # (a key that stands out, so that errors do not average out)
+    q.moe_kv_append(dev, q.KvBatch(i32(table), i32([L]), L), kt, vt)
+    cache = A.Cache(dev.codes.cpu().numpy(), f64(dev.scales), page, Hk, D)
+    out, lse = _decode(q, dev, table, [L], [1], qt, 0.125)
+    K, V, _ = cache.read(table[0], 0, L)
+    # (exp(-29000) of the second half's weights is below any bound here)
+    ref, rl, mag, smag = A.attention(f64(qt), K, V, np.arange(L)[None] >= L // 2, 0.125)
+    assert smag.max() < 20
+    check_attention(out, lse, ref, rl, *_split_bounds(dt, D, ref, mag, smag, L), "jump")
 
 
 @pytest.mark.parametrize("width", WIDTHS)
