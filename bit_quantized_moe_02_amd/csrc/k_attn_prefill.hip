@@ -11,7 +11,13 @@ namespace {
 
 constexpr int kTile = 64;                   // keys a workgroup stages at once
 constexpr int kWaves = 4;
-constexpr float kLazy = 8.f;                // how far a score may exceed the running maximum, in powers of 2
+// A row's weights are powers of two above a reference.  It is put 2^kHead under
+// the largest score so far, and raised only when a score would exceed it by 2^kMost:
+// the sums are hardly ever rescaled, and weights stay in fp16's range (up to 65504)
+// while its smallest number, 2^-24, is at most 2^-34 of the row's largest weight
+// (with a reference at the maximum itself, 2^-24: 4000 keys 2^-24.4 beside one that has
+// no value were a third off).
+constexpr float kHead = 10.f, kMost = 15.f;
 constexpr int kThreads = 64 * kWaves;
 
 // K and V rows lie in LDS as they do in memory, 2*D bytes each, their
@@ -83,7 +89,7 @@ template <typename T, int D>
 struct Rows {
   u32x4 q[D / 16];
   f32x16 o[D / 32];
-  float m, l;
+  float m, l;                               // reference, sum of the weights
   int last;                                 // last key the row sees, -1: none
 };
 
@@ -116,11 +122,11 @@ struct Weights {
   u32x4 p[4];
 };
 
-// Scores as powers of two under the running maximum, in place; says whether
-// some row's maximum has to be raised, and gives the tile's.  It is only
-// raised when a score exceeds it by 2^8 (or a row has none yet): the weights
-// are then at most 2^8, which costs no precision, and the sums are hardly ever
-// rescaled.
+// Scores as powers of two above the reference, in place; says whether some
+// row's has to be raised, and gives the tile's largest.  (32-bit: an exponent is
+// good to 2^-24 of how far apart score and reference are, as its score is to
+// 2^-24 of itself.  Raising first, with exponents made once, costs 2.5%: 2048 rows
+// behind 6144 keys 224 us, 229.)
 // Masked, partly: some row of the workgroup does not see some key of the tile.
 template <bool Masked, typename T, int D>
 __device__ __forceinline__ bool exponents(const Rows<T, D>& R, Scores& S, float& mx, int j0, bool partly, float c,
@@ -144,13 +150,13 @@ __device__ __forceinline__ bool exponents(const Rows<T, D>& R, Scores& S, float&
     m[i] = fmaxf(m[i], S.s[i][15]);
   }
   mx = max_halves(fmaxf(m[0], m[1]));
-  return __any(mx > kLazy || (R.m == kMinusInf && mx > kMinusInf));
+  return __any(mx > kMost || (R.m == kMinusInf && mx > kMinusInf));
 }
 
 template <typename T, int D>
-__device__ __forceinline__ void raise_maximum(Rows<T, D>& R, Scores& S, float mx) {
-  const bool raise = mx > kLazy || (R.m == kMinusInf && mx > kMinusInf);
-  const float d = raise ? mx : 0.f;
+__device__ __forceinline__ void raise_reference(Rows<T, D>& R, Scores& S, float mx) {
+  const bool raise = mx > kMost || (R.m == kMinusInf && mx > kMinusInf);
+  const float d = raise ? mx - kHead : 0.f;
   const float r = !raise ? 1.f : R.m == kMinusInf ? 0.f : exp2_fast(-d);
   if (raise) R.m = (R.m == kMinusInf ? 0.f : R.m) + d;
   R.l *= r;
@@ -291,7 +297,7 @@ __device__ __forceinline__ bool step(Rows<T, D>& R, Scores& S, Weights& W, const
       __builtin_amdgcn_sched_group_barrier(0x002, D == 64 ? 7 : 4, 0);
     }
   }
-  if (raise) raise_maximum<T, D>(R, S, mx);
+  if (raise) raise_reference<T, D>(R, S, mx);
   weights<T, D>(R, S, W);
   if (!Masked || t + 1 < t1) scores<T, D>(R, S, k_next, lane);
   // (the weights are made here, among the products, not where they are used)

@@ -205,8 +205,10 @@ typedef struct moe_packed {
 size_t moe_attn_prefill_workspace_bytes(const moe_packed* p);
 
 /* Attention of packed sequences: as moe_attn_decode, with k and v rows in
- * place of the cache, and the weights p of one tile rounded to the row type
- * (half a step of each).  causal != 0: query row i of n sees key rows
+ * place of the cache, and the weights p rounded to the row type: half a step
+ * of each, fp16's below 2^-24 of the row's largest to a multiple of 2^-34 of it.
+ * Scores are 32-bit sums, good to 2^-24 of the largest |score| among a row's
+ * keys.  causal != 0: query row i of n sees key rows
  * j <= m - n + i of the sequence's m (aligned at the end: a chunk's rows come
  * last; with n > m the first n - m rows see nothing); else all m.  rows_k may
  * be 0 (k and v are not read then).  out, lse and ws as above. */

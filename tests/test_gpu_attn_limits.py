@@ -153,3 +153,37 @@ def test_decode_many_small_weights_beside_a_large_one(q, dt, width):
     K, V, _ = cache.read(table[0], 0, L)
     ref, rl, mag, smag = A.attention(f64(qt), K, V, np.ones((1, L), bool), scale)
     check_attention(out, lse, ref, rl, *_split_bounds(dt, D, ref, mag, smag, L), "small weights")
+
+
+# ---------------------------------------------------------------------------
+# packed prompts
+
+
+def _prefill(q, qt, kt, vt, ns, ms, scale, causal=True):
+    T, Hq, D = qt.shape
+    out, lse = torch.full_like(qt, 9.0), torch.full((T, Hq), 9.0, device="cuda")
+    ws = torch.full((q.moe_attn_prefill_workspace_bytes(T, len(ns), max(ns), kt.shape[0], Hq, kt.shape[1], D),), 0xFF, dtype=torch.uint8,
+                    device="cuda")
+    q.moe_attn_prefill(qt, kt, vt, i32(cu_of(ns)), i32(cu_of(ms)), max(ns), out, ws, scale, causal, lse)
+    torch.cuda.synchronize()
+    return out, lse
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_prefill_many_small_weights_beside_a_large_one(q, D, dt):
+    """As in decode: the weights are rounded to the row type, fp16's as multiples of at most 2^-34 of the
+    largest, so that small ones keep their bits."""
+    dt = DT[dt]
+    n, L, heads = 2, 4097, 64
+    kt = torch.zeros((L, heads, D), dtype=dt, device="cuda")
+    vt = torch.full((L, heads, D), 40.0, dtype=dt, device="cuda")
+    qt = torch.zeros((n, heads, D), dtype=dt, device="cuda")
+    kt[0, :, 0], vt[0], qt[:, :, 0] = 16.0, 0.0, 1.0
+    scale = 24.4 * np.log(2) / 16
+    out, lse = _prefill(q, qt, kt, vt, [n], [L], scale)
+    seen = np.arange(L)[None] <= (L - n + np.arange(n))[:, None]
+    ref, rl, mag, smag = A.attention(f64(qt), f64(kt), f64(vt), seen, scale)
+    # half a multiple of 2^-34 for each of L weights, of values 40
+    tol, tl = attention_bounds(dt, D, np.zeros(1), ref, mag, smag, L)
+    check_attention(out, lse, ref, rl, tol + 2.0 ** -35 * 40 * L, tl, "small weights")
