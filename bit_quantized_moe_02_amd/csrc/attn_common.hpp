@@ -43,6 +43,7 @@ struct Bf16 {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
   }
   static constexpr uint32_t kExpOne = 0x7F80u;
+  static constexpr int kOver = 120;         // codes times 2^kOver may leave the type's range
   // acc + lo^2 + hi^2
   static __device__ __forceinline__ float square2(uint32_t w, float acc) {
     const bf16x2 v = __builtin_bit_cast(bf16x2, w);
@@ -69,6 +70,7 @@ struct F16 {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
   }
   static constexpr uint32_t kExpOne = 0x7C00u;
+  static constexpr int kOver = 8;
   static __device__ __forceinline__ float square2(uint32_t w, float acc) {
     const f16x2 v = __builtin_bit_cast(f16x2, w);
     return __builtin_amdgcn_fdot2(v, v, acc, false);

@@ -391,6 +391,20 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int nb) 
   }
 }
 
+// Whether codes times this scale (the wave's) may leave the row type's range, and then two
+// values of which an infinite one becomes the type's largest (a code is never
+// infinite: its row was finite, at most half a step of the code away).
+template <typename T>
+__device__ __forceinline__ bool may_leave(float scale) {
+  return (__builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, scale)) >> 23 & 0xFF) >= 127 + T::kOver;
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t kept_finite(uint32_t w) {
+  const uint32_t lo = (w & 0x7FFFu) == T::kExpOne ? 1u : 0u, hi = (w >> 16 & 0x7FFFu) == T::kExpOne ? 0x10000u : 0u;
+  return w - lo - hi;
+}
+
 // One wave takes one block of one sequence and head: the K codes go out as
 // they lie (a lane holds 8 consecutive columns of one token), the V codes
 // through a transposing tile in LDS, so that rows are written 16 bytes a lane.
@@ -431,18 +445,32 @@ __global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs a, int nb) {
   const bool on = n >= f && n < e;
   if (on) {
     uint16_t* p = (uint16_t*)a.k_out + (row_of_slot0 + n) * a.kos + (int64_t)h * D + 8 * g;
+    const bool k_over = may_leave<T>(sk);
 #pragma unroll
     for (int q = 0; q < D / 64; ++q) {
-      *reinterpret_cast<u32x4*>(p + 64 * q) = dec8<T>(kw[q].x, kw[q].y, sk);
-      *reinterpret_cast<u32x4*>(p + 64 * q + 32) = dec8<T>(kw[q].z, kw[q].w, sk);
+      u32x4 x = dec8<T>(kw[q].x, kw[q].y, sk), y = dec8<T>(kw[q].z, kw[q].w, sk);
+      if (k_over) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[i] = kept_finite<T>(x[i]);
+          y[i] = kept_finite<T>(y[i]);
+        }
+      }
+      *reinterpret_cast<u32x4*>(p + 64 * q) = x;
+      *reinterpret_cast<u32x4*>(p + 64 * q + 32) = y;
     }
   }
+  const bool v_over = may_leave<T>(sv);
 #pragma unroll
   for (int q = 0; q < D / 64; ++q) {
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       const uint32_t word = w == 0 ? vw[q].x : w == 1 ? vw[q].y : w == 2 ? vw[q].z : vw[q].w;
-      const uint32_t x = T::dec2(word, sv, false), y = T::dec2(word, sv, true);
+      uint32_t x = T::dec2(word, sv, false), y = T::dec2(word, sv, true);
+      if (v_over) {
+        x = kept_finite<T>(x);
+        y = kept_finite<T>(y);
+      }
       const int d = 64 * q + 16 * w + n;
       vt[wave][4 * g][d] = (uint16_t)x;
       vt[wave][4 * g + 1][d] = (uint16_t)(x >> 16);

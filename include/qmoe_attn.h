@@ -157,7 +157,8 @@ int moe_kv_append(const moe_kv_cache* cache, const moe_kv_batch* batch, const mo
 
 /* The step's positions out of the cache, as rows (with as many rows as a
  * sequence has positions, its whole context): code * scale, rounded to the
- * row type.  Negative positions read as zeros.  Here rows need not be new
+ * row type; beyond its range its largest number (65504 has code 256 at scale
+ * 256).  Negative positions read as zeros.  Here rows need not be new
  * ones, only the sequence's last. */
 int moe_kv_read(const moe_kv_cache* cache, const moe_kv_batch* batch, int dtype, void* k_out,
                 int64_t k_out_stride, void* v_out, int64_t v_out_stride, void* stream);

@@ -155,6 +155,34 @@ def test_decode_many_small_weights_beside_a_large_one(q, dt, width):
     check_attention(out, lse, ref, rl, *_split_bounds(dt, D, ref, mag, smag, L), "small weights")
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_read_of_values_next_to_the_types_largest(q, D, dt):
+    """Finite rows come back finite: what its code rounds past the row type's range reads as its largest number;
+    infinities and NaN as not a number."""
+    dt = DT[dt]
+    rng = np.random.default_rng(65)
+    Hk, page, L = 3, 32, 50
+    big = torch.finfo(dt).max
+    table, n_pages = page_table(rng, [L], page)
+    cache = A.Cache(*random_cache(rng, n_pages, page, Hk, D), page, Hk, D)
+    dev = to_device(q, cache)
+    kt, kv = rows_in(rng, L, Hk, D, dt, sigma=big / 8)
+    vt, vv = rows_in(rng, L, Hk, D, dt, sigma=big / 8)
+    kt[3, 1], vt[20, 0, ::3], vt[49, 2, 1::2] = big, -big, big
+    kt[3, 1, 7], vt[20, 0, 1] = float("inf"), float("nan")
+    batch = q.KvBatch(i32(table), i32([L]), L)
+    q.moe_kv_append(dev, batch, kt, vt)
+    cache = A.Cache(dev.codes.cpu().numpy(), f64(dev.scales), page, Hk, D)
+    back = [torch.zeros_like(kt), torch.zeros_like(vt)]
+    q.moe_kv_read(dev, batch, *back)
+    for x, got, want in zip((kt, vt), back, cache.read(table[0], 0, L)):
+        assert np.nanmax(np.abs(want)) > big
+        want = np.clip(want, -big, big)                 # (codes times powers of two: exact in the row type)
+        assert np.array_equal(f64(got), want, equal_nan=True)
+        assert torch.equal(got.isfinite(), x.isfinite())
+
+
 # ---------------------------------------------------------------------------
 # packed prompts
 
