@@ -5,7 +5,8 @@ becomes a QmoeError carrying moe_last_error().  Every computation happens in
 the library's kernels or its host quantizer.
 
 Import torch before this module (the library then shares torch's HIP
-runtime); a missing libqmoe.so or _attn.so raises at import time.
+runtime); a missing libqmoe.so raises at import time, a missing _attn.so when
+one of the attention calls that need it is made.
 """
 from __future__ import annotations
 
@@ -16,10 +17,21 @@ import numpy as np
 
 import torch
 
+
+class _NotBuilt:
+    """Stands for a module that is missing or does not load: its calls say so."""
+
+    def __init__(self, name, why):
+        self._name, self._why = name, why
+
+    def __getattr__(self, call):
+        raise ImportError(f"{self._name} does not load ({self._why}); run `python -m bit_quantized_moe_02_amd.build`")
+
+
 try:
     from . import _attn
-except ImportError as e:
-    raise ImportError("_attn.so is not built; run `python -m bit_quantized_moe_02_amd.build`") from e
+except ImportError as e:                       # (the calls of the expert layer do not need it)
+    _attn = _NotBuilt("_attn.so", str(e))
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # QMOE_LIB names another build of the same library (the host-sanitizer build
@@ -480,11 +492,14 @@ class ExpertCache:
 
 _DTYPE = {torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16}
 
-_attn.use(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
-            for f in ("moe_kv_append", "moe_kv_read", "moe_attn_decode", "moe_attn_prefill")))
+if not isinstance(_attn, _NotBuilt):
+    _attn.use(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
+                for f in ("moe_kv_append", "moe_kv_read", "moe_attn_decode", "moe_attn_prefill")))
 
-# index of the current device, where the library launches
-_device = torch._C._cuda_getDevice
+# index of the current device, where the library launches, and its current
+# stream's address: by torch's short ways, where it has them
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _here(t, name, dev):
@@ -527,7 +542,7 @@ def _heads(t):
 
 
 def _stream_on(stream, dev):
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    return _current_stream(dev) if stream is None else _stream(stream)
 
 
 def moe_kv_code_bytes(n_pages: int, page_tokens: int, kv_heads: int, head_dim: int) -> int:
