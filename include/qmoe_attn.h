@@ -53,7 +53,7 @@ extern "C" {
  *   So one 16-byte load per lane is the matrix core's operand.
  * scales: float [n_pages][kv_heads][page_tokens/16][2]: the scales of the
  *   block's K and V; value = code * scale.  moe_kv_append writes powers of
- *   two, and the readers use the exponent only.
+ *   two from 2^-64 to 2^121, and the readers use the exponent only.
  */
 typedef struct moe_kv_cache {
   int32_t n_pages;
@@ -124,7 +124,7 @@ typedef struct moe_rope {
  * (Scaling rules: Chen et al. 2023, "Extending Context Window of Large
  * Language Models via Positional Interpolation"; Peng et al. 2023, "YaRN".)
  * MOE_ERR_INVALID_ARG for rot_dim not a positive multiple of 16 (<= 256),
- * base <= 1, factor < 1, PARTS without 0 <= slow < fast and trained > 0, BASE
+ * base <= 1, factor < 1 (but for PLAIN, which has none), PARTS without 0 <= slow < fast and trained > 0, BASE
  * with rot_dim < 4, numbers not finite, an unknown rule or NULL. */
 int moe_rope_freqs(int32_t rot_dim, double base, int rule, double factor, double trained, double slow,
                    double fast, double* freqs_out);
@@ -136,20 +136,26 @@ int moe_rope_freqs(int32_t rot_dim, double base, int rule, double factor, double
  *           no q.
  *   k_out   the turned k rows, rounded once to the row type (may be k
  *           itself); NULL: not wanted.
- * q is turned in 32 bits, k in 64; k_out and the codes are the turned values
- * rounded once (nearest, ties to even).  Scale of a block's K (or V): the least power
- * of two s with |x| <= 448 s for every finite x of the block's tokens so far,
- * not below 2^-64.  A token that needs a larger scale than its block has
- * makes the earlier tokens' codes of that block be divided by the growth
- * and rounded again (exact but for values below 2^-6 of the new scale).
+ * q is turned in 32 bits; k in 64, with sines and cosines good to 2^-40, and
+ * k_out and the codes are the turned values rounded once (nearest, ties to
+ * even).  Scale of a block's K (or V): the least power of two s, not below 2^-64,
+ * with |x| <= 448 s for every finite x that was appended to the block since its
+ * first slot was last written.  Tokens that were cut off again (a rejected
+ * draft: kv_lens goes back, and the next step overwrites them) count among
+ * those: the block keeps the scale they made it need, and its earlier tokens
+ * the second rounding, until its first slot is written again.  (Where a
+ * rejected draft must leave no trace, put the block's codes and scales back as
+ * they were before it.)  A token that needs a larger scale than its block has
+ * makes the earlier tokens' codes of that block be divided by the growth and
+ * rounded again (exact but for values below 2^-6 of the new scale).
  * Infinities and NaN become the code for not a number.  The first slot of a
  * block starts a new scale, so pages may be reused without clearing.  Slots
  * behind the new tokens are left as they are.
  * Rows at negative positions (more rows than kv_lens) are turned but not
  * appended.  Two sequences of one step must not append to the same page
  * (they may share pages that neither appends to), nor one sequence to a page
- * that its table names twice.  q_out, k_out and the
- * inputs must not overlap otherwise. */
+ * that its table names twice.  q_out, k_out and the inputs must not overlap
+ * otherwise. */
 int moe_kv_append(const moe_kv_cache* cache, const moe_kv_batch* batch, const moe_rope* rope, int dtype,
                   const void* q, int64_t q_stride, int32_t q_heads, const void* k, int64_t k_stride,
                   const void* v, int64_t v_stride, void* q_out, int64_t q_out_stride, void* k_out,
