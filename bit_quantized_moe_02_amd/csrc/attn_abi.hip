@@ -20,6 +20,7 @@ constexpr int64_t kMaxRows = 1 << 24;       // rows of a call
 constexpr int64_t kMaxStride = 1 << 24;     // elements: a tile's offsets then fit 32 bits
 constexpr int64_t kMaxGrid = (1 << 24) - 1; // workgroups of 256 threads: 32-bit thread numbers
 constexpr int64_t kMaxBatch = 1 << 20;
+constexpr float kLog2e = 1.4426950408889634f;
 
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
@@ -104,6 +105,9 @@ int check_cache(const char* who, const moe_kv_cache* c, const moe_kv_batch* b, K
   if ((int64_t)a->B * (a->max_new / 16 + 2) > kMaxGrid) return bad(who, "batch * max_new is too large");
   return MOE_OK;
 }
+
+// (the kernels' factor of scores is scale * log2(e))
+bool scale_ok(float scale) { return scale > 0 && isfinite(scale * kLog2e); }
 
 int check_heads(const char* who, int q_heads, int kv_heads) {
   if (q_heads < 1 || q_heads > 4096 || q_heads % kv_heads != 0)
@@ -272,7 +276,7 @@ extern "C" int moe_attn_decode(const moe_kv_cache* cache, const moe_kv_batch* ba
   if ((rc = check_dtype(who, dtype)) != MOE_OK) return rc;
   if ((rc = check_rows(who, "q", q, q_stride, q_heads, a.kv.D)) != MOE_OK) return rc;
   if ((rc = check_rows(who, "out", out, out_stride, q_heads, a.kv.D)) != MOE_OK) return rc;
-  if (!(scale > 0) || !isfinite(scale)) return bad(who, "scale must be positive and finite");
+  if (!scale_ok(scale)) return bad(who, "scale must be positive, and finite times log2(e)");
   if (!aligned4(lse)) return bad(who, "lse must be 4-byte aligned");
   if (!ws || !aligned16(ws)) return bad(who, "ws must be 16-byte aligned memory");
   const int n = attn_decode_workers(a.kv, q_heads, n_cus());
@@ -285,7 +289,7 @@ extern "C" int moe_attn_decode(const moe_kv_cache* cache, const moe_kv_batch* ba
   a.qs = q_stride;
   a.os = out_stride;
   a.Hq = q_heads;
-  a.c = scale * 1.4426950408889634f;
+  a.c = scale * kLog2e;
   a.split = {(float*)((uint8_t*)ws + w.o), (float*)((uint8_t*)ws + w.ml), (int2*)((uint8_t*)ws + w.where), n};
   hipError_t e = launch_attn_decode(a, dtype, (hipStream_t)stream);
   return e == hipSuccess ? MOE_OK : hip_fail(who, e);
@@ -357,7 +361,7 @@ extern "C" int moe_attn_prefill(const moe_packed* p, int dtype, const void* q, i
     if ((rc = check_rows(who, "v", v, v_stride, a.Hk, a.D)) != MOE_OK) return rc;
   }
   if ((rc = check_rows(who, "out", out, out_stride, a.Hq, a.D)) != MOE_OK) return rc;
-  if (!(scale > 0) || !isfinite(scale)) return bad(who, "scale must be positive and finite");
+  if (!scale_ok(scale)) return bad(who, "scale must be positive, and finite times log2(e)");
   if (!aligned4(lse)) return bad(who, "lse must be 4-byte aligned");
   if (!ws || !aligned16(ws)) return bad(who, "ws must be 16-byte aligned memory");
   const int n = attn_prefill_parts(a, n_cus());
@@ -373,7 +377,7 @@ extern "C" int moe_attn_prefill(const moe_packed* p, int dtype, const void* q, i
   a.ks = k_stride;
   a.vs = v_stride;
   a.os = out_stride;
-  a.c = scale * 1.4426950408889634f;
+  a.c = scale * kLog2e;
   a.causal = causal != 0;
   a.split = {(float*)((uint8_t*)ws + w.o), (float*)((uint8_t*)ws + w.ml), nullptr, n};
   hipError_t e = launch_attn_prefill(a, dtype, (hipStream_t)stream);

@@ -178,6 +178,7 @@ size_t moe_attn_decode_workspace_bytes(const moe_kv_cache* cache, const moe_kv_b
  * values already appended) over its cached positions:
  *   out[r,h] = sum_j p_j V_j, p = softmax_j(scale q[r,h] . K_j), over the
  *   positions j <= the row's own; a row with none of them gives zeros.
+ * scale: positive, scale * log2(e) finite.
  * lse (device float [rows][q_heads], NULL: not wanted): log sum_j
  * exp(scale q . K_j), -inf for an empty row.  Codes and scales enter the
  * products exactly, whatever the row type's range is; a weight p is held to
