@@ -159,22 +159,24 @@ constexpr float kVDown = 0x1p-32f, kVUp = 0x1p32f;
 // are exact: K's are the codes themselves, their scale in the score's factor,
 // V's are bf16 numbers whatever the row type is (fp16 ends at 65504, and a code
 // times its scale does not), and a weight is the sum of two bf16 numbers, its
-// rounded value and what that leaves, good to 2^-16: the second products are
-// hidden by the loads.  HBM bounds
-// it, so a wave's loads never stop: the next step's K codes are asked for as
-// soon as this step's are in the first product, its V codes after the second.
-// (Two steps ahead holds twice the registers and gains nothing: 16 drafts of
-// up to 3 tokens 28.2 us a call, one step 26.0.)
+// rounded value and what that leaves, good to 2^-16.  (One product of rounded
+// weights: 777 positions 6.6 us a call, 6.9 with both, 8 contexts of 16384, 32
+// tokens each, heads of 128, 135 and 153, long contexts the same; bf16 outputs
+// were then 0.0021 to 0.0024 of their size off, 0.0017 with both, which is their
+// own rounding.)
+// HBM bounds it, so a wave's loads never stop: the next step's K codes are asked
+// for as soon as this step's are in the first product, its V codes after the
+// second.  (Two steps ahead holds twice the registers and gains nothing: 16
+// drafts of up to 3 tokens 28.2 us a call where one step took 26.0.)
 //
 // One context of 131071, 8 key heads of 128: 269 MB in 45 us, 6.0 TB/s; 64 of
 // up to 8192: 603 MB in 99 us, 6.1 TB/s (the copy reaches 4.7, reading and
 // writing).  16 drafts of up to 3 tokens, 64 + 8 heads, contexts up to 4099: 85
-// MB in 22 us: five rounds a wave, each of its steps' latencies one after the
+// MB in 23 us: five rounds a wave, each of its steps' latencies one after the
 // other, and what comes before the first.
 //
 // Short: a workgroup of 8 waves takes a whole sequence, so that there is no
-// join to launch (777 positions, 8 key heads: 6 us, parts and join 8.6 us and
-// a second launch).
+// join to launch (768 positions, 8 key heads: 6.8 us a call, parts and join 7.9).
 template <typename T, int D, int NR, bool Short>
 __global__ __launch_bounds__(64 * (Short ? kShortWaves : kWaves), Short ? 1 : occupancy(D, NR)) void decode_kernel(DecodeArgs a) {
   constexpr int NW = Short ? kShortWaves : kWaves;
@@ -551,18 +553,20 @@ int rows_of(const KvArgs& kv, int Hq) { return kv.max_new * (Hq / kv.Hk); }
 // Row tiles of 16 a workgroup takes: two serve up to 32 rows with one read of
 // the codes and leave room for two workgroups a compute unit.  More rows go to
 // neighbours in the grid's third dimension, which find the codes in the
-// caches: 8 contexts of 16384, 32 tokens each, 32 + 8 heads of 64, 91 us (one
-// tile a workgroup 116, four, at one workgroup a compute unit, 110); heads of
-// 128 133 us (249, 131).
+// caches: 8 contexts of 16384, 32 tokens each, 32 + 8 heads of 64, 118 us (one
+// tile a workgroup 146); heads of 128 153 us (252).  (Four tiles, at one workgroup
+// a compute unit, were no better.)
 int row_tiles(const KvArgs& kv, int Hq) { return rows_of(kv, Hq) <= 16 ? 1 : 2; }
 
 // Whether contexts (by the page table) are taken whole: up to six rounds of a
-// workgroup's waves, where even one sequence alone loses nothing by it (1536
-// positions, 32 + 8 heads of 128: 9.2 us, parts and join 9.4; 16 sequences
-// 11.5 and 14.1).  Two tiles of the widest rows do not fit the registers of 8
-// waves.
+// workgroup's waves, or four where the workgroups would leave most of the card
+// idle (us a call whole, and cut into parts and joined; 32 + 8 heads of 128, of
+// 1024, 1280 and 1536 positions: one sequence 7.8, 8.9, 10.0 and 7.9, 8.2, 8.3; four
+// 7.9, 9.1, 10.0 and 8.4, 9.8, 10.4; 16 8.5, 10.1, 11.6 and 11.4, 13.6, 14.6).  Two
+// tiles of the widest rows do not fit the registers of 8 waves.
 bool is_short(const KvArgs& kv, int nr) {
-  return kv.max_len <= 6 * kShortWaves * kStep && nr * kv.D <= 256 && kv.B <= 65535;
+  const int rounds = (int64_t)kv.B * kv.Hk >= 32 ? 6 : 4;
+  return kv.max_len <= rounds * kShortWaves * kStep && nr * kv.D <= 256 && kv.B <= 65535;
 }
 
 template <typename T, int D>

@@ -187,7 +187,14 @@ size_t moe_attn_decode_workspace_bytes(const moe_kv_cache* cache, const moe_kv_b
  * its range gives infinity).  Meant for few rows a sequence
  * (1..16 in decoding and draft verification; any number works).  ws: device
  * scratch, no initialization needed; calls that overlap in time need one each.
- * out and lse must not overlap the inputs. */
+ * out and lse must not overlap the inputs.
+ * pages_per_seq * page_tokens, and not what kv_lens holds, chooses how contexts
+ * are taken: up to 1024 positions (1536 where batch * kv_heads >= 32) by one
+ * workgroup each, wider tables cut into ranges and joined by a second launch.
+ * A program whose table has the width of its longest possible context may
+ * describe the first pages of each row only (a smaller pages_per_seq with the
+ * same table_stride) where they hold all the contexts of a step: one context of
+ * 777 positions is then 7.6 us a call, 9.3 with a table of 32768. */
 int moe_attn_decode(const moe_kv_cache* cache, const moe_kv_batch* batch, int dtype, const void* q,
                     int64_t q_stride, int32_t q_heads, float scale, void* out, int64_t out_stride, float* lse,
                     void* ws, size_t ws_bytes, void* stream);
