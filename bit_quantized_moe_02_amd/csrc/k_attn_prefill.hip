@@ -322,9 +322,9 @@ __device__ __forceinline__ bool step(Rows<T, D>& R, Scores& S, Weights& W, const
 // in two LDS buffers: the next tile is on its way while one is computed.
 //
 // Bound by the card's power with heads of 128: 2048 rows behind 6144 keys, 32 + 8
-// heads, 240 GFLOP in 224 us, 1.07 PFLOP/s; with zeros for inputs 164 us, since
+// heads, 240 GFLOP in 224 us, 1.07 PFLOP/s; with zeros for inputs 161 us, since
 // the clock falls to some 1.6 GHz under random ones (the library's largest
-// product: 1.34 and 1.80 PFLOP/s).  With heads of 64 the vector unit does as
+// product: 1.35 and 1.79 PFLOP/s).  With heads of 64 the vector unit does as
 // much for half the products: 8 prompts of up to 2048, 32 + 4 heads, 104 us,
 // 666 TFLOP/s, vector unit busy 61%, matrix core 33%.  A short prompt waits: one
 // tile 6.0 us, each one more about 1 (2100 cycles for a wave alone on its SIMD,
