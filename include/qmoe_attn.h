@@ -53,7 +53,8 @@ extern "C" {
  *   So one 16-byte load per lane is the matrix core's operand.
  * scales: float [n_pages][kv_heads][page_tokens/16][2]: the scales of the
  *   block's K and V; value = code * scale.  moe_kv_append writes powers of
- *   two from 2^-64 to 2^121, and the readers use the exponent only.
+ *   two from 2^-64 to 2^121, whatever else fills a cache keeps to that range, and
+ *   the readers use the exponent only.
  */
 typedef struct moe_kv_cache {
   int32_t n_pages;

@@ -125,6 +125,36 @@ def test_append_far_positions_code_by_code(q, dt, inter):
     _same(dev, ref)
 
 
+@pytest.mark.parametrize("width", [1040, 1296, 1536, 1552])
+@pytest.mark.parametrize("B", [1, 16])
+def test_decode_by_the_tables_width(q, B, width):
+    """Contexts next to where they are taken whole and where they are cut, few sequences and many, and a narrower view of
+    a wide table: each right."""
+    rng = np.random.default_rng(74)
+    Hq, Hk, D, page, dt = 4, 2, 64, 16, torch.bfloat16
+    lens = [1030] + [int(x) for x in rng.integers(0, 1030, B - 1)]
+    table, n_pages = page_table(rng, lens, page, width=width // page)
+    cache = A.Cache(*random_cache(rng, n_pages, page, Hk, D), page, Hk, D)
+    dev = to_device(q, cache)
+    qt, qv = rows_in(rng, B, Hq, D, dt, sigma=2.0)
+    wide = torch.full((B, 4096), -1, dtype=torch.int32, device="cuda")
+    wide[:, :width // page] = i32(table)
+    got = []
+    for t in (i32(table), wide[:, :width // page], wide):
+        batch = q.KvBatch(t, i32(lens), B)
+        out, lse = torch.full_like(qt, 9.0), torch.full((B, Hq), 9.0, device="cuda")
+        ws = torch.full((q.moe_attn_decode_workspace_bytes(dev, batch, Hq),), 0xFF, dtype=torch.uint8, device="cuda")
+        q.moe_attn_decode(dev, batch, qt, out, ws, D ** -0.5, lse)
+        got.append((out, lse))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    for b, length in enumerate(lens):
+        K, V, _ = cache.read(table[b], 0, length)
+        ref, rl, mag, smag = A.attention(qv[b:b + 1], K, V, np.ones((1, length), bool), D ** -0.5)
+        bounds = attention_bounds(dt, D, V, ref, mag, smag, length)
+        for out, lse in got[1:]:
+            check_attention(out[b:b + 1], lse[b:b + 1], ref, rl, *bounds, f"sequence {b}")
+
+
 @pytest.mark.parametrize("n_keys", [60, 6000])          # whole, and cut into parts
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
 @pytest.mark.parametrize("D", [64, 128, 256])

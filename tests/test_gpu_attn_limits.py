@@ -155,6 +155,30 @@ def test_decode_many_small_weights_beside_a_large_one(q, dt, width):
     check_attention(out, lse, ref, rl, *_split_bounds(dt, D, ref, mag, smag, L), "small weights")
 
 
+@pytest.mark.parametrize("width", WIDTHS)
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("rise", [1.0, 6.0, 40.0])
+def test_decode_scores_that_rise(q, dt, width, rise):
+    """Scores that rise (and, for another head, fall) by 2^rise from one 32 positions to the next."""
+    dt = DT[dt]
+    rng = np.random.default_rng(66)
+    D, Hq, Hk, page, L = 128, 2, 1, 16, 1000
+    table, n_pages = _table(rng, [L], page, width)
+    cache = A.Cache(*random_cache(rng, n_pages, page, Hk, D), page, Hk, D)
+    dev = to_device(q, cache)
+    kt, _ = rows_in(rng, L, Hk, D, dt)
+    vt, _ = rows_in(rng, L, Hk, D, dt)
+    qt, _ = rows_in(rng, 1, Hq, D, dt, sigma=0.5)
+    kt[:, :, 0] = (torch.arange(L, device="cuda") // 32 * rise * np.log(2)).to(dt)[:, None]
+    qt[:, 0, 0], qt[:, 1, 0] = 8.0, -8.0
+    q.moe_kv_append(dev, q.KvBatch(i32(table), i32([L]), L), kt, vt)
+    cache = A.Cache(dev.codes.cpu().numpy(), f64(dev.scales), page, Hk, D)
+    out, lse = _decode(q, dev, table, [L], [1], qt, 0.125)
+    K, V, _ = cache.read(table[0], 0, L)
+    ref, rl, mag, smag = A.attention(f64(qt), K, V, np.ones((1, L), bool), 0.125)
+    check_attention(out, lse, ref, rl, *_split_bounds(dt, D, ref, mag, smag, L), f"rise {rise}")
+
+
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_read_of_values_next_to_the_types_largest(q, D, dt):
@@ -215,3 +239,23 @@ def test_prefill_many_small_weights_beside_a_large_one(q, D, dt):
     # half a multiple of 2^-34 for each of L weights, of values 40
     tol, tl = attention_bounds(dt, D, np.zeros(1), ref, mag, smag, L)
     check_attention(out, lse, ref, rl, tol + 2.0 ** -35 * 40 * L, tl, "small weights")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("rise", [1.0, 6.0, 40.0])
+def test_prefill_scores_that_rise(q, D, dt, rise):
+    """As in decode, from one 64 keys to the next: the reference is raised at every tile, at some, and (for the falling
+    head) never."""
+    dt = DT[dt]
+    rng = np.random.default_rng(67)
+    n, L, Hq = 3, 1500, 64
+    kt, _ = rows_in(rng, L, Hq // 2, D, dt)
+    vt, vv = rows_in(rng, L, Hq // 2, D, dt)
+    qt, _ = rows_in(rng, n, Hq, D, dt, sigma=0.5)
+    kt[:, :, 0] = (torch.arange(L, device="cuda") // 64 * rise * np.log(2)).to(dt)[:, None]
+    qt[:, ::2, 0], qt[:, 1::2, 0] = 8.0, -8.0
+    out, lse = _prefill(q, qt, kt, vt, [n], [L], 0.125)
+    seen = np.arange(L)[None] <= (L - n + np.arange(n))[:, None]
+    ref, rl, mag, smag = A.attention(f64(qt), f64(kt), vv, seen, 0.125)
+    check_attention(out, lse, ref, rl, *attention_bounds(dt, D, vv, ref, mag, smag, L), f"rise {rise}")
