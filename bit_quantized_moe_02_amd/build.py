@@ -1,5 +1,5 @@
-"""Builds libqmoe.so (gfx950) and _attn.so, the attention calls' tensor
-arguments from Python, in this package directory.
+"""Builds libqmoe.so (gfx950) and _attn.so, the tensor arguments from Python of
+the attention calls and of those around them, in this package directory.
 
 The host translation unit (quantizer / packer, no HIP) is compiled by the
 host C++ compiler with -ffp-contract=off so its fp64 quantization decisions
@@ -30,9 +30,10 @@ ARCH = os.environ.get("QMOE_ARCH", "gfx950")
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 CXX = os.environ.get("CXX_HOST", shutil.which("g++") or "c++")
 
-HOST_SOURCES = ["host_quant.cpp"]
+HOST_SOURCES = ["host_quant.cpp", "host_linear.cpp"]
 DEVICE_SOURCES = ["abi.hip", "k_route.hip", "k_decode.hip", "k_decode1.hip", "k_decodem.hip", "k_prefill.hip", "k_misc.hip",
-                  "expert_cache.hip", "attn_abi.hip", "k_kv.hip", "k_attn_decode.hip", "k_attn_prefill.hip"]
+                  "expert_cache.hip", "attn_abi.hip", "k_kv.hip", "k_attn_decode.hip", "k_attn_prefill.hip",
+                  "step_abi.hip", "k_norm.hip", "k_linear_bf16.hip", "k_linear_f16.hip", "k_linear_i8.hip", "k_pages.hip"]
 
 HIP_FLAGS = ["-O3", "-fPIC", "-std=c++17", f"--offload-arch={ARCH}",
              "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -79,16 +80,16 @@ def build(verbose: bool = False) -> str:
         # (no Python.h, no torch: the expert layer's calls do without it)
         if os.path.exists(PY_ATTN):
             os.remove(PY_ATTN)
-        print(f"_attn.so was not built, the attention calls will say so from Python: {e}", file=sys.stderr)
+        print(f"_attn.so was not built, the attention and step calls will say so from Python: {e}", file=sys.stderr)
     return LIB
 
 
 def build_py_attn() -> str:
-    """Compiles the Python module that hands the attention calls' tensors to the library (host code only)."""
+    """Compiles the Python module that hands the tensors of the attention and step calls to the library (host code only)."""
     torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
     _run([CXX, "-O2", "-fPIC", "-std=c++17", "-Wall", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
-          "-I", os.path.join(torch_dir, "include"), "-shared", os.path.join(CSRC, "py_attn.cpp"), "-o", PY_ATTN + ".tmp",
-          "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"])
+          "-I", os.path.join(torch_dir, "include"), "-shared", os.path.join(CSRC, "py_attn.cpp"), os.path.join(CSRC, "py_step.cpp"),
+          "-o", PY_ATTN + ".tmp", "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"])
     os.replace(PY_ATTN + ".tmp", PY_ATTN)
     return PY_ATTN
 

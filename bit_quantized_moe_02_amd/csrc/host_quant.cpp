@@ -341,6 +341,9 @@ void pack_tile_bf16(const float* rows, int64_t stride, uint8_t* tile) {
 }
 
 }  // namespace
+
+uint16_t f64_to_f16_rne(double x) { return f64_to_f16(x); }
+double f16_value(uint16_t h) { return f16_to_f64(h); }
 }  // namespace qmoe
 
 using namespace qmoe;

@@ -1,0 +1,259 @@
+// Root-mean-square norm with the residual's addition (moe_rms_norm).
+//
+// Memory bound: each value is read and written once.  A vector stays in
+// registers, 8 columns a thread and pass, between the sum of its squares and the
+// outputs.  Vectors of up to 512 columns take the least power of two of lanes
+// that holds them (several to a wave, no barrier); longer ones a workgroup of 8
+// columns a thread, up to 1024 threads, then two passes of that.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/qmoe_step.h"
+#include "k_step.h"
+
+namespace qmoe {
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+template <int T>
+struct Raw {                       // 8 values of a type
+  u32x4 v[T == MOE_DT_F32 ? 2 : 1];
+};
+
+template <int T>
+__device__ __forceinline__ Raw<T> load8(const void* p, int64_t at) {
+  Raw<T> r;
+  if (T == MOE_DT_F32) {
+    const u32x4* q = (const u32x4*)((const float*)p + at);
+    r.v[0] = q[0];
+    r.v[T == MOE_DT_F32] = q[1];
+  } else {
+    r.v[0] = *(const u32x4*)((const uint16_t*)p + at);
+  }
+  return r;
+}
+
+template <int T>
+__device__ __forceinline__ void to_f32(const Raw<T>& r, float* f) {
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t word = r.v[T == MOE_DT_F32 ? i / 4 : 0][i % 4];    // (a bit cast takes a copy: of a vector's element it reads the first)
+    if (T == MOE_DT_F32) f[i] = __builtin_bit_cast(float, word);
+    else if (T == MOE_DT_BF16) f[i] = __builtin_bit_cast(float, i % 2 ? r.v[0][i / 2] & 0xFFFF0000u : r.v[0][i / 2] << 16);
+    else f[i] = (float)__builtin_bit_cast(_Float16, (uint16_t)(r.v[0][i / 2] >> (16 * (i % 2))));
+  }
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2){a, b}, bf2));
+}
+__device__ __forceinline__ uint32_t f16_pair(float a, float b) {
+  typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2){a, b}, h2));
+}
+
+template <int T>
+__device__ __forceinline__ Raw<T> from_f32(const float* f) {
+  Raw<T> r;
+  if (T == MOE_DT_F32) {
+    for (int i = 0; i < 8; ++i) r.v[i / 4][i % 4] = __builtin_bit_cast(uint32_t, f[i]);
+  } else {
+    for (int i = 0; i < 4; ++i)
+      r.v[0][i] = T == MOE_DT_BF16 ? bf16_pair(f[2 * i], f[2 * i + 1]) : f16_pair(f[2 * i], f[2 * i + 1]);
+  }
+  return r;
+}
+
+template <int T>
+__device__ __forceinline__ void store8(void* p, int64_t at, const Raw<T>& r) {
+  if (T == MOE_DT_F32) {
+    u32x4* q = (u32x4*)((float*)p + at);
+    q[0] = r.v[0];
+    q[1] = r.v[T == MOE_DT_F32];
+  } else {
+    *(u32x4*)((uint16_t*)p + at) = r.v[0];
+  }
+}
+
+__device__ __forceinline__ void store8_as(int type, void* p, int64_t at, const float* f) {
+  if (type == MOE_DT_F32) store8<MOE_DT_F32>(p, at, from_f32<MOE_DT_F32>(f));
+  else if (type == MOE_DT_BF16) store8<MOE_DT_BF16>(p, at, from_f32<MOE_DT_BF16>(f));
+  else store8<MOE_DT_F16>(p, at, from_f32<MOE_DT_F16>(f));
+}
+
+__device__ __forceinline__ void weight8(const NormArgs& a, int col, float* f) {
+  if (!a.w) {
+    for (int i = 0; i < 8; ++i) f[i] = 1.0f;
+  } else if (a.wt == MOE_DT_F32) {
+    to_f32<MOE_DT_F32>(load8<MOE_DT_F32>(a.w, col), f);
+  } else if (a.wt == MOE_DT_BF16) {
+    to_f32<MOE_DT_BF16>(load8<MOE_DT_BF16>(a.w, col), f);
+  } else {
+    to_f32<MOE_DT_F16>(load8<MOE_DT_F16>(a.w, col), f);
+  }
+}
+
+// |y| as an unsigned number, which orders as |y| does, not a number on top.
+__device__ __forceinline__ uint32_t size_bits(float y) { return __builtin_bit_cast(uint32_t, y) & 0x7FFFFFFFu; }
+
+constexpr int kResNone = -1;
+
+// LANES <= 64: that many lanes of a wave take a vector, without LDS; more: a workgroup of
+// LANES threads takes one.  A thread holds 8 columns of each pass of 8 * LANES.
+template <int XT, int RT, int LANES, int PASSES>
+__global__ __launch_bounds__(LANES <= 64 ? 256 : LANES) void norm_kernel(NormArgs a) {
+  constexpr bool kWave = LANES <= 64;
+  constexpr int kWaves = kWave ? 1 : LANES / 64;
+  __shared__ double part[kWave ? 1 : kWaves];
+  __shared__ uint32_t top[kWave ? 1 : kWaves];
+  const int lane = kWave ? threadIdx.x % LANES : threadIdx.x;
+  // (below 2^24 vectors)
+  const uint32_t vec = kWave ? blockIdx.x * (256 / LANES) + threadIdx.x / LANES : blockIdx.x;
+  const bool here = vec < (uint32_t)a.rows * (uint32_t)a.heads;
+  const int row = !here ? 0 : a.heads == 1 ? vec : vec / (uint32_t)a.heads, head = here ? vec - (uint32_t)row * a.heads : 0;
+  const int64_t first = (int64_t)head * a.cols;
+  const int64_t xat = row * a.xs + first, rat = row * a.rs + first;
+
+  constexpr int RTx = RT == kResNone ? XT : RT;
+  Raw<XT> x[PASSES];
+  Raw<RTx> r[PASSES];
+  float h[PASSES][8], w[PASSES][8];
+  bool in[PASSES];
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    const int col = (p * LANES + lane) * 8;
+    in[p] = here && col < a.cols;
+    if (in[p]) {
+      x[p] = load8<XT>(a.x, xat + col);
+      if (RT != kResNone) r[p] = load8<RTx>(a.res, rat + col);
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p)
+    if (in[p]) weight8(a, (p * LANES + lane) * 8, w[p]);
+  double ss = 0;
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    if (in[p]) {
+      to_f32<XT>(x[p], h[p]);
+      if (RT != kResNone) {
+        float f[8];
+        to_f32<RTx>(r[p], f);
+        for (int i = 0; i < 8; ++i) h[p][i] += f[i];
+        const Raw<RTx> s = from_f32<RTx>(h[p]);        // (the norm is of the sum as it is kept)
+        to_f32<RTx>(s, h[p]);
+        if (a.sum) store8<RTx>(a.sum, row * a.ss + first + (p * LANES + lane) * 8, s);
+      }
+    } else {
+      for (int i = 0; i < 8; ++i) h[p][i] = 0, w[p][i] = 0;
+    }
+    for (int i = 0; i < 8; ++i) ss = fma((double)h[p][i], (double)h[p][i], ss);
+  }
+  if (!a.out && !a.codes) return;
+#pragma unroll
+  for (int d = 1; d < (kWave ? LANES : 64); d *= 2) ss += __shfl_xor(ss, d);
+  if (!kWave) {
+    if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = ss;
+    __syncthreads();
+    ss = 0;
+    for (int i = 0; i < kWaves; ++i) ss += part[i];
+  }
+  const double inv = 1.0 / sqrt(ss / a.cols + (double)a.eps);
+
+  if (a.out) {
+    const float f = (float)inv;
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+      if (!in[p]) continue;
+      float y[8];
+      for (int i = 0; i < 8; ++i) y[i] = h[p][i] * f * w[p][i];
+      store8_as(a.ot, a.out, row * a.os + first + (p * LANES + lane) * 8, y);
+    }
+  }
+  if (!a.codes) return;
+
+  // 8 bits: y in 64 bits, its sizes compared as 32-bit numbers (rounding keeps their order)
+  uint32_t m[PASSES];
+  uint32_t all = 0;
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    m[p] = 0;
+    for (int i = 0; i < 8; ++i) m[p] = max(m[p], size_bits((float)((double)h[p][i] * inv * (double)w[p][i])));
+    all = max(all, m[p]);
+  }
+  const int groups = a.group ? (a.cols + a.group - 1) / a.group : 1;
+  if (a.group) {                                       // 128 columns: 16 lanes
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p)
+#pragma unroll
+      for (int d = 1; d < (LANES < 16 ? LANES : 16); d *= 2) m[p] = max(m[p], (uint32_t)__shfl_xor((int)m[p], d));
+  } else {
+#pragma unroll
+    for (int d = 1; d < (kWave ? LANES : 64); d *= 2) all = max(all, (uint32_t)__shfl_xor((int)all, d));
+    if (!kWave) {
+      if (threadIdx.x % 64 == 0) top[threadIdx.x / 64] = all;
+      __syncthreads();
+      for (int i = 0; i < kWaves; ++i) all = max(all, top[i]);
+    }
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) m[p] = all;
+  }
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    if (!in[p]) continue;
+    const int col = (p * LANES + lane) * 8;
+    const bool fine = m[p] < 0x7F800000u;
+    const float scale = fine ? __builtin_bit_cast(float, m[p]) / 127.0f : __builtin_nanf("");
+    const double back = fine && scale > 0 ? 1.0 / (double)scale : 0.0;
+    u32x2 c = {0, 0};
+    for (int i = 0; i < 8; ++i) {
+      // (nothing not finite gets here: back is 0 then, and its product is taken for 0)
+      double q = back == 0.0 ? 0.0 : rint((double)h[p][i] * inv * (double)w[p][i] * back);
+      q = fmin(fmax(q, -127.0), 127.0);
+      c[i / 4] |= ((uint32_t)(int)q & 0xFFu) << (8 * (i % 4));
+    }
+    *(u32x2*)(a.codes + row * a.cs + first + col) = c;
+    const int g = a.group ? col / a.group : 0;
+    if (col == g * (a.group ? a.group : 1)) a.scales[((int64_t)head * groups + g) * a.scs + row] = scale;
+  }
+}
+
+template <int XT, int RT>
+hipError_t launch_types(const NormArgs& a, hipStream_t s) {
+  const int64_t n = (int64_t)a.rows * a.heads;
+#define WAVE(L) norm_kernel<XT, RT, L, 1><<<dim3((unsigned)((n + 256 / L - 1) / (256 / L))), dim3(256), 0, s>>>(a)
+#define GROUP(L, P) norm_kernel<XT, RT, L, P><<<dim3((unsigned)n), dim3(L), 0, s>>>(a)
+  if (a.cols <= 64) WAVE(8);
+  else if (a.cols <= 128) WAVE(16);
+  else if (a.cols <= 256) WAVE(32);
+  else if (a.cols <= 512) WAVE(64);
+  else if (a.cols <= 2048) GROUP(256, 1);
+  else if (a.cols <= 4096) GROUP(512, 1);
+  else if (a.cols <= 8192) GROUP(1024, 1);
+  else GROUP(1024, 2);
+#undef WAVE
+#undef GROUP
+  return hipGetLastError();
+}
+
+template <int XT>
+hipError_t launch_x(const NormArgs& a, hipStream_t s) {
+  if (!a.res) return launch_types<XT, kResNone>(a, s);
+  if (a.rt == MOE_DT_BF16) return launch_types<XT, MOE_DT_BF16>(a, s);
+  if (a.rt == MOE_DT_F16) return launch_types<XT, MOE_DT_F16>(a, s);
+  return launch_types<XT, MOE_DT_F32>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
+  if (a.xt == MOE_DT_BF16) return launch_x<MOE_DT_BF16>(a, s);
+  if (a.xt == MOE_DT_F16) return launch_x<MOE_DT_F16>(a, s);
+  return launch_x<MOE_DT_F32>(a, s);
+}
+
+}  // namespace qmoe

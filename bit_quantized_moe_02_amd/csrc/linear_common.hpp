@@ -1,0 +1,332 @@
+// Products of a few rows with 4-bit weights (moe_linear): the kernel, built
+// for each type of row by k_linear_bf16.hip, k_linear_f16.hip, k_linear_i8.hip.
+//
+// Weight bytes bound it.  A workgroup of 8 waves takes NT tiles of 16 weight rows and all
+// of k: the waves take its tiles of 128 columns in turn, so the workgroup reads
+// one contiguous run of memory, and add their sums up through LDS in wave order (no
+// workspace, no atomics).  A lane's 16 bytes of a tile are its operand of four
+// 16x16x32 products (lane c = 16*g + r: weight row r, 8 columns of each); the rows of
+// x are the other operand, 16 * MT of them at once, read from the caches.
+//
+// Codes enter the products exactly.  16-bit rows: q goes into the upper
+// mantissa bits of 1.0, u = 1 + q/16 (shift, mask, exclusive or: the codes are stored as q ^ 8),
+// and sum_j x_j (q_j - z) = 16 (sum_j x_j u_j - (1 + z/16) sum_j x_j), the sums of x
+// by one more product, with ones.  8-bit rows: 16 (q - 8) is a signed byte
+// already, (q ^ 8) << 4, and sums are whole numbers; those of x are needed only with zero points.
+// A group's sum is scaled once, in 32 bits.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/qmoe_step.h"
+#include "k_step.h"
+
+namespace qmoe {
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+template <int XT>
+struct Types {
+  typedef u32x4 X;                  // 8 values of x: one chunk of 32 columns, one lane
+  typedef f32x4 Acc;
+};
+template <>
+struct Types<MOE_DT_I8> {
+  typedef u32x2 X;
+  typedef i32x4 Acc;
+};
+
+template <int XT>
+__device__ __forceinline__ f32x4 mma16(const u32x4& a, const u32x4& b, const f32x4& c) {
+  if constexpr (XT == MOE_DT_BF16) {
+    typedef __bf16 v8 __attribute__((ext_vector_type(8)));
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+  } else {
+    typedef _Float16 v8 __attribute__((ext_vector_type(8)));
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+  }
+}
+
+// One word of codes (q ^ 8 of columns j at bit 4*(j/2) + 16*(j%2)) as 8 numbers 1 + q/16.
+template <int XT>
+__device__ __forceinline__ u32x4 units(uint32_t w) {
+  constexpr int kAt = XT == MOE_DT_BF16 ? 3 : 6;                    // lowest of the four upper mantissa bits
+  constexpr uint32_t kMask = 0x000F000Fu << kAt;
+  constexpr uint32_t kFlip = (XT == MOE_DT_BF16 ? 0x3F803F80u : 0x3C003C00u) ^ (0x00080008u << kAt);
+  u32x4 r;
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    const int by = kAt - 4 * p;
+    r[p] = ((by >= 0 ? w << (by & 31) : w >> (-by & 31)) & kMask) ^ kFlip;
+  }
+  return r;
+}
+
+// The same as 8 signed bytes 16 (q - 8).
+__device__ __forceinline__ u32x2 bytes(uint32_t w) {
+  const uint32_t lo = (w << 4) & 0xF0F0F0F0u, hi = w & 0xF0F0F0F0u;  // columns 0 4 1 5 and 2 6 3 7
+  return (u32x2){__builtin_amdgcn_perm(hi, lo, 0x06040200u), __builtin_amdgcn_perm(hi, lo, 0x07050301u)};
+}
+
+// Reads past the end of a buffer give zeros and cost no traffic: what lies past the last
+// column, row or tile is read there.  (Offsets are in the vector operand only, which is what is compared with the end.)
+typedef __amdgpu_buffer_rsrc_t Buffer;
+__device__ __forceinline__ Buffer buffer(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, (int)bytes, 0x00027000);
+}
+
+// A tile's share of a lane: codes, and (perhaps with its neighbours') its row's scales and zero points.
+template <int G, bool Z>
+struct Weights {
+  u32x4 q;
+  u32x2 s;                           // fp16 scales of 128 / G groups
+  uint32_t z;                        // bytes z - 8
+};
+
+template <int G, bool Z>
+__device__ __forceinline__ Weights<G, Z> load_weights(Buffer b, uint32_t tile, uint32_t lane) {
+  constexpr int kGroups = 128 / G;
+  const uint32_t r = lane & 15;
+  Weights<G, Z> w;
+  w.q = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, tile + 16 * lane, 0, 0));
+  if constexpr (G == 32) w.s = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(b, tile + 1024 + 8 * r, 0, 0));
+  else w.s = (u32x2){(uint32_t)__builtin_amdgcn_raw_buffer_load_b32(b, tile + 1024 + (G == 64 ? 4 * r : 4 * (r / 2)), 0, 0), 0};
+  w.z = 0;
+  if constexpr (Z)
+    w.z = __builtin_amdgcn_raw_buffer_load_b32(b, tile + 1024 + 32 * kGroups + (G == 32 ? 4 * r : G == 64 ? 4 * (r / 2) : 4 * (r / 4)), 0, 0);
+  return w;
+}
+
+// Scale and z - 8 of group i of the lane's row.
+template <int G, bool Z>
+__device__ __forceinline__ float scale_of(const Weights<G, Z>& w, int i, uint32_t lane) {
+  const uint32_t s = G == 128 ? w.s[0] >> (16 * (lane & 1)) : w.s[i / 2] >> (16 * (i % 2));
+  return (float)__builtin_bit_cast(_Float16, (uint16_t)s);
+}
+template <int G, bool Z>
+__device__ __forceinline__ int zero_of(const Weights<G, Z>& w, int i, uint32_t lane) {
+  const uint32_t z = G == 128 ? w.z >> (8 * (lane & 3)) : G == 64 ? w.z >> (16 * (lane & 1) + 8 * i) : w.z >> (8 * i);
+  return (int)(int8_t)z;
+}
+
+template <int XT>
+__device__ __forceinline__ typename Types<XT>::X load_x(Buffer b, uint32_t at) {
+  if constexpr (XT == MOE_DT_I8) return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(b, at, 0, 0));
+  else return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, at, 0, 0));
+}
+
+// Waves of a workgroup: 16 with 128 registers each, as long as two tiles' operands fit.
+constexpr int waves_of(int mt, int nt) { return mt * nt <= 2 ? 16 : 8; }
+
+// Z: with zero points.  XG: 8-bit rows with a scale for each 128 columns.
+template <int XT, int G, int MT, int NT, bool Z, bool XG>
+__global__ __launch_bounds__(64 * waves_of(MT, NT)) void linear_kernel(LinearArgs a) {
+  constexpr int kWaves = waves_of(MT, NT), kDepth = 2, kGroups = 128 / G;
+  constexpr bool kInt = XT == MOE_DT_I8;
+  constexpr int kXBytes = kInt ? 1 : 2;
+  constexpr uint32_t kTile = 1024 + 32 * kGroups + (Z ? 16 * kGroups : 0);
+  typedef typename Types<XT>::X X;
+  __shared__ f32x4 sums[kWaves][MT * NT][64];
+
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const uint32_t lane = threadIdx.x % 64, r = lane & 15, g = lane >> 4;
+  const int kc_n = (a.k + 127) / 128, rt_n = (a.n + 15) / 16;
+  const int t0 = blockIdx.y * (16 * MT), rt0 = blockIdx.x * NT;
+  Buffer tiles[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+    tiles[i] = buffer(a.w + (int64_t)(rt0 + i) * kc_n * kTile, rt0 + i < rt_n ? kc_n * kTile : 0);
+  // 16 * MT rows of x from t0 on: below 2^31 bytes, as strides are at most 2^24
+  constexpr uint32_t kNoRow = 0x80000000u, kNoColumn = 0x7FFFFFF0u;
+  const int rows = min(a.rows - t0, 16 * MT);
+  const Buffer xs = buffer((const uint8_t*)a.x + (int64_t)t0 * a.x_stride * kXBytes,
+                           (uint32_t)(((rows - 1) * a.x_stride + a.k) * kXBytes));
+  uint32_t xrow[MT], trow[MT];                                       // trow: the lane's 4 rows of the results
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    xrow[m] = (int)(16 * m + r) < rows ? (16 * m + r) * (uint32_t)a.x_stride * kXBytes : kNoRow;
+    trow[m] = (uint32_t)min(t0 + 16 * m + 4 * (int)g, (a.rows - 1) & ~3);
+  }
+
+  Weights<G, Z> w[kDepth][NT];
+  X x[kDepth][MT][4];
+  f32x4 xg[kDepth][XG ? MT : 1];
+  auto load = [&](int d, int i) {                                    // the wave's tile i
+    const int kc = wave + i * kWaves;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) w[d][t] = load_weights<G, Z>(tiles[t], kc * kTile, lane);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int col = kc * 128 + 32 * c + 8 * (int)g;
+      const uint32_t at = col < a.k ? (uint32_t)col * kXBytes : kNoColumn;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) x[d][m][c] = load_x<XT>(xs, xrow[m] + at);
+    }
+    if constexpr (XG) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m) xg[d][m] = *(const f32x4*)(a.xs + min(kc, kc_n - 1) * a.xs_stride + trow[m]);
+    }
+  };
+  f32x4 total[MT][NT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) total[m][t] = (f32x4){0, 0, 0, 0};
+
+  auto add = [&](int d) {
+#pragma unroll
+    for (int gi = 0; gi < kGroups; ++gi) {
+      if constexpr (!kInt) {
+        constexpr uint32_t kOne = XT == MOE_DT_BF16 ? 0x3F803F80u : 0x3C003C00u;
+        const u32x4 one = {kOne, kOne, kOne, kOne};
+        f32x4 acc[MT][NT], accx[MT];
+#pragma unroll
+        for (int c = 0; c < G / 32; ++c) {
+          const int at = gi * (G / 32) + c;
+          u32x4 b[NT];
+#pragma unroll
+          for (int t = 0; t < NT; ++t) b[t] = units<XT>(w[d][t].q[at]);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            accx[m] = mma16<XT>(x[d][m][at], one, c ? accx[m] : (f32x4){0, 0, 0, 0});
+#pragma unroll
+            for (int t = 0; t < NT; ++t) acc[m][t] = mma16<XT>(x[d][m][at], b[t], c ? acc[m][t] : (f32x4){0, 0, 0, 0});
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const float s = 16.0f * scale_of(w[d][t], gi, lane);
+          const float z = Z ? -1.5f - 0.0625f * (float)zero_of(w[d][t], gi, lane) : -1.5f;
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) total[m][t][j] = fmaf(s, fmaf(z, accx[m][j], acc[m][t][j]), total[m][t][j]);
+        }
+      } else {
+        i32x4 acc[MT][NT], accx[MT];
+        if constexpr (G == 32) {
+          long b[NT];
+#pragma unroll
+          for (int t = 0; t < NT; ++t) b[t] = __builtin_bit_cast(long, bytes(w[d][t].q[gi]));
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            const long xv = __builtin_bit_cast(long, x[d][m][gi]);
+            if constexpr (Z) accx[m] = __builtin_amdgcn_mfma_i32_16x16x32_i8(xv, 0x0101010101010101l, (i32x4){0, 0, 0, 0}, 0, 0, 0);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) acc[m][t] = __builtin_amdgcn_mfma_i32_16x16x32_i8(xv, b[t], (i32x4){0, 0, 0, 0}, 0, 0, 0);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < G / 64; ++c) {
+            const int at = gi * (G / 32) + 2 * c;
+            i32x4 b[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              const u32x2 b0 = bytes(w[d][t].q[at]), b1 = bytes(w[d][t].q[at + 1]);
+              b[t] = (i32x4){(int)b0[0], (int)b0[1], (int)b1[0], (int)b1[1]};
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              const u32x2 x0 = x[d][m][at], x1 = x[d][m][at + 1];
+              const i32x4 xv = {(int)x0[0], (int)x0[1], (int)x1[0], (int)x1[1]};
+              const i32x4 one = {0x01010101, 0x01010101, 0x01010101, 0x01010101};
+              if constexpr (Z) accx[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(xv, one, c ? accx[m] : (i32x4){0, 0, 0, 0}, 0, 0, 0);
+#pragma unroll
+              for (int t = 0; t < NT; ++t)
+                acc[m][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(xv, b[t], c ? acc[m][t] : (i32x4){0, 0, 0, 0}, 0, 0, 0);
+            }
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const float s = 0.0625f * scale_of(w[d][t], gi, lane);
+          const int z = Z ? 16 * zero_of(w[d][t], gi, lane) : 0;
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              // (below 2^24 in size: exact)
+              const float v = (float)(Z ? acc[m][t][j] - z * accx[m][j] : acc[m][t][j]);
+              total[m][t][j] = fmaf(XG ? s * xg[d][XG ? m : 0][j] : s, v, total[m][t][j]);
+            }
+        }
+      }
+    }
+  };
+
+  const int steps = (kc_n + kWaves * kDepth - 1) / (kWaves * kDepth);
+#pragma unroll
+  for (int d = 0; d < kDepth; ++d) load(d, d);
+  for (int i = 0; i < steps; ++i) {
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+      // (stages mixed up would need more registers than there are)
+      __builtin_amdgcn_sched_barrier(0);
+      add(d);
+      __builtin_amdgcn_sched_barrier(0);
+      load(d, (i + 1) * kDepth + d);
+    }
+  }
+
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) sums[wave][m * NT + t][lane] = total[m][t];
+  __syncthreads();
+  for (int at = threadIdx.x; at < MT * NT * 256; at += 64 * kWaves) {
+    // consecutive threads: consecutive weight rows
+    const int row = at / (16 * NT), nn = at % (16 * NT);
+    const int m = row / 16, t = nn / 16, l = 16 * (row % 16 / 4) + nn % 16, j = row % 4;
+    const int tok = t0 + row, n = rt0 * 16 + nn;
+    if (tok >= a.rows || n >= a.n) continue;
+    float v = 0;
+#pragma unroll
+    for (int wv = 0; wv < kWaves; ++wv) v += sums[wv][m * NT + t][l][j];
+    if (kInt && !XG) v *= a.xs[tok];
+    if (a.bias) v += a.bias[n];
+    const int64_t to = (int64_t)tok * a.y_stride + n;
+    if (a.y_type == MOE_DT_F32) ((float*)a.y)[to] = v;
+    else if (a.y_type == MOE_DT_BF16) ((__bf16*)a.y)[to] = (__bf16)v;
+    else ((_Float16*)a.y)[to] = (_Float16)v;
+  }
+}
+
+template <int XT, int G, int MT, int NT>
+hipError_t launch_tiles(const LinearArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)(((a.n + 15) / 16 + NT - 1) / NT), (unsigned)((a.rows + 16 * MT - 1) / (16 * MT)));
+  const dim3 block(64 * waves_of(MT, NT));
+  constexpr bool kInt = XT == MOE_DT_I8;
+  if (kInt && a.x_group) {
+    if (a.zeros) linear_kernel<XT, G, MT, NT, true, kInt><<<grid, block, 0, s>>>(a);
+    else linear_kernel<XT, G, MT, NT, false, kInt><<<grid, block, 0, s>>>(a);
+  } else if (a.zeros) {
+    linear_kernel<XT, G, MT, NT, true, false><<<grid, block, 0, s>>>(a);
+  } else {
+    linear_kernel<XT, G, MT, NT, false, false><<<grid, block, 0, s>>>(a);
+  }
+  return hipGetLastError();
+}
+
+template <int XT, int G>
+hipError_t launch_group(const LinearArgs& a, int cus, hipStream_t s) {
+  const bool wide = (a.n + 31) / 32 >= cus;
+  if (a.rows <= 16) return wide ? launch_tiles<XT, G, 1, 2>(a, s) : launch_tiles<XT, G, 1, 1>(a, s);
+  if (a.rows <= 32) return wide ? launch_tiles<XT, G, 2, 2>(a, s) : launch_tiles<XT, G, 2, 1>(a, s);
+  return wide ? launch_tiles<XT, G, 4, 2>(a, s) : launch_tiles<XT, G, 4, 1>(a, s);
+}
+
+}  // namespace
+
+template <int XT>
+hipError_t launch_linear_type(const LinearArgs& a, int group, int cus, hipStream_t s) {
+  if (group == 32) return launch_group<XT, 32>(a, cus, s);
+  if (group == 64) return launch_group<XT, 64>(a, cus, s);
+  return launch_group<XT, 128>(a, cus, s);
+}
+
+}  // namespace qmoe

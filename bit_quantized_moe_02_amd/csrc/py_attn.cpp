@@ -6,13 +6,7 @@
 //
 // Each function returns the library's code, or -1 when a tensor is not what
 // the call needs; the caller finds out which and says so.
-#define PY_SSIZE_T_CLEAN
-#include <Python.h>
-#include <torch/csrc/autograd/python_variable.h>
-
-#include <exception>
-
-#include "../../include/qmoe_attn.h"
+#include "py_args.hpp"
 
 namespace {
 
@@ -21,87 +15,6 @@ decltype(&moe_kv_append) p_append;
 decltype(&moe_kv_read) p_read;
 decltype(&moe_attn_decode) p_decode;
 decltype(&moe_attn_prefill) p_prefill;
-
-struct Rows {
-  void* p = nullptr;
-  int64_t stride = 0;
-};
-
-// 16-bit row types
-int row_type(PyObject* o) {
-  if (!THPVariable_Check(o)) return -1;
-  const auto t = THPVariable_Unpack(o).scalar_type();
-  return t == at::kBFloat16 ? MOE_DT_BF16 : t == at::kHalf ? MOE_DT_F16 : -1;
-}
-
-bool here(const at::Tensor& t, int64_t dev) { return t.is_cuda() && t.layout() == at::kStrided && t.get_device() == dev; }
-
-// A row tensor [>= n, heads, dim] on device `dev`, its heads back to back.
-bool rows(PyObject* o, int64_t heads, int64_t dim, int64_t n, int dtype, int64_t dev, Rows* r) {
-  if (row_type(o) != dtype) return false;
-  const at::Tensor& t = THPVariable_Unpack(o);
-  if (!here(t, dev) || t.dim() != 3) return false;
-  const auto size = t.sizes(), stride = t.strides();
-  if (size[0] < n || size[1] != heads || size[2] != dim || stride[2] != 1 || (stride[1] != dim && heads != 1)) return false;
-  r->p = t.data_ptr();
-  r->stride = size[0] > 1 ? stride[0] : heads * dim;
-  return true;
-}
-
-// Heads of a row tensor, 0 for others (which rows() then refuses).
-int64_t heads_of(PyObject* o) {
-  if (!THPVariable_Check(o)) return 0;
-  const at::Tensor& t = THPVariable_Unpack(o);
-  return t.layout() == at::kStrided && t.dim() == 3 ? t.size(1) : 0;
-}
-
-// A contiguous tensor of at least n elements; its address and size.
-bool vec(PyObject* o, at::ScalarType type, int64_t n, int64_t dev, void** p, int64_t* numel = nullptr) {
-  if (!THPVariable_Check(o)) return false;
-  const at::Tensor& t = THPVariable_Unpack(o);
-  if (!here(t, dev) || t.scalar_type() != type || !t.is_contiguous() || t.numel() < n) return false;
-  *p = t.data_ptr();
-  if (numel) *numel = t.numel();
-  return true;
-}
-
-bool vec_or_none(PyObject* o, at::ScalarType type, int64_t n, int64_t dev, void** p) {
-  return o == Py_None || vec(o, type, n, dev, p);
-}
-
-// Numbers and addresses among the arguments; a Python error is left set.
-struct Args {
-  PyObject* const* a;
-  int64_t num(int i) const { return PyLong_AsLongLong(a[i]); }
-  void* addr(int i) const { return PyLong_AsVoidPtr(a[i]); }
-};
-
-PyObject* refused() { return PyErr_Occurred() ? nullptr : PyLong_FromLong(-1); }
-
-template <typename F>
-PyObject* call(PyObject* const* a, Py_ssize_t given, Py_ssize_t wanted, F f) {
-  if (given != wanted) {
-    PyErr_SetString(PyExc_TypeError, "wrong number of arguments");
-    return nullptr;
-  }
-  try {
-    return f(Args{a});
-  } catch (const std::exception& e) {
-    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
-    return nullptr;
-  }
-}
-
-// The library's call without the interpreter's lock.
-template <typename F>
-PyObject* run(F f) {
-  if (PyErr_Occurred()) return nullptr;
-  int rc;
-  Py_BEGIN_ALLOW_THREADS
-  rc = f();
-  Py_END_ALLOW_THREADS
-  return PyLong_FromLong(rc);
-}
 
 // use(append, read, decode, prefill): addresses of the library's functions
 PyObject* use(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -205,9 +118,11 @@ PyObject* prefill(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
-#define FAST(f) (PyCFunction)(void (*)(void)) f, METH_FASTCALL, nullptr
 PyMethodDef methods[] = {{"use", FAST(use)},       {"append", FAST(append)},   {"read", FAST(read)},
-                         {"decode", FAST(decode)}, {"prefill", FAST(prefill)}, {nullptr, nullptr, 0, nullptr}};
+                         {"decode", FAST(decode)}, {"prefill", FAST(prefill)},
+                         {"step_use", FAST(step_use)},       {"norm", FAST(step_norm)}, {"linear", FAST(step_linear)},
+                         {"resize", FAST(step_resize)},      {"fork", FAST(step_fork)}, {"compact", FAST(step_compact)},
+                         {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_attn", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,4 +1,4 @@
-"""Python binding of libqmoe (include/qmoe.h, include/qmoe_attn.h): the same calls under the same
+"""Python binding of libqmoe (include/qmoe.h, qmoe_attn.h, qmoe_step.h): the same calls under the same
 names, with argument marshalling only -- torch tensors become device
 pointers, the current torch stream becomes the hipStream_t, a nonzero status
 becomes a QmoeError carrying moe_last_error().  Every computation happens in
@@ -6,7 +6,7 @@ the library's kernels or its host quantizer.
 
 Import torch before this module (the library then shares torch's HIP
 runtime); a missing libqmoe.so raises at import time, a missing _attn.so when
-one of the attention calls that need it is made.
+one of the attention or step calls that need it is made.
 """
 from __future__ import annotations
 
@@ -66,10 +66,17 @@ EXPORTED_ATTN = [
     "moe_kv_code_bytes", "moe_kv_scale_bytes", "moe_rope_freqs", "moe_kv_append", "moe_kv_read",
     "moe_attn_decode_workspace_bytes", "moe_attn_decode", "moe_attn_prefill_workspace_bytes", "moe_attn_prefill",
 ]
+# norm, 4-bit products, pages (include/qmoe_step.h)
+EXPORTED_STEP = [
+    "moe_rms_norm", "moe_linear_quantize", "moe_linear_packed_bytes", "moe_linear_pack", "moe_linear", "moe_kv_resize",
+    "moe_kv_fork_workspace_bytes", "moe_kv_fork", "moe_kv_compact_workspace_bytes", "moe_kv_compact",
+]
 MOE_NOALLOC_SCRATCH_BYTES = 8 << 20
 
 MOE_DT_BF16 = 0
 MOE_DT_F16 = 1
+MOE_DT_F32 = 2
+MOE_DT_I8 = 3
 MOE_ROPE = {"plain": 0, "linear": 1, "base": 2, "parts": 3}
 
 MOE_KERNEL = {"route_logits": 0, "route_topk": 1, "decode_upgate": 2, "decode_down": 3,
@@ -123,6 +130,35 @@ class MoePacked(ctypes.Structure):
                 ("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
 
 
+class MoeNorm(ctypes.Structure):
+    """Mirror of struct moe_norm."""
+    _fields_ = [("rows", ctypes.c_int32), ("heads", ctypes.c_int32), ("cols", ctypes.c_int32), ("x_dtype", ctypes.c_int32),
+                ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("residual_dtype", ctypes.c_int32),
+                ("weight_dtype", ctypes.c_int32), ("residual", ctypes.c_void_p), ("residual_stride", ctypes.c_int64),
+                ("sum", ctypes.c_void_p), ("sum_stride", ctypes.c_int64), ("weight", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("out_dtype", ctypes.c_int32), ("out", ctypes.c_void_p), ("out_stride", ctypes.c_int64),
+                ("codes", ctypes.c_void_p), ("codes_stride", ctypes.c_int64), ("scales", ctypes.c_void_p),
+                ("scale_stride", ctypes.c_int64), ("group", ctypes.c_int32)]
+
+
+class MoeLinearWeights(ctypes.Structure):
+    """Mirror of struct moe_linear_weights."""
+    _fields_ = [("n", ctypes.c_int32), ("k", ctypes.c_int32), ("group", ctypes.c_int32), ("with_zeros", ctypes.c_int32),
+                ("packed", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
+
+
+class MoeKvPool(ctypes.Structure):
+    """Mirror of struct moe_kv_pool."""
+    _fields_ = [("n_pages", ctypes.c_int32), ("n_caches", ctypes.c_int32), ("caches", ctypes.POINTER(MoeKvCache)),
+                ("refs", ctypes.c_void_p)]
+
+
+class MoeKvTables(ctypes.Structure):
+    """Mirror of struct moe_kv_tables."""
+    _fields_ = [("seqs", ctypes.c_int32), ("pages_per_seq", ctypes.c_int32), ("page_tokens", ctypes.c_int32),
+                ("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("kv_lens", ctypes.c_void_p)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built; run `python -m bit_quantized_moe_02_amd.build`")
@@ -171,6 +207,16 @@ def _load():
         "moe_attn_prefill_workspace_bytes": (sz, [vp]),
         "moe_attn_prefill": (ctypes.c_int, [vp, ctypes.c_int, vp, i64, vp, i64, vp, i64, ctypes.c_float, ctypes.c_int, vp, i64,
                                             vp, vp, sz, vp]),
+        "moe_rms_norm": (ctypes.c_int, [vp, vp]),
+        "moe_linear_quantize": (ctypes.c_int, [vp, i64, i64, i32, vp, vp, vp, ctypes.c_int]),
+        "moe_linear_packed_bytes": (sz, [i64, i64, i32, ctypes.c_int]),
+        "moe_linear_pack": (ctypes.c_int, [vp, vp, vp, i64, i64, i32, vp, sz, ctypes.c_int]),
+        "moe_linear": (ctypes.c_int, [vp, i32, ctypes.c_int, vp, i64, vp, i64, i32, ctypes.c_int, vp, i64, vp]),
+        "moe_kv_resize": (ctypes.c_int, [vp, vp, vp, vp, vp]),
+        "moe_kv_fork_workspace_bytes": (sz, [vp, vp]),
+        "moe_kv_fork": (ctypes.c_int, [vp, vp, vp, vp, vp, sz, vp]),
+        "moe_kv_compact_workspace_bytes": (sz, [vp, vp]),
+        "moe_kv_compact": (ctypes.c_int, [vp, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -698,3 +744,213 @@ def moe_attn_prefill(q, k, v, cu_q, cu_k, max_q, out, ws, scale, causal=True, ls
                  [(cu_q, "cu_q", torch.int32, 2, dev), (cu_k, "cu_k", torch.int32, getattr(cu_q, "numel", int)(), dev),
                   (ws, "ws", torch.uint8, 0, dev), (lse, "lse", torch.float32, nq * hq, dev, True)])
 
+
+
+# ---------------------------------------------------------------------------
+# Norm, 4-bit products, pages of a cache (include/qmoe_step.h).
+
+
+if not isinstance(_attn, _NotBuilt):
+    _attn.step_use(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
+                     for f in ("moe_rms_norm", "moe_linear", "moe_kv_resize", "moe_kv_fork", "moe_kv_compact")))
+
+_NORM_TYPES = (torch.bfloat16, torch.float16, torch.float32)
+
+
+def _look_vectors(t, name, shape, types, dev):
+    """Raises unless t is a tensor of vectors of this shape, a row's values back to back, on device `dev`."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in types:
+        raise ValueError(f"{name} must be {' or '.join(str(x) for x in types)}, not {t.dtype}")
+    if t.dim() not in (2, 3) or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; the call needs {'[rows, cols] or [rows, heads, cols]' if shape is None else list(shape)}")
+    _here(t, name, dev)
+    if t.layout != torch.strided or t.stride(-1) != 1 or (t.dim() == 3 and t.shape[1] != 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name}'s rows must be contiguous")
+
+
+def _look_scales(t, name, groups, rows, dev):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.float32:
+        raise ValueError(f"{name} must be a torch.float32 CUDA tensor")
+    _here(t, name, dev)
+    if t.dim() != 2 or t.shape[0] != groups or t.shape[1] < rows or t.stride(1) != 1:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; the call needs [{groups}, at least {rows}], rows of it contiguous")
+
+
+def moe_scales_shape(rows: int, cols: int, group: int = 0, heads: int = 1):
+    """Shape of the scales of 8-bit rows: [groups of a row, rows (a multiple of 4)]."""
+    return heads * (-(-cols // group) if group else 1), max(-(-rows // 4) * 4, 4)
+
+
+def moe_rms_norm(x, out=None, weight=None, eps=1e-6, residual=None, sum_out=None, codes=None, scales=None, group=0, stream=None):
+    """x [rows, cols] or [rows, heads, cols] (+ residual, whose sum with x goes to sum_out), normed into out and/or into
+    int8 codes with fp32 scales (moe_scales_shape)."""
+    dev = _device()
+    rc = _attn.norm(dev, _stream_on(stream, dev), x, out, weight, eps, residual, sum_out, codes, scales, group)
+    if rc:
+        looks = []
+        if rc < 0:
+            _look_vectors(x, "x", None, _NORM_TYPES, dev)
+            for t, name, types in ((out, "out", _NORM_TYPES), (residual, "residual", _NORM_TYPES),
+                                   (sum_out, "sum_out", (getattr(residual, "dtype", None),)), (codes, "codes", (torch.int8,))):
+                if t is not None:
+                    _look_vectors(t, name, x.shape, types, dev)
+            if weight is not None:
+                if not isinstance(weight, torch.Tensor) or weight.dtype not in _NORM_TYPES or weight.dim() != 1:
+                    raise ValueError("weight must be a 1-dimensional CUDA tensor of 16 or 32 bits")
+                looks.append((weight, "weight", weight.dtype, x.shape[-1], dev))
+                if weight.numel() != x.shape[-1]:
+                    raise ValueError(f"weight holds {weight.numel()} elements; the call needs {x.shape[-1]}")
+            if scales is not None and group >= 0:
+                _look_scales(scales, "scales", moe_scales_shape(x.shape[0], x.shape[-1], group, x.shape[1] if x.dim() == 3 else 1)[0],
+                             x.shape[0], dev)
+        _refused(rc, [], looks)
+
+
+def moe_linear_packed_bytes(n: int, k: int, group: int, with_zeros: bool) -> int:
+    return int(lib.moe_linear_packed_bytes(n, k, group, int(bool(with_zeros))))
+
+
+def moe_linear_quantize(w: np.ndarray, group: int = 128, with_zeros: bool = False, n_threads: int = 0):
+    """fp32 host matrix [n, k] -> (codes uint8 [n, k], scales fp16 [n, groups], zero points uint8 [n, groups] or None)."""
+    w = np.ascontiguousarray(w, dtype=np.float32)
+    n, k = w.shape
+    groups = -(-k // group) if group > 0 else 1
+    codes, scales = np.empty((n, k), np.uint8), np.empty((n, groups), np.float16)
+    zeros = np.empty((n, groups), np.uint8) if with_zeros else None
+    _check(lib.moe_linear_quantize(w.ctypes.data, n, k, group, codes.ctypes.data, scales.ctypes.data,
+                                   None if zeros is None else zeros.ctypes.data, n_threads))
+    return codes, scales, zeros
+
+
+def moe_linear_pack(codes: np.ndarray, scales: np.ndarray, zeros: np.ndarray | None = None, group: int = 128,
+                    n_threads: int = 0) -> np.ndarray:
+    """Codes, scales and zero points (host) -> packed uint8 bytes (host)."""
+    codes = np.ascontiguousarray(codes, dtype=np.uint8)
+    if codes.ndim != 2:
+        raise ValueError("codes must be [n, k]")
+    n, k = codes.shape
+    groups = (n, -(-k // group) if group > 0 else 1)
+    scales = np.ascontiguousarray(scales, dtype=np.float16)
+    zeros = None if zeros is None else np.ascontiguousarray(zeros, dtype=np.uint8)
+    if scales.shape != groups or (zeros is not None and zeros.shape != groups):
+        raise ValueError(f"scales and zeros must be {list(groups)}")
+    out = np.empty(max(moe_linear_packed_bytes(n, k, group, zeros is not None), 1), np.uint8)
+    _check(lib.moe_linear_pack(codes.ctypes.data, scales.ctypes.data, None if zeros is None else zeros.ctypes.data, n, k, group,
+                               out.ctypes.data, out.nbytes, n_threads))
+    return out
+
+
+class LinearWeights:
+    """A packed 4-bit matrix [n, k] in device memory (struct moe_linear_weights): `packed` uint8 CUDA (moe_linear_pack),
+    bias fp32 CUDA [n] or None."""
+
+    def __init__(self, packed, n, k, group=128, with_zeros=False, bias=None):
+        need = moe_linear_packed_bytes(n, k, group, with_zeros)
+        if need == 0:
+            raise ValueError("n must be in [1, 2^24], k a multiple of 8 in [8, 2^20], group 32, 64 or 128")
+        self.tensors = (packed, bias)
+        self.n, self.k = n, k
+        self.c = MoeLinearWeights(n, k, group, int(bool(with_zeros)), _dev(packed, "packed", torch.uint8, need),
+                                  _dev(bias, "bias", torch.float32, n, optional=True))
+        self.device = packed.get_device()
+        if bias is not None:
+            _here(bias, "bias", self.device)
+        self.at = ctypes.addressof(self.c)
+
+
+def moe_linear(w, x, y, x_scales=None, x_group=0, stream=None):
+    """y [rows, n] = x [rows, k] times the weights' transpose; x 16-bit, or int8 codes with x_scales (moe_scales_shape).
+    Rows may also be [rows, heads, dim] with heads * dim columns."""
+    dev = _device()
+    if w.device != dev:
+        raise ValueError(f"the weights are on device {w.device}, the current one is {dev}")
+    rc = _attn.linear(w.at, w.n, w.k, dev, _stream_on(stream, dev), x, y, x_scales, x_group)
+    if rc:
+        if rc < 0:
+            _look_vectors(x, "x", None, (torch.bfloat16, torch.float16, torch.int8), dev)
+            _look_vectors(y, "y", None, _NORM_TYPES, dev)
+            for t, name, cols in ((x, "x", w.k), (y, "y", w.n)):
+                if t.shape[1:].numel() != cols or t.shape[0] != x.shape[0]:
+                    raise ValueError(f"{name} has shape {tuple(t.shape)}; the call needs [{x.shape[0]}, {cols}]")
+            if x_scales is not None and x_group >= 0:
+                _look_scales(x_scales, "x_scales", moe_scales_shape(x.shape[0], w.k, x_group)[0], x.shape[0], dev)
+        _refused(rc, [])
+
+
+class KvPool:
+    """The pages of one or more caches of the same n_pages and page_tokens (struct moe_kv_pool): refs int32 CUDA
+    [n_pages], how many table entries name each page (zeros: all free)."""
+
+    def __init__(self, refs, caches=()):
+        self.caches, self.refs = list(caches), refs
+        array = (MoeKvCache * max(len(self.caches), 1))(*(c.c for c in self.caches))
+        self.c = MoeKvPool(refs.numel() if isinstance(refs, torch.Tensor) else 0, len(self.caches), array,
+                           _dev(refs, "refs", torch.int32, 1))
+        self.device = refs.get_device()
+        for c in self.caches:
+            _here(c.codes, "a cache", self.device)
+        self._array = array
+        self.ref, self.at = ctypes.byref(self.c), ctypes.addressof(self.c)
+
+
+class KvTables:
+    """Rows of a page table (struct moe_kv_tables): page_table int32 CUDA [seqs, pages] (rows may be strided), kv_lens
+    int32 CUDA [seqs]; the tensors of KvBatch."""
+
+    def __init__(self, page_table, kv_lens, page_tokens):
+        if not isinstance(page_table, torch.Tensor) or not page_table.is_cuda or page_table.dim() != 2 or page_table.dtype != torch.int32:
+            raise ValueError("page_table must be a 2-dimensional int32 CUDA tensor")
+        seqs, pages = page_table.shape
+        if page_table.stride(1) != 1 and pages > 1:
+            raise ValueError("page_table's rows must be contiguous")
+        self.tensors = (page_table, kv_lens)
+        self.seqs = seqs
+        self.c = MoeKvTables(seqs, pages, page_tokens, page_table.data_ptr(),
+                             page_table.stride(0) if seqs > 1 else max(page_table.stride(0), pages),
+                             _dev(kv_lens, "kv_lens", torch.int32, seqs))
+        self.device = page_table.get_device()
+        _here(kv_lens, "kv_lens", self.device)
+        self.ref, self.at = ctypes.byref(self.c), ctypes.addressof(self.c)
+
+
+def _pages(pool, tables):
+    """The current device, which must be the pool's and the tables'."""
+    dev = _device()
+    if pool.device != dev or tables.device != dev:
+        raise ValueError(f"the pool is on device {pool.device}, the tables on {tables.device}, the current one is {dev}")
+    return dev
+
+
+def moe_kv_resize(pool, tables, new_lens, missing=None, stream=None):
+    """new_lens int32 [seqs] (negative: left alone); missing int32 [1] or None."""
+    dev = _pages(pool, tables)
+    rc = _attn.resize(pool.at, tables.at, tables.seqs, dev, _stream_on(stream, dev), new_lens, missing)
+    if rc:
+        _refused(rc, [], [(new_lens, "new_lens", torch.int32, tables.seqs, dev), (missing, "missing", torch.int32, 1, dev, True)])
+
+
+def moe_kv_fork_workspace_bytes(pool, tables) -> int:
+    return int(lib.moe_kv_fork_workspace_bytes(pool.ref, tables.ref))
+
+
+def moe_kv_fork(pool, tables, from_rows, ws, missing=None, stream=None):
+    """from_rows int32 [seqs]: the row that each row goes on from (negative: left alone)."""
+    dev = _pages(pool, tables)
+    rc = _attn.fork(pool.at, tables.at, tables.seqs, dev, _stream_on(stream, dev), from_rows, missing, ws)
+    if rc:
+        _refused(rc, [], [(from_rows, "from_rows", torch.int32, tables.seqs, dev), (missing, "missing", torch.int32, 1, dev, True),
+                          (ws, "ws", torch.uint8, 0, dev)])
+
+
+def moe_kv_compact_workspace_bytes(pool, tables) -> int:
+    return int(lib.moe_kv_compact_workspace_bytes(pool.ref, tables.ref))
+
+
+def moe_kv_compact(pool, tables, ws, held=None, stream=None):
+    """held int32 [1] or None: the number of pages held, which are then the pool's first ones."""
+    dev = _pages(pool, tables)
+    rc = _attn.compact(pool.at, tables.at, dev, _stream_on(stream, dev), held, ws)
+    if rc:
+        _refused(rc, [], [(held, "held", torch.int32, 1, dev, True), (ws, "ws", torch.uint8, 0, dev)])
