@@ -63,7 +63,7 @@ int quantize(const float* w, int64_t n, int64_t k, int32_t group, uint8_t* codes
             lo = std::min(lo, (double)x[j]);
             hi = std::max(hi, (double)x[j]);
           }
-          const uint16_t h = f64_to_f16_rne(zeros ? (hi - lo) / 15.0 : std::max(-lo, hi) / 7.0);
+          const uint16_t h = f64_to_f16_rne(zeros ? (hi - lo) / 15.0 : (std::max(-lo, hi) + 0.0) / 7.0);    // (+0 for zeros)
           const double s = f16_value(h);
           if (!isfinite(s)) wrong |= 2;
           if (pass == 0) continue;

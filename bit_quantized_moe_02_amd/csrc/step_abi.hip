@@ -72,14 +72,15 @@ extern "C" int moe_rms_norm(const moe_norm* p, void* stream) {
   if (p->heads < 1 || p->heads > 4096 || (int64_t)p->heads * p->rows > kMaxGrid)
     return bad(who, "need 1 <= heads <= 4096, rows * heads < 2^24");
   if (!(p->eps >= 0) || !isfinite(p->eps)) return bad(who, "eps must be finite and not negative");
-  if (!p->out && !p->codes && !p->sum) return bad(who, "no output is wanted");
   if (!float_type(p->x_dtype) || (p->residual && !float_type(p->residual_dtype)) || (p->weight && !float_type(p->weight_dtype)) ||
       (p->out && !float_type(p->out_dtype)))
     return fail(MOE_ERR_UNSUPPORTED, std::string(who) + ": unknown type");
+  if (p->rows == 0) return MOE_OK;
   const int64_t width = (int64_t)p->heads * p->cols;
   int rc = check_rows(who, "x", p->x, p->x_stride, width);
   if (rc != MOE_OK) return rc;
   if (p->residual && (rc = check_rows(who, "residual", p->residual, p->residual_stride, width)) != MOE_OK) return rc;
+  if (!p->out && !p->codes && !p->sum) return bad(who, "no output is wanted");
   if (p->sum && !p->residual) return bad(who, "sum needs a residual");
   if (p->sum && (rc = check_rows(who, "sum", p->sum, p->sum_stride, width)) != MOE_OK) return rc;
   if (p->out && (rc = check_rows(who, "out", p->out, p->out_stride, width)) != MOE_OK) return rc;
@@ -102,7 +103,6 @@ extern "C" int moe_rms_norm(const moe_norm* p, void* stream) {
   if ((rc = check_place(who, "out", p->out, p->out_dtype, p->out_stride, "residual", p->residual, p->residual_dtype,
                         p->residual_stride)) != MOE_OK)
     return rc;
-  if (p->rows == 0) return MOE_OK;
   NormArgs a{};
   a.x = p->x;
   a.res = p->residual;
@@ -143,6 +143,7 @@ extern "C" int moe_linear(const moe_linear_weights* w, int32_t rows, int x_dtype
   if (x_dtype != MOE_DT_BF16 && x_dtype != MOE_DT_F16 && x_dtype != MOE_DT_I8)
     return fail(MOE_ERR_UNSUPPORTED, std::string(who) + ": unknown type of x");
   if (!float_type(y_dtype)) return fail(MOE_ERR_UNSUPPORTED, std::string(who) + ": unknown type of y");
+  if (rows == 0) return MOE_OK;
   int rc = check_rows(who, "x", x, x_stride, w->k);
   if (rc != MOE_OK) return rc;
   if (x_dtype == MOE_DT_I8) {
@@ -156,7 +157,6 @@ extern "C" int moe_linear(const moe_linear_weights* w, int32_t rows, int x_dtype
   if (!y || !aligned(y, 16)) return bad(who, "y must be 16-byte aligned memory");
   if (y_stride < w->n || y_stride > kMaxStride) return bad(who, "y_stride must be at least n, at most 2^24");
   if (y == x) return bad(who, "y must not overlap x");
-  if (rows == 0) return MOE_OK;
   LinearArgs a{};
   a.w = (const uint8_t*)w->packed;
   a.bias = w->bias;

@@ -54,7 +54,7 @@ extern "C" {
  * At least one of out, codes and sum is wanted; sum needs a residual.  sum may be the
  * residual or x itself, out may be x, residual or... any input whose rows it
  * takes the place of exactly (same type and stride); outputs must not overlap
- * inputs or each other otherwise.  rows = 0: nothing is done. */
+ * inputs or each other otherwise.  rows = 0: nothing is done (the rows may be NULL). */
 typedef struct moe_norm {
   int32_t rows;
   int32_t heads;
@@ -146,8 +146,8 @@ typedef struct moe_linear_weights {
  * rows' are exact inside a group of columns that share both scales and 32-bit between them; the result is
  * rounded once.  A row that holds a value that is not finite gives infinities or
  * not a number; other rows are not touched by it.  Meant for few rows (1 to 64 share one
- * reading of the weights); any number up to 2^20 works.  rows = 0: nothing is done.
- * y must not overlap the inputs. */
+ * reading of the weights); any number up to 2^20 works.  rows = 0: nothing is done
+ * (the rows may be NULL).  y must not overlap the inputs. */
 int moe_linear(const moe_linear_weights* w, int32_t rows, int x_dtype, const void* x, int64_t x_stride,
                const float* x_scales, int64_t scale_stride, int32_t x_group, int y_dtype, void* y, int64_t y_stride,
                void* stream);
