@@ -21,6 +21,7 @@
 
 #include "../../include/qmoe_step.h"
 #include "k_step.h"
+#include "launch_util.h"
 
 namespace qmoe {
 namespace {
@@ -114,63 +115,93 @@ __device__ __forceinline__ int zero_of(const Weights<G, Z>& w, int i, uint32_t l
   return (int)(int8_t)z;
 }
 
-template <int XT>
-__device__ __forceinline__ typename Types<XT>::X load_x(Buffer b, uint32_t at) {
-  if constexpr (XT == MOE_DT_I8) return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(b, at, 0, 0));
-  else return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, at, 0, 0));
-}
-
-// Waves of a workgroup: 16 with 128 registers each, as long as two tiles' operands fit.
-constexpr int waves_of(int mt, int nt) { return mt * nt <= 2 ? 16 : 8; }
+// How a workgroup is made for up to R rows of x and NT tiles of 16 weight rows.
+template <int XT, int R, int NT>
+struct Shape {
+  static constexpr int kXBytes = XT == MOE_DT_I8 ? 1 : 2;
+  static constexpr int kMt = (R + 15) / 16;                          // 16-row operands of x
+  static constexpr int kWaves = kMt == 1 ? 16 : 8;              // 128 or 256 registers each
+  static constexpr int kLanesARow = 8 * kXBytes;                     // 16 bytes of a row's 128 columns a lane
+  static constexpr int kRowsALoad = 64 / kLanesARow;
+  static constexpr int kLoads = R <= kRowsALoad ? 1 : R / kRowsALoad;
+  static constexpr int kXTile = 1024 * kLoads, kSums = kMt * NT * 1024;
+  static constexpr int kLds = kXTile > kSums ? kXTile : kSums;       // of a wave
+  // (rows past R: whatever lies behind them, in its wave's or a neighbour's part)
+  static constexpr int kLdsAll = (kWaves - 1) * kLds + (kLds > 2048 * kXBytes * kMt ? kLds : 2048 * kXBytes * kMt);
+  static constexpr int kAhead = kMt <= 2 ? 2 : 1;                    // tiles of x in flight
+};
 
 // Z: with zero points.  XG: 8-bit rows with a scale for each 128 columns.
-template <int XT, int G, int MT, int NT, bool Z, bool XG>
-__global__ __launch_bounds__(64 * waves_of(MT, NT)) void linear_kernel(LinearArgs a) {
-  constexpr int kWaves = waves_of(MT, NT), kDepth = 2, kGroups = 128 / G;
+template <int XT, int G, int R, int NT, bool Z, bool XG>
+__global__ __launch_bounds__((64 * Shape<XT, R, NT>::kWaves)) void linear_kernel(LinearArgs a) {
+  typedef Shape<XT, R, NT> S;
+  constexpr int MT = S::kMt, kWaves = S::kWaves, kGroups = 128 / G, kDepth = 2;
   constexpr bool kInt = XT == MOE_DT_I8;
-  constexpr int kXBytes = kInt ? 1 : 2;
+  constexpr int kXBytes = S::kXBytes;
   constexpr uint32_t kTile = 1024 + 32 * kGroups + (Z ? 16 * kGroups : 0);
   typedef typename Types<XT>::X X;
-  __shared__ f32x4 sums[kWaves][MT * NT][64];
+  extern __shared__ uint8_t lds[];
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const uint32_t lane = threadIdx.x % 64, r = lane & 15, g = lane >> 4;
   const int kc_n = (a.k + 127) / 128, rt_n = (a.n + 15) / 16;
-  const int t0 = blockIdx.y * (16 * MT), rt0 = blockIdx.x * NT;
+  const int t0 = blockIdx.y * R, rt0 = blockIdx.x * NT;
   Buffer tiles[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i)
     tiles[i] = buffer(a.w + (int64_t)(rt0 + i) * kc_n * kTile, rt0 + i < rt_n ? kc_n * kTile : 0);
-  // 16 * MT rows of x from t0 on: below 2^31 bytes, as strides are at most 2^24
+  // R rows of x from t0 on: below 2^31 bytes, as strides are at most 2^24
   constexpr uint32_t kNoRow = 0x80000000u, kNoColumn = 0x7FFFFFF0u;
-  const int rows = min(a.rows - t0, 16 * MT);
+  const int rows = min(a.rows - t0, R);
   const Buffer xs = buffer((const uint8_t*)a.x + (int64_t)t0 * a.x_stride * kXBytes,
                            (uint32_t)(((rows - 1) * a.x_stride + a.k) * kXBytes));
-  uint32_t xrow[MT], trow[MT];                                       // trow: the lane's 4 rows of the results
+  // A load takes whole stretches of rows; the wave's part of LDS turns them into operands.  16 bytes u of row i lie
+  // at u ^ i among the row's, so that the 16 rows of an operand are in different banks.
+  const uint32_t lrow = lane / S::kLanesARow, unit = lane % S::kLanesARow;
+  uint32_t xrow[S::kLoads], trow[MT];                                // trow: the lane's 4 rows of the results
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    xrow[m] = (int)(16 * m + r) < rows ? (16 * m + r) * (uint32_t)a.x_stride * kXBytes : kNoRow;
-    trow[m] = (uint32_t)min(t0 + 16 * m + 4 * (int)g, (a.rows - 1) & ~3);
+  for (int q = 0; q < S::kLoads; ++q) {
+    const int i = q * S::kRowsALoad + lrow;
+    xrow[q] = i < rows ? i * (uint32_t)a.x_stride * kXBytes : kNoRow;
   }
+#pragma unroll
+  for (int m = 0; m < MT; ++m) trow[m] = (uint32_t)min(t0 + 16 * m + 4 * (int)g, (a.rows - 1) & ~3);
+  uint8_t* const mine = lds + wave * S::kLds;
+  uint8_t* const put = mine + lrow * (16 * S::kLanesARow);
+  const uint8_t* const get = mine + r * (16 * S::kLanesARow);
 
   Weights<G, Z> w[kDepth][NT];
-  X x[kDepth][MT][4];
+  u32x4 x[S::kAhead][S::kLoads];
   f32x4 xg[kDepth][XG ? MT : 1];
-  auto load = [&](int d, int i) {                                    // the wave's tile i
+  auto load_w = [&](int d, int i) {                                  // of the wave's tile i
     const int kc = wave + i * kWaves;
 #pragma unroll
     for (int t = 0; t < NT; ++t) w[d][t] = load_weights<G, Z>(tiles[t], kc * kTile, lane);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int col = kc * 128 + 32 * c + 8 * (int)g;
-      const uint32_t at = col < a.k ? (uint32_t)col * kXBytes : kNoColumn;
-#pragma unroll
-      for (int m = 0; m < MT; ++m) x[d][m][c] = load_x<XT>(xs, xrow[m] + at);
-    }
     if constexpr (XG) {
 #pragma unroll
       for (int m = 0; m < MT; ++m) xg[d][m] = *(const f32x4*)(a.xs + min(kc, kc_n - 1) * a.xs_stride + trow[m]);
     }
+  };
+  auto load_x = [&](int d, int i) {
+    const int col = (wave + i * kWaves) * 128 + (int)unit * (16 / kXBytes);
+    const uint32_t at = col < a.k ? (uint32_t)col * kXBytes : kNoColumn;
+#pragma unroll
+    for (int q = 0; q < S::kLoads; ++q)
+      x[d][q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(xs, xrow[q] + at, 0, 0));
+  };
+  auto turn = [&](int d, int i) {
+    const bool half = kInt && (wave + i * kWaves) * 128 + (int)unit * 16 + 8 >= a.k;   // (k is a multiple of 8)
+#pragma unroll
+    for (int q = 0; q < S::kLoads; ++q) {
+      u32x4 v = x[d][q];
+      if (half) v[2] = 0, v[3] = 0;
+      const uint32_t row = q * S::kRowsALoad + lrow;
+      *(u32x4*)(put + q * 1024 + 16 * (unit ^ (row & (S::kLanesARow - 1)))) = v;
+    }
+  };
+  auto operand = [&](int m, int c) {                                 // 8 columns of row 16 m + r, 32 c + 8 g and on
+    if constexpr (kInt) return *(const u32x2*)(get + m * 2048 + 16 * ((2 * c + (g >> 1)) ^ (r & 7)) + 8 * (g & 1));
+    else return *(const u32x4*)(get + m * 4096 + 16 * ((4 * c + g) ^ r));
   };
   f32x4 total[MT][NT];
 #pragma unroll
@@ -193,9 +224,10 @@ __global__ __launch_bounds__(64 * waves_of(MT, NT)) void linear_kernel(LinearArg
           for (int t = 0; t < NT; ++t) b[t] = units<XT>(w[d][t].q[at]);
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
-            accx[m] = mma16<XT>(x[d][m][at], one, c ? accx[m] : (f32x4){0, 0, 0, 0});
+            const X xv = operand(m, at);
+            accx[m] = mma16<XT>(xv, one, c ? accx[m] : (f32x4){0, 0, 0, 0});
 #pragma unroll
-            for (int t = 0; t < NT; ++t) acc[m][t] = mma16<XT>(x[d][m][at], b[t], c ? acc[m][t] : (f32x4){0, 0, 0, 0});
+            for (int t = 0; t < NT; ++t) acc[m][t] = mma16<XT>(xv, b[t], c ? acc[m][t] : (f32x4){0, 0, 0, 0});
           }
         }
 #pragma unroll
@@ -215,7 +247,7 @@ __global__ __launch_bounds__(64 * waves_of(MT, NT)) void linear_kernel(LinearArg
           for (int t = 0; t < NT; ++t) b[t] = __builtin_bit_cast(long, bytes(w[d][t].q[gi]));
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
-            const long xv = __builtin_bit_cast(long, x[d][m][gi]);
+            const long xv = __builtin_bit_cast(long, operand(m, gi));
             if constexpr (Z) accx[m] = __builtin_amdgcn_mfma_i32_16x16x32_i8(xv, 0x0101010101010101l, (i32x4){0, 0, 0, 0}, 0, 0, 0);
 #pragma unroll
             for (int t = 0; t < NT; ++t) acc[m][t] = __builtin_amdgcn_mfma_i32_16x16x32_i8(xv, b[t], (i32x4){0, 0, 0, 0}, 0, 0, 0);
@@ -232,7 +264,7 @@ __global__ __launch_bounds__(64 * waves_of(MT, NT)) void linear_kernel(LinearArg
             }
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-              const u32x2 x0 = x[d][m][at], x1 = x[d][m][at + 1];
+              const u32x2 x0 = operand(m, at), x1 = operand(m, at + 1);
               const i32x4 xv = {(int)x0[0], (int)x0[1], (int)x1[0], (int)x1[1]};
               const i32x4 one = {0x01010101, 0x01010101, 0x01010101, 0x01010101};
               if constexpr (Z) accx[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(xv, one, c ? accx[m] : (i32x4){0, 0, 0, 0}, 0, 0, 0);
@@ -261,22 +293,28 @@ __global__ __launch_bounds__(64 * waves_of(MT, NT)) void linear_kernel(LinearArg
 
   const int steps = (kc_n + kWaves * kDepth - 1) / (kWaves * kDepth);
 #pragma unroll
-  for (int d = 0; d < kDepth; ++d) load(d, d);
+  for (int d = 0; d < S::kAhead; ++d) load_x(d, d);
+#pragma unroll
+  for (int d = 0; d < kDepth; ++d) load_w(d, d);
   for (int i = 0; i < steps; ++i) {
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) {
       // (stages mixed up would need more registers than there are)
       __builtin_amdgcn_sched_barrier(0);
+      turn(d % S::kAhead, i * kDepth + d);
+      load_x(d % S::kAhead, i * kDepth + d + S::kAhead);
+      __builtin_amdgcn_sched_barrier(0);
       add(d);
       __builtin_amdgcn_sched_barrier(0);
-      load(d, (i + 1) * kDepth + d);
+      load_w(d, (i + 1) * kDepth + d);
     }
   }
 
+  f32x4* const sums = (f32x4*)mine;
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int t = 0; t < NT; ++t) sums[wave][m * NT + t][lane] = total[m][t];
+    for (int t = 0; t < NT; ++t) sums[(m * NT + t) * 64 + lane] = total[m][t];
   __syncthreads();
   for (int at = threadIdx.x; at < MT * NT * 256; at += 64 * kWaves) {
     // consecutive threads: consecutive weight rows
@@ -286,7 +324,7 @@ __global__ __launch_bounds__(64 * waves_of(MT, NT)) void linear_kernel(LinearArg
     if (tok >= a.rows || n >= a.n) continue;
     float v = 0;
 #pragma unroll
-    for (int wv = 0; wv < kWaves; ++wv) v += sums[wv][m * NT + t][l][j];
+    for (int wv = 0; wv < kWaves; ++wv) v += ((const float*)(lds + wv * S::kLds))[((m * NT + t) * 64 + l) * 4 + j];
     if (kInt && !XG) v *= a.xs[tok];
     if (a.bias) v += a.bias[n];
     const int64_t to = (int64_t)tok * a.y_stride + n;
@@ -296,28 +334,38 @@ __global__ __launch_bounds__(64 * waves_of(MT, NT)) void linear_kernel(LinearArg
   }
 }
 
-template <int XT, int G, int MT, int NT>
-hipError_t launch_tiles(const LinearArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)(((a.n + 15) / 16 + NT - 1) / NT), (unsigned)((a.rows + 16 * MT - 1) / (16 * MT)));
-  const dim3 block(64 * waves_of(MT, NT));
-  constexpr bool kInt = XT == MOE_DT_I8;
-  if (kInt && a.x_group) {
-    if (a.zeros) linear_kernel<XT, G, MT, NT, true, kInt><<<grid, block, 0, s>>>(a);
-    else linear_kernel<XT, G, MT, NT, false, kInt><<<grid, block, 0, s>>>(a);
-  } else if (a.zeros) {
-    linear_kernel<XT, G, MT, NT, true, false><<<grid, block, 0, s>>>(a);
-  } else {
-    linear_kernel<XT, G, MT, NT, false, false><<<grid, block, 0, s>>>(a);
+template <int XT, int G, int R, int NT, bool Z, bool XG>
+hipError_t launch_one(const LinearArgs& a, hipStream_t s) {
+  typedef Shape<XT, R, NT> S;
+  const auto kernel = linear_kernel<XT, G, R, NT, Z, XG>;
+  if (S::kLdsAll > 65536) {
+    const hipError_t e = ensure_dyn_lds((const void*)kernel);
+    if (e != hipSuccess) return e;
   }
+  const dim3 grid((unsigned)(((a.n + 15) / 16 + NT - 1) / NT), (unsigned)((a.rows + R - 1) / R));
+  kernel<<<grid, dim3(64 * S::kWaves), S::kLdsAll, s>>>(a);
   return hipGetLastError();
+}
+
+template <int XT, int G, int R, int NT>
+hipError_t launch_tiles(const LinearArgs& a, hipStream_t s) {
+  constexpr bool kInt = XT == MOE_DT_I8;
+  if (kInt && a.x_group) return a.zeros ? launch_one<XT, G, R, NT, true, kInt>(a, s) : launch_one<XT, G, R, NT, false, kInt>(a, s);
+  return a.zeros ? launch_one<XT, G, R, NT, true, false>(a, s) : launch_one<XT, G, R, NT, false, false>(a, s);
+}
+
+template <int XT, int G, int R>
+hipError_t launch_rows(const LinearArgs& a, int cus, hipStream_t s) {
+  return (a.n + 15) / 16 > cus ? launch_tiles<XT, G, R, 2>(a, s) : launch_tiles<XT, G, R, 1>(a, s);
 }
 
 template <int XT, int G>
 hipError_t launch_group(const LinearArgs& a, int cus, hipStream_t s) {
-  const bool wide = (a.n + 31) / 32 >= cus;
-  if (a.rows <= 16) return wide ? launch_tiles<XT, G, 1, 2>(a, s) : launch_tiles<XT, G, 1, 1>(a, s);
-  if (a.rows <= 32) return wide ? launch_tiles<XT, G, 2, 2>(a, s) : launch_tiles<XT, G, 2, 1>(a, s);
-  return wide ? launch_tiles<XT, G, 4, 2>(a, s) : launch_tiles<XT, G, 4, 1>(a, s);
+  constexpr int kFew = XT == MOE_DT_I8 ? 8 : 4;        // rows of one load
+  if (a.rows <= kFew) return launch_rows<XT, G, kFew>(a, cus, s);
+  if (a.rows <= 16) return launch_rows<XT, G, 16>(a, cus, s);
+  if (a.rows <= 32) return launch_rows<XT, G, 32>(a, cus, s);
+  return launch_rows<XT, G, 64>(a, cus, s);
 }
 
 }  // namespace
