@@ -115,27 +115,29 @@ __device__ __forceinline__ int zero_of(const Weights<G, Z>& w, int i, uint32_t l
   return (int)(int8_t)z;
 }
 
-// How a workgroup is made for up to R rows of x and NT tiles of 16 weight rows.
-template <int XT, int R, int NT>
+// How a workgroup of W waves is made for up to R rows of x and NT tiles of 16 weight rows.
+template <int XT, int R, int NT, int W>
 struct Shape {
   static constexpr int kXBytes = XT == MOE_DT_I8 ? 1 : 2;
-  static constexpr int kMt = (R + 15) / 16;                          // 16-row operands of x
-  static constexpr int kWaves = kMt == 1 ? 16 : 8;              // 128 or 256 registers each
+  // A wave takes up to 32 rows: 16 waves then have registers (128 each) for what they have in flight.  For more rows
+  // waves of the same columns go side by side and read the same weights.
+  static constexpr int kRows = R < 32 ? R : 32, kSides = R / kRows, kSteps = W / kSides;
+  static constexpr int kMt = (kRows + 15) / 16;                      // 16-row operands of x
   static constexpr int kLanesARow = 8 * kXBytes;                     // 16 bytes of a row's 128 columns a lane
   static constexpr int kRowsALoad = 64 / kLanesARow;
-  static constexpr int kLoads = R <= kRowsALoad ? 1 : R / kRowsALoad;
+  static constexpr int kLoads = kRows <= kRowsALoad ? 1 : kRows / kRowsALoad;
   static constexpr int kXTile = 1024 * kLoads, kSums = kMt * NT * 1024;
   static constexpr int kLds = kXTile > kSums ? kXTile : kSums;       // of a wave
-  // (rows past R: whatever lies behind them, in its wave's or a neighbour's part)
-  static constexpr int kLdsAll = (kWaves - 1) * kLds + (kLds > 2048 * kXBytes * kMt ? kLds : 2048 * kXBytes * kMt);
-  static constexpr int kAhead = kMt <= 2 ? 2 : 1;                    // tiles of x in flight
+  // (rows past kRows: whatever lies behind them, in its wave's or a neighbour's part)
+  static constexpr int kLdsAll = (W - 1) * kLds + (kLds > 2048 * kXBytes * kMt ? kLds : 2048 * kXBytes * kMt);
+  static constexpr int kAhead = kMt == 1 ? 2 : 1;                    // tiles of x in flight
 };
 
 // Z: with zero points.  XG: 8-bit rows with a scale for each 128 columns.
-template <int XT, int G, int R, int NT, bool Z, bool XG>
-__global__ __launch_bounds__((64 * Shape<XT, R, NT>::kWaves)) void linear_kernel(LinearArgs a) {
-  typedef Shape<XT, R, NT> S;
-  constexpr int MT = S::kMt, kWaves = S::kWaves, kGroups = 128 / G, kDepth = 2;
+template <int XT, int G, int R, int NT, int W, bool Z, bool XG>
+__global__ __launch_bounds__(64 * W) void linear_kernel(LinearArgs a) {
+  typedef Shape<XT, R, NT, W> S;
+  constexpr int MT = S::kMt, kSteps = S::kSteps, kGroups = 128 / G, kDepth = 2;
   constexpr bool kInt = XT == MOE_DT_I8;
   constexpr int kXBytes = S::kXBytes;
   constexpr uint32_t kTile = 1024 + 32 * kGroups + (Z ? 16 * kGroups : 0);
@@ -145,16 +147,17 @@ __global__ __launch_bounds__((64 * Shape<XT, R, NT>::kWaves)) void linear_kernel
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const uint32_t lane = threadIdx.x % 64, r = lane & 15, g = lane >> 4;
   const int kc_n = (a.k + 127) / 128, rt_n = (a.n + 15) / 16;
-  const int t0 = blockIdx.y * R, rt0 = blockIdx.x * NT;
+  const int side = wave / kSteps, step = wave % kSteps;
+  const int t0 = blockIdx.y * R + side * S::kRows, rt0 = blockIdx.x * NT;   // (t0 may lie past the last row)
   Buffer tiles[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i)
     tiles[i] = buffer(a.w + (int64_t)(rt0 + i) * kc_n * kTile, rt0 + i < rt_n ? kc_n * kTile : 0);
-  // R rows of x from t0 on: below 2^31 bytes, as strides are at most 2^24
+  // kRows rows of x from t0 on: below 2^31 bytes, as strides are at most 2^24
   constexpr uint32_t kNoRow = 0x80000000u, kNoColumn = 0x7FFFFFF0u;
-  const int rows = min(a.rows - t0, R);
-  const Buffer xs = buffer((const uint8_t*)a.x + (int64_t)t0 * a.x_stride * kXBytes,
-                           (uint32_t)(((rows - 1) * a.x_stride + a.k) * kXBytes));
+  const int rows = min(a.rows - t0, S::kRows);
+  const Buffer xs = buffer((const uint8_t*)a.x + (rows > 0 ? (int64_t)t0 * a.x_stride * kXBytes : 0),
+                           rows > 0 ? (uint32_t)(((rows - 1) * a.x_stride + a.k) * kXBytes) : 0);
   // A load takes whole stretches of rows; the wave's part of LDS turns them into operands.  16 bytes u of row i lie
   // at u ^ i among the row's, so that the 16 rows of an operand are in different banks.
   const uint32_t lrow = lane / S::kLanesARow, unit = lane % S::kLanesARow;
@@ -174,7 +177,7 @@ __global__ __launch_bounds__((64 * Shape<XT, R, NT>::kWaves)) void linear_kernel
   u32x4 x[S::kAhead][S::kLoads];
   f32x4 xg[kDepth][XG ? MT : 1];
   auto load_w = [&](int d, int i) {                                  // of the wave's tile i
-    const int kc = wave + i * kWaves;
+    const int kc = step + i * kSteps;
 #pragma unroll
     for (int t = 0; t < NT; ++t) w[d][t] = load_weights<G, Z>(tiles[t], kc * kTile, lane);
     if constexpr (XG) {
@@ -183,14 +186,14 @@ __global__ __launch_bounds__((64 * Shape<XT, R, NT>::kWaves)) void linear_kernel
     }
   };
   auto load_x = [&](int d, int i) {
-    const int col = (wave + i * kWaves) * 128 + (int)unit * (16 / kXBytes);
+    const int col = (step + i * kSteps) * 128 + (int)unit * (16 / kXBytes);
     const uint32_t at = col < a.k ? (uint32_t)col * kXBytes : kNoColumn;
 #pragma unroll
     for (int q = 0; q < S::kLoads; ++q)
       x[d][q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(xs, xrow[q] + at, 0, 0));
   };
   auto turn = [&](int d, int i) {
-    const bool half = kInt && (wave + i * kWaves) * 128 + (int)unit * 16 + 8 >= a.k;   // (k is a multiple of 8)
+    const bool half = kInt && (step + i * kSteps) * 128 + (int)unit * 16 + 8 >= a.k;   // (k is a multiple of 8)
 #pragma unroll
     for (int q = 0; q < S::kLoads; ++q) {
       u32x4 v = x[d][q];
@@ -291,7 +294,7 @@ __global__ __launch_bounds__((64 * Shape<XT, R, NT>::kWaves)) void linear_kernel
     }
   };
 
-  const int steps = (kc_n + kWaves * kDepth - 1) / (kWaves * kDepth);
+  const int steps = (kc_n + kSteps * kDepth - 1) / (kSteps * kDepth);
 #pragma unroll
   for (int d = 0; d < S::kAhead; ++d) load_x(d, d);
 #pragma unroll
@@ -316,15 +319,16 @@ __global__ __launch_bounds__((64 * Shape<XT, R, NT>::kWaves)) void linear_kernel
 #pragma unroll
     for (int t = 0; t < NT; ++t) sums[(m * NT + t) * 64 + lane] = total[m][t];
   __syncthreads();
-  for (int at = threadIdx.x; at < MT * NT * 256; at += 64 * kWaves) {
+  for (int at = threadIdx.x; at < R * NT * 16; at += 64 * W) {
     // consecutive threads: consecutive weight rows
-    const int row = at / (16 * NT), nn = at % (16 * NT);
+    const int row = at / (16 * NT) % S::kRows, from = at / (16 * NT) / S::kRows, nn = at % (16 * NT);
     const int m = row / 16, t = nn / 16, l = 16 * (row % 16 / 4) + nn % 16, j = row % 4;
-    const int tok = t0 + row, n = rt0 * 16 + nn;
+    const int tok = blockIdx.y * R + from * S::kRows + row, n = rt0 * 16 + nn;
     if (tok >= a.rows || n >= a.n) continue;
+    const float* part = (const float*)(lds + from * kSteps * S::kLds) + ((m * NT + t) * 64 + l) * 4 + j;
     float v = 0;
 #pragma unroll
-    for (int wv = 0; wv < kWaves; ++wv) v += ((const float*)(lds + wv * S::kLds))[((m * NT + t) * 64 + l) * 4 + j];
+    for (int s = 0; s < kSteps; ++s) v += part[s * (S::kLds / 4)];
     if (kInt && !XG) v *= a.xs[tok];
     if (a.bias) v += a.bias[n];
     const int64_t to = (int64_t)tok * a.y_stride + n;
@@ -334,29 +338,29 @@ __global__ __launch_bounds__((64 * Shape<XT, R, NT>::kWaves)) void linear_kernel
   }
 }
 
-template <int XT, int G, int R, int NT, bool Z, bool XG>
+template <int XT, int G, int R, int NT, int W, bool Z, bool XG>
 hipError_t launch_one(const LinearArgs& a, hipStream_t s) {
-  typedef Shape<XT, R, NT> S;
-  const auto kernel = linear_kernel<XT, G, R, NT, Z, XG>;
+  typedef Shape<XT, R, NT, W> S;
+  const auto kernel = linear_kernel<XT, G, R, NT, W, Z, XG>;
   if (S::kLdsAll > 65536) {
     const hipError_t e = ensure_dyn_lds((const void*)kernel);
     if (e != hipSuccess) return e;
   }
   const dim3 grid((unsigned)(((a.n + 15) / 16 + NT - 1) / NT), (unsigned)((a.rows + R - 1) / R));
-  kernel<<<grid, dim3(64 * S::kWaves), S::kLdsAll, s>>>(a);
+  kernel<<<grid, dim3(64 * W), S::kLdsAll, s>>>(a);
   return hipGetLastError();
 }
 
-template <int XT, int G, int R, int NT>
+template <int XT, int G, int R, int NT, int W>
 hipError_t launch_tiles(const LinearArgs& a, hipStream_t s) {
   constexpr bool kInt = XT == MOE_DT_I8;
-  if (kInt && a.x_group) return a.zeros ? launch_one<XT, G, R, NT, true, kInt>(a, s) : launch_one<XT, G, R, NT, false, kInt>(a, s);
-  return a.zeros ? launch_one<XT, G, R, NT, true, false>(a, s) : launch_one<XT, G, R, NT, false, false>(a, s);
+  if (kInt && a.x_group) return a.zeros ? launch_one<XT, G, R, NT, W, true, kInt>(a, s) : launch_one<XT, G, R, NT, W, false, kInt>(a, s);
+  return a.zeros ? launch_one<XT, G, R, NT, W, true, false>(a, s) : launch_one<XT, G, R, NT, W, false, false>(a, s);
 }
 
 template <int XT, int G, int R>
 hipError_t launch_rows(const LinearArgs& a, int cus, hipStream_t s) {
-  return (a.n + 15) / 16 > cus ? launch_tiles<XT, G, R, 2>(a, s) : launch_tiles<XT, G, R, 1>(a, s);
+  return (a.n + 15) / 16 > cus ? launch_tiles<XT, G, R, 2, R <= 16 ? 8 : 12>(a, s) : launch_tiles<XT, G, R, 1, R <= 16 ? 8 : 16>(a, s);
 }
 
 template <int XT, int G>
