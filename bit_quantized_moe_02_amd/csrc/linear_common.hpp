@@ -130,14 +130,16 @@ struct Shape {
   static constexpr int kLds = kXTile > kSums ? kXTile : kSums;       // of a wave
   // (rows past kRows: whatever lies behind them, in its wave's or a neighbour's part)
   static constexpr int kLdsAll = (W - 1) * kLds + (kLds > 2048 * kXBytes * kMt ? kLds : 2048 * kXBytes * kMt);
-  static constexpr int kAhead = kMt == 1 ? 2 : 1;                    // tiles of x in flight
+  // Tiles in flight, of x and of the weights alike: loads are waited for in the order in which they were issued, so a
+  // later x would hold up the weights in front of it.
+  static constexpr int kDepth = R <= 16 ? 2 : 1;
 };
 
 // Z: with zero points.  XG: 8-bit rows with a scale for each 128 columns.
 template <int XT, int G, int R, int NT, int W, bool Z, bool XG>
 __global__ __launch_bounds__(64 * W) void linear_kernel(LinearArgs a) {
   typedef Shape<XT, R, NT, W> S;
-  constexpr int MT = S::kMt, kSteps = S::kSteps, kGroups = 128 / G, kDepth = 2;
+  constexpr int MT = S::kMt, kSteps = S::kSteps, kGroups = 128 / G, kDepth = S::kDepth;
   constexpr bool kInt = XT == MOE_DT_I8;
   constexpr int kXBytes = S::kXBytes;
   constexpr uint32_t kTile = 1024 + 32 * kGroups + (Z ? 16 * kGroups : 0);
@@ -174,7 +176,7 @@ __global__ __launch_bounds__(64 * W) void linear_kernel(LinearArgs a) {
   const uint8_t* const get = mine + r * (16 * S::kLanesARow);
 
   Weights<G, Z> w[kDepth][NT];
-  u32x4 x[S::kAhead][S::kLoads];
+  u32x4 x[kDepth][S::kLoads];
   f32x4 xg[kDepth][XG ? MT : 1];
   auto load_w = [&](int d, int i) {                                  // of the wave's tile i
     const int kc = step + i * kSteps;
@@ -294,23 +296,32 @@ __global__ __launch_bounds__(64 * W) void linear_kernel(LinearArgs a) {
     }
   };
 
-  const int steps = (kc_n + kSteps * kDepth - 1) / (kSteps * kDepth);
+  const int tiles_n = (kc_n - step + kSteps - 1) / kSteps;            // of this wave (0 where there are fewer than waves)
 #pragma unroll
-  for (int d = 0; d < S::kAhead; ++d) load_x(d, d);
-#pragma unroll
-  for (int d = 0; d < kDepth; ++d) load_w(d, d);
-  for (int i = 0; i < steps; ++i) {
+  for (int d = 0; d < kDepth; ++d) {
+    load_x(d, d);
+    load_w(d, d);
+  }
+  int i = 0;
+  for (; i + kDepth <= tiles_n; i += kDepth) {
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) {
       // (stages mixed up would need more registers than there are)
       __builtin_amdgcn_sched_barrier(0);
-      turn(d % S::kAhead, i * kDepth + d);
-      load_x(d % S::kAhead, i * kDepth + d + S::kAhead);
+      turn(d, i + d);
+      load_x(d, i + d + kDepth);
       __builtin_amdgcn_sched_barrier(0);
       add(d);
       __builtin_amdgcn_sched_barrier(0);
-      load_w(d, (i + 1) * kDepth + d);
+      load_w(d, i + d + kDepth);
     }
+  }
+#pragma unroll
+  for (int d = 0; d < kDepth - 1; ++d) {
+    if (i + d >= tiles_n) break;
+    __builtin_amdgcn_sched_barrier(0);
+    turn(d, i + d);
+    add(d);
   }
 
   f32x4* const sums = (f32x4*)mine;
@@ -360,7 +371,13 @@ hipError_t launch_tiles(const LinearArgs& a, hipStream_t s) {
 
 template <int XT, int G, int R>
 hipError_t launch_rows(const LinearArgs& a, int cus, hipStream_t s) {
-  return (a.n + 15) / 16 > cus ? launch_tiles<XT, G, R, 2, R <= 16 ? 8 : 12>(a, s) : launch_tiles<XT, G, R, 1, R <= 16 ? 8 : 16>(a, s);
+  const int tiles = (a.n + 15) / 16;
+  // several tiles of weights share the rows' way through LDS, as long as there is a workgroup for nearly every compute unit
+  if constexpr (R >= 16) {
+    if (tiles >= cus * 7 / 2) return launch_tiles<XT, G, R, 4, 8>(a, s);
+  }
+  if (tiles > cus) return launch_tiles<XT, G, R, 2, R <= 16 ? 8 : 12>(a, s);
+  return launch_tiles<XT, G, R, 1, R <= 16 ? 8 : 16>(a, s);
 }
 
 template <int XT, int G>
