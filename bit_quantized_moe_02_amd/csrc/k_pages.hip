@@ -13,6 +13,7 @@
 #include <type_traits>
 
 #include "k_step.h"
+#include "launch_util.h"
 
 namespace qmoe {
 namespace {
@@ -28,7 +29,7 @@ struct Scratch {
 
 // Sums of v over the threads before this one and over all of them.  `which` alternates between calls, so that one barrier
 // a call is enough.
-__device__ __forceinline__ int scan(Scratch& s, int which, int v, int* all) {
+__device__ __forceinline__ int scan(Scratch& s, int& which, int v, int* all) {
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   int sum = v;
 #pragma unroll
@@ -45,129 +46,104 @@ __device__ __forceinline__ int scan(Scratch& s, int which, int v, int* all) {
     before += i < wave ? o : 0;
     total += o;
   }
+  which ^= 1;
   *all = total;
   return before + sum - v;
 }
 
-// Which ids of a window of 4096 * S are free: bit 4 i + c of a lane is that of id first_id(base, i) + c.
+// Which ids of a window of 4096 * S are free: words of 64 ids, bit by bit.
 template <int S>
 struct Free {
-  static constexpr int kWindow = kThreads * 4 * S;
-  uint32_t bits;
+  static constexpr int kWords = 64 * S, kWindow = 64 * kWords;
+  uint64_t word[kWords];
 };
 
-template <int S>
-__device__ __forceinline__ uint32_t first_id(int base, int i) {
-  return base + (((int)threadIdx.x / 64 * S + i) * 64 + (int)threadIdx.x % 64) * 4;
+template <int N>
+__device__ __forceinline__ uint32_t or_row(uint32_t v) {       // with the lane N columns on in its row of 16
+  return v | (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + N, 0xF, 0xF, false);
 }
 
-// (ids past the pool are not free)
-template <int S>
-__device__ __forceinline__ Free<S> load_free(const PagesArgs& a, int base) {
-  i32x4 v[S];
+// Of 64 ids from `id` on, those below n.
+__device__ __forceinline__ uint64_t ids_below(uint32_t id, uint32_t n) {
+  return id >= n ? 0 : n - id >= 64 ? ~0ull : (1ull << (n - id)) - 1;
+}
+
+// The window's words (ids past the pool are not free).  A wave's load is 4 ids a lane; 16 lanes put theirs together.
+// kFresh: not from the first-level cache, which does not see the atomics.
+template <bool kFresh = false, int S>
+__device__ __forceinline__ void load_free(const PagesArgs& a, int base, Free<S>& f) {
+  constexpr int kAtOnce = S < 8 ? S : 8;
+  const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  // (past the end of it a buffer reads as zeros)
+  const __amdgpu_buffer_rsrc_t refs = __builtin_amdgcn_make_buffer_rsrc(a.refs, 0, a.n_pages * 4, 0x00027000);
 #pragma unroll
-  for (int i = 0; i < S; ++i) {
-    const uint32_t id = first_id<S>(base, i);
-    v[i] = (i32x4){-1, -1, -1, -1};
-    if (id + 4 <= (uint32_t)a.n_pages) {
-      v[i] = *(const i32x4*)(a.refs + id);
-    } else {
+  for (int i0 = 0; i0 < S; i0 += kAtOnce) {
+    i32x4 v[kAtOnce];
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (id + c < (uint32_t)a.n_pages) v[i][c] = a.refs[id + c];
+    for (int i = 0; i < kAtOnce; ++i)
+      v[i] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(refs, (base + ((i0 + i) * kWaves + wave) * 256 + lane * 4) * 4, 0,
+                                                                               kFresh ? 16 : 0));
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      uint32_t four = 0;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) four |= (uint32_t)(v[i][c] == 0) << c;
+      uint32_t lo = lane & 8 ? 0 : four << (lane % 8 * 4), hi = lane & 8 ? four << (lane % 8 * 4) : 0;
+      lo = or_row<8>(or_row<4>(or_row<2>(or_row<1>(lo))));
+      hi = or_row<8>(or_row<4>(or_row<2>(or_row<1>(hi))));
+      const int at = ((i0 + i) * kWaves + wave) * 4 + lane / 16;
+      if (lane % 16 == 0) f.word[at] = ((uint64_t)hi << 32 | lo) & ids_below(base + at * 64, a.n_pages);
     }
-  }
-  Free<S> r{0};
-#pragma unroll
-  for (int i = 0; i < S; ++i)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) r.bits |= (uint32_t)(v[i][c] == 0) << (4 * i + c);
-  return r;
-}
-
-// How many ids of the wave's part `want` says yes to.
-template <int S, typename Want>
-__device__ __forceinline__ int count(int base, const Free<S>& r, Want want) {
-  int n = 0;
-#pragma unroll
-  for (int i = 0; i < S; ++i) {
-    const uint32_t id = first_id<S>(base, i);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) n += __popcll(__ballot(want(id + c, (r.bits >> (4 * i + c)) & 1)));
-    __builtin_amdgcn_sched_barrier(0);         // (one step's ballots at a time: they are scalar registers)
-  }
-  return n;
-}
-
-// f(id, yes, rank) for every id of the wave's part; rank is `first` and the number of yeses before it.
-template <int S, typename Want, typename F>
-__device__ __forceinline__ void each(int base, const Free<S>& r, int first, Want want, F f) {
-  const int lane = threadIdx.x % 64;
-  const uint64_t below = (1ull << lane) - 1;
-  uint32_t bits = r.bits;
-  asm volatile("" : "+v"(bits));               // (or all ballots are kept from one call to the next, in too many registers)
-#pragma unroll
-  for (int i = 0; i < S; ++i) {
-    const uint32_t id = first_id<S>(base, i);
-    uint64_t yes[4];
-    int rank = first;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      yes[c] = __ballot(want(id + c, (bits >> (4 * i + c)) & 1));
-      rank += __popcll(yes[c] & below);
-      first += __popcll(yes[c]);
-    }
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const bool is = (yes[c] >> lane) & 1;
-      f(id + c, is, rank);
-      rank += is;
-    }
-    __builtin_amdgcn_sched_barrier(0);
+    if (S > kAtOnce) __builtin_amdgcn_sched_barrier(0);
   }
 }
 
-// A wave's number in every lane to the sum of those before it.
-__device__ __forceinline__ int scan_waves(Scratch& s, int which, int v, int* all) {
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  if (lane == 0) s.wave[which][wave] = v;
-  __syncthreads();
-  int before = 0, total = 0;
-#pragma unroll
-  for (int i = 0; i < kWaves; ++i) {
-    const int o = s.wave[which][i];
-    before += i < wave ? o : 0;
-    total += o;
-  }
-  *all = total;
-  return before;
+// A number that is the same in all lanes, as a scalar.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ uint64_t uniform(uint64_t v) {
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 | (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
 }
 
-constexpr int kList = 4096;        // free pages listed at a time
+// Of a (uniform) word's ids a lane takes one: how many set ones come before it.
+__device__ __forceinline__ int set_before(uint64_t w) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(w >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)w, 0));
+}
 
-// Numbers of LDS: sums of the rows' needs and two more numbers a row, and a list of free pages.
+// Numbers of LDS: sums of the rows' needs and another number a row; a list of free pages, as many as there is room for.
 struct Rows {
-  int32_t *needs, *x, *y, *list;
-  __device__ Rows(int32_t* lds, int seqs) : needs(lds + kList), x(needs + seqs), y(x + seqs), list(lds) {}
+  int32_t *needs, *x, *list;
+  int most;
+  __device__ Rows(int32_t* lds, int seqs, int n) : needs(lds), x(needs + seqs), list(x + seqs), most(n) {}
 };
-inline size_t rows_lds(int seqs) { return ((size_t)kList + 3 * (size_t)seqs) * 4; }
+// (one workgroup has all of LDS to itself: 160 KB less what is declared, at most)
+constexpr int kDeclared = 16384;
+inline int list_of(const PagesArgs& a) { return a.n_pages < 36864 - 2 * a.seqs ? a.n_pages : 36864 - 2 * a.seqs; }
+inline size_t rows_lds(const PagesArgs& a) { return ((size_t)list_of(a) + 2 * (size_t)a.seqs) * 4; }
 
 // Gives the rows whose summed needs fit the lowest free pages, in order: give(first, n) is called with pages of ranks
-// first .. first + n - 1 in the list.  Returns how many pages the rows were given.  r: the free pages of the first window.
+// first .. first + n - 1 in the list.  Returns how many pages the rows were given.  f: the words of the first window.
 template <int S, typename Give>
-__device__ __forceinline__ int grant(const PagesArgs& a, Scratch& s, const Rows& rows, int total, Free<S>& r, Give give) {
+__device__ __forceinline__ int grant(const PagesArgs& a, Scratch& s, int& which, const Rows& rows, int total, Free<S>& f, Give give) {
   constexpr int kWindow = Free<S>::kWindow;
   if (total == 0) return 0;
-  const auto is_free = [](uint32_t, bool yes) { return yes; };
   __shared__ int32_t fits;
-  int free_pages = 0, mine = 0, before = 0, which = 0;
-  for (int base = 0; base < a.n_pages && free_pages < total; base += kWindow) {
-    if (base) r = load_free<S>(a, base);
-    mine = count(base, r, is_free);
+  // A thread has one word: its free pages, and the rank of the first of them.
+  uint64_t bits = 0;
+  int rank = 0;
+  auto ranks = [&](int passed) {
+    bits = threadIdx.x < Free<S>::kWords ? f.word[threadIdx.x] : 0;
     int all;
-    before = scan_waves(s, which, mine, &all);
-    which ^= 1;
-    free_pages += all;
+    rank = passed + scan(s, which, __popcll(bits), &all);
+    return all;
+  };
+  int free_pages = 0;
+  for (int base = 0; base < a.n_pages && free_pages < total; base += kWindow) {
+    if (base) {
+      __syncthreads();
+      load_free<true>(a, base, f);
+      __syncthreads();
+    }
+    free_pages += ranks(free_pages);
   }
   int granted = total;
   if (free_pages < total) {
@@ -178,29 +154,22 @@ __device__ __forceinline__ int grant(const PagesArgs& a, Scratch& s, const Rows&
     __syncthreads();
     granted = fits;
   }
-  const bool one = a.n_pages <= kWindow;
   int passed = 0;                                             // free pages of the windows before
   for (int base = 0; passed < granted; base += kWindow) {
     int all = free_pages;
-    if (!one) {
-      r = load_free<S>(a, base);
-      mine = count(base, r, is_free);
-      before = scan_waves(s, which, mine, &all);
-      which ^= 1;
+    if (a.n_pages > kWindow) {
+      __syncthreads();
+      load_free<true>(a, base, f);
+      __syncthreads();
+      all = ranks(passed);
     }
     const int last = min(granted, passed + all);
-    for (int first = passed; first < last; first += kList) {
-      const int n = min(kList, last - first);
-      if (passed + before < first + n && passed + before + mine > first)
-        each(base, r, passed + before, is_free, [&](uint32_t id, bool yes, int rank) {
-          if (yes && rank >= first && rank < first + n) {
-            rows.list[rank - first] = id;
-            a.refs[id] = 1;
-          }
-        });
+    for (int first = passed; first < last; first += rows.most) {
+      const int end = min(first + rows.most, last);
+      for (; bits && rank < end; ++rank, bits &= bits - 1) rows.list[rank - first] = base + threadIdx.x * 64 + __builtin_ctzll(bits);
       __syncthreads();
-      give(first, n);
-      if (first + n < granted) __syncthreads();               // (the list is written again)
+      give(first, end - first);
+      if (end < granted) __syncthreads();                     // (the list is written again)
     }
     passed += all;
   }
@@ -212,12 +181,14 @@ __device__ __forceinline__ int pages(const PagesArgs& a, int len) { return (len 
 __device__ __forceinline__ bool in_pool(const PagesArgs& a, int p) { return p >= 0 && p < a.n_pages; }
 
 // Entries from..to-1 of a row given back, by `lanes` threads of which this is number `lane`.
+template <int kScope>
 __device__ __forceinline__ void release(const PagesArgs& a, int b, int from, int to, int lane, int lanes) {
   int32_t* row = a.table + b * a.stride;
+#pragma unroll 4
   for (int j = from + lane; j < to; j += lanes) {
     const int p = row[j];
     row[j] = -1;
-    if (in_pool(a, p)) atomicSub(a.refs + p, 1);
+    if (in_pool(a, p)) __hip_atomic_fetch_sub(a.refs + p, 1, __ATOMIC_RELAXED, kScope);
   }
 }
 
@@ -226,32 +197,33 @@ __device__ __forceinline__ void release(const PagesArgs& a, int b, int from, int
 __global__ __launch_bounds__(256) void release_kernel(PagesArgs a, const int32_t* new_lens) {
   const int b = blockIdx.y, old = a.lens[b], to = new_lens[b];
   if (to < 0) return;
-  release(a, b, pages(a, length(a, to)), pages(a, length(a, old)), blockIdx.x * 256 + threadIdx.x, gridDim.x * 256);
+  release<__HIP_MEMORY_SCOPE_AGENT>(a, b, pages(a, length(a, to)), pages(a, length(a, old)), blockIdx.x * 256 + threadIdx.x, gridDim.x * 256);
 }
 
 template <int S>
-__global__ __launch_bounds__(kThreads) void resize_kernel(PagesArgs a, const int32_t* new_lens, int32_t* missing, bool released) {
+__global__ __launch_bounds__(kThreads) void resize_kernel(PagesArgs a, const int32_t* new_lens, int32_t* missing, bool released, int list) {
   extern __shared__ int32_t lds[];
   __shared__ Scratch s;
-  const Rows rows(lds, a.seqs);                                // x: pages held, y: pages wanted
-  Free<S> r = load_free<S>(a, 0);                                         // (for the case that none is given back)
+  __shared__ Free<S> f;
+  const Rows rows(lds, a.seqs, list);                                // x: pages held
   int need_all = 0, which = 0;
   bool drops = false;
   for (int b0 = 0; b0 < a.seqs; b0 += kThreads) {
     const int b = b0 + threadIdx.x;
-    int have = 0, want = 0;
+    int old = 0, to = -1;
     if (b < a.seqs) {
-      const int old = a.lens[b], to = new_lens[b];
-      have = pages(a, length(a, old));
-      want = to < 0 ? have : pages(a, length(a, to));
-      rows.x[b] = have;
-      rows.y[b] = want;
+      old = a.lens[b];
+      to = new_lens[b];
     }
+    if (b0 == 0) load_free(a, 0, f);                           // (for the case that none is given back)
+    const int have = pages(a, length(a, old)), want = to < 0 ? have : pages(a, length(a, to));
     drops |= want < have;
     int all;
     const int before = scan(s, which, max(want - have, 0), &all);
-    which ^= 1;
-    if (b < a.seqs) rows.needs[b] = need_all + before + max(want - have, 0);
+    if (b < a.seqs) {
+      rows.x[b] = have;
+      rows.needs[b] = need_all + before + max(want - have, 0);
+    }
     need_all += all;
   }
   // 16 threads a row, or as many as there are for fewer than 64 rows
@@ -259,17 +231,27 @@ __global__ __launch_bounds__(kThreads) void resize_kernel(PagesArgs a, const int
   while (lanes < kThreads && lanes * a.seqs < kThreads) lanes *= 2;
   const int group = threadIdx.x / lanes, groups = kThreads / lanes, lane = threadIdx.x % lanes;
   if (__syncthreads_or(drops && !released)) {
-    for (int b = group; b < a.seqs; b += groups) release(a, b, rows.y[b], rows.x[b], lane, lanes);
-    __threadfence();
+    for (int b = group; b < a.seqs; b += groups) {
+      const int to = new_lens[b];
+      if (to >= 0) release<__HIP_MEMORY_SCOPE_WORKGROUP>(a, b, pages(a, length(a, to)), rows.x[b], lane, lanes);
+    }
+    // (the counts are this workgroup's alone: its atomics done, in the second-level cache, is enough)
+    __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
-    r = load_free<S>(a, 0);
+    load_free<true>(a, 0, f);
+    __syncthreads();
   }
-  const int granted = grant(a, s, rows, need_all, r, [&](int first, int n) {
+  const int granted = grant(a, s, which, rows, need_all, f, [&](int first, int n) {
     for (int b = group; b < a.seqs; b += groups) {
       const int end = rows.needs[b], begin = b ? rows.needs[b - 1] : 0;
       if (end <= first || begin >= first + n) continue;
       int32_t* to = a.table + b * a.stride + rows.x[b] - begin;
-      for (int i = max(begin, first) + lane; i < min(end, first + n); i += lanes) to[i] = rows.list[i - first];
+#pragma unroll 4
+      for (int i = max(begin, first) + lane; i < min(end, first + n); i += lanes) {
+        const int p = rows.list[i - first];
+        to[i] = p;
+        a.refs[p] = 1;
+      }
     }
   });
   for (int b = threadIdx.x; b < a.seqs; b += kThreads) {
@@ -281,58 +263,60 @@ __global__ __launch_bounds__(kThreads) void resize_kernel(PagesArgs a, const int
 
 template <int S>
 __global__ __launch_bounds__(kThreads) void fork_kernel(PagesArgs a, const int32_t* from, int32_t* missing, int32_t* head,
-                                                        ForkJob* jobs) {
+                                                        ForkJob* jobs, int list) {
   extern __shared__ int32_t lds[];
   __shared__ Scratch s;
-  const Rows rows(lds, a.seqs);                                // x: the row's job (-1: none), y: its new length (-1: as it is)
-  Free<S> r = load_free<S>(a, 0);
+  __shared__ Free<S> f;
+  const Rows rows(lds, a.seqs, list);                                // x: the row's job (-1: none)
   int sums = 0, which = 0;                                     // jobs, and in the upper half needs, of the rows before
   for (int b0 = 0; b0 < a.seqs; b0 += kThreads) {
     const int b = b0 + threadIdx.x;
-    int need = 0, len = 0;
+    int need = 0, p = -1, own = 0;
     ForkJob job{b, -1, -1, -1, 0};
     if (b < a.seqs) {
-      const int p = from[b], own = length(a, a.lens[b]);
-      if (p >= 0 && p < a.seqs) {
-        len = length(a, a.lens[p]);
-        const int rest = len & ((1 << a.shift) - 1);
-        if (len > 0 && (p == b ? rest > 0 : own == 0)) {
-          if (rest) {
-            const int last = a.table[p * a.stride + (len >> a.shift)];
-            job.src = in_pool(a, last) ? last : -1;
-            // (a page of its own already needs no other)
-            need = p != b || (job.src >= 0 && a.refs[job.src] > 1);
-            job.blocks = (rest + 15) / 16;
-          }
-          if (p != b || need) job.parent = p;
+      p = from[b];
+      own = length(a, a.lens[b]);
+    }
+    if (b0 == 0) load_free(a, 0, f);
+    if (p >= 0 && p < a.seqs) {
+      const int len = length(a, a.lens[p]), rest = len & ((1 << a.shift) - 1);
+      if (len > 0 && (p == b ? rest > 0 : own == 0)) {
+        if (rest) {
+          const int last = a.table[p * a.stride + (len >> a.shift)];
+          job.src = in_pool(a, last) ? last : -1;
+          // (a page of its own already needs no other)
+          need = p != b || (job.src >= 0 && a.refs[job.src] > 1);
+          job.blocks = (rest + 15) / 16;
         }
+        if (p != b || need) job.parent = p;
       }
     }
     int all;
     const int before = sums + scan(s, which, (job.parent >= 0) | need << 16, &all);
-    which ^= 1;
     sums += all;
     if (job.parent >= 0) jobs[before & 0xFFFF] = job;
     if (b < a.seqs) {
       rows.needs[b] = (before >> 16) + need;
       rows.x[b] = job.parent >= 0 ? before & 0xFFFF : -1;
-      rows.y[b] = job.parent >= 0 && job.parent != b ? len : -1;
     }
   }
   const int need_all = sums >> 16;
-  __threadfence();
   __syncthreads();
-  const int granted = grant(a, s, rows, need_all, r, [&](int first, int n) {
+  const int granted = grant(a, s, which, rows, need_all, f, [&](int first, int n) {
     for (int b = threadIdx.x; b < a.seqs; b += kThreads) {
       const int end = rows.needs[b], begin = b ? rows.needs[b - 1] : 0;
-      if (end > begin && begin >= first && begin < first + n) jobs[rows.x[b]].dst = rows.list[begin - first];
+      if (end > begin && begin >= first && begin < first + n) {
+        const int p = rows.list[begin - first];
+        jobs[rows.x[b]].dst = p;
+        a.refs[p] = 1;
+      }
     }
   });
   for (int b = threadIdx.x; b < a.seqs; b += kThreads) {
     if (rows.x[b] < 0) continue;
-    const int end = rows.needs[b], need = end - (b ? rows.needs[b - 1] : 0);
+    const int end = rows.needs[b], need = end - (b ? rows.needs[b - 1] : 0), p = from[b];
     if (need && end > granted) jobs[rows.x[b]].parent = -1;
-    else if (rows.y[b] >= 0) a.lens[b] = rows.y[b];
+    else if (p != b) a.lens[b] = length(a, a.lens[p]);         // (a parent's own length does not change here)
   }
   if (threadIdx.x == 0) {
     *head = sums & 0xFFFF;
@@ -409,37 +393,54 @@ __global__ __launch_bounds__(kCopyThreads) void fork_copy_kernel(PagesArgs a, co
 
 template <int S>
 __global__ __launch_bounds__(kThreads) void compact_kernel(PagesArgs a, int32_t* held, int32_t* ws) {
-  constexpr int kWindow = Free<S>::kWindow;
+  constexpr int kWindow = Free<S>::kWindow, kWords = Free<S>::kWords;
   __shared__ Scratch s;
+  __shared__ Free<S> f;
+  __shared__ int32_t filled[kWords], moving[kWords];           // ranks of a word's first hole and moving page
   int32_t *rank = ws + 4, *dst = rank + a.n_pages, *src = dst + a.n_pages;
-  Free<S> r{0};
-  int n = 0, which = 0, all;
+  const int t = threadIdx.x, lane = t % 64, wave = uniform(t / 64);
+  int n = a.n_pages, which = 0, all;
   for (int base = 0; base < a.n_pages; base += kWindow) {
-    r = load_free<S>(a, base);
-    scan_waves(s, which, count(base, r, [&](uint32_t id, bool free) { return id < (uint32_t)a.n_pages && !free; }), &all);
-    which ^= 1;
-    n += all;
+    load_free(a, base, f);
+    __syncthreads();
+    scan(s, which, t < kWords ? __popcll(f.word[t]) : 0, &all);
+    n -= all;
+    if (a.n_pages > kWindow) __syncthreads();                  // (the words are written again)
   }
-  const auto hole = [=](uint32_t id, bool free) { return id < (uint32_t)n && free; };
-  const auto move = [&](uint32_t id, bool free) { return id >= (uint32_t)n && id < (uint32_t)a.n_pages && !free; };
   int holes = 0, moves = 0;                                    // of the windows before
   for (int base = 0; base < a.n_pages; base += kWindow) {
-    if (a.n_pages > kWindow) r = load_free<S>(a, base);
-    const int hole0 = holes + scan_waves(s, which, count(base, r, hole), &all);
-    which ^= 1;
+    if (a.n_pages > kWindow) {
+      load_free(a, base, f);
+      __syncthreads();
+    }
+    uint64_t hole = 0, move = 0;
+    if (t < kWords) {
+      const uint32_t id = base + t * 64;
+      hole = f.word[t] & ids_below(id, n);
+      move = ~f.word[t] & ~ids_below(id, n) & ids_below(id, a.n_pages);
+    }
+    const int k = holes + scan(s, which, __popcll(hole), &all);
     holes += all;
-    const int move0 = moves + scan_waves(s, which, count(base, r, move), &all);
-    which ^= 1;
+    const int l = moves + scan(s, which, __popcll(move), &all);
     moves += all;
-    each(base, r, hole0, hole, [&](uint32_t id, bool yes, int k) {
-      if (yes) dst[k] = id;
-    });
-    each(base, r, move0, move, [&](uint32_t id, bool yes, int k) {
-      if (yes) src[k] = id;
-      if (id >= (uint32_t)n && id < (uint32_t)a.n_pages) rank[id] = yes ? k : -1;
-    });
+    if (t < kWords) {
+      filled[t] = k;
+      moving[t] = l;
+    }
+    __syncthreads();
+    for (int i = wave; i < kWords; i += kWaves) {
+      const uint32_t id = base + i * 64, p = id + lane;
+      if (id >= (uint32_t)a.n_pages) break;
+      const uint64_t w = uniform(f.word[i]), low = ids_below(id, n), hole = w & low, move = ~w & ~low & ids_below(id, a.n_pages);
+      if (__builtin_amdgcn_inverse_ballot_w64(hole)) dst[filled[i] + set_before(hole)] = p;
+      const bool moved = __builtin_amdgcn_inverse_ballot_w64(move);
+      const int number = moving[i] + set_before(move);
+      if (moved) src[number] = p;
+      if (p >= (uint32_t)n && p < (uint32_t)a.n_pages) rank[p] = moved ? number : -1;
+    }
+    __syncthreads();
   }
-  if (threadIdx.x == 0) {
+  if (t == 0) {
     ws[0] = moves;
     ws[1] = n;
     if (held) *held = n;
@@ -475,18 +476,17 @@ __global__ __launch_bounds__(kCopyThreads) void compact_copy_kernel(PagesArgs a,
   }
 }
 
-// Pools of more than 32768 pages are gone through in windows of that many.
+// Pools of more than 65536 pages are gone through in windows of that many.
 template <typename F>
 void by_size(const PagesArgs& a, F f) {
   if (a.n_pages <= Free<1>::kWindow) f(std::integral_constant<int, 1>());
   else if (a.n_pages <= Free<4>::kWindow) f(std::integral_constant<int, 4>());
-  else f(std::integral_constant<int, 8>());
+  else f(std::integral_constant<int, 16>());
 }
 
 }  // namespace
 
 hipError_t launch_resize(const PagesArgs& a, const int32_t* new_lens, int32_t* missing, hipStream_t s) {
-  // 256 rows of up to 256 pages, half of which end: 48 us by one workgroup, ?? by two launches; one row: ?? and ??
   const bool many = (int64_t)a.seqs * a.per_seq > 8192;
   if (many) {
     const int x = a.per_seq < 1024 ? 1 : a.per_seq < 8192 ? a.per_seq / 1024 : 8;
@@ -494,20 +494,26 @@ hipError_t launch_resize(const PagesArgs& a, const int32_t* new_lens, int32_t* m
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
+  hipError_t e = hipSuccess;
   by_size(a, [&](auto steps) {
-    resize_kernel<steps.value><<<dim3(1), dim3(kThreads), rows_lds(a.seqs), s>>>(a, new_lens, missing, many);
+    const auto kernel = resize_kernel<steps.value>;
+    if (rows_lds(a) > 32768) e = ensure_dyn_lds((const void*)kernel, kDeclared);
+    if (e == hipSuccess) kernel<<<dim3(1), dim3(kThreads), rows_lds(a), s>>>(a, new_lens, missing, many, list_of(a));
   });
-  return hipGetLastError();
+  return e == hipSuccess ? hipGetLastError() : e;
 }
 
 hipError_t launch_fork(const PagesArgs& a, const int32_t* from, int32_t* missing, void* ws, const PageCopy* c, int n_caches, int cus,
                        hipStream_t s) {
   int32_t* head = (int32_t*)ws;
   ForkJob* jobs = (ForkJob*)((uint8_t*)ws + kForkHead);
+  hipError_t e = hipSuccess;
   by_size(a, [&](auto steps) {
-    fork_kernel<steps.value><<<dim3(1), dim3(kThreads), rows_lds(a.seqs), s>>>(a, from, missing, head, jobs);
+    const auto kernel = fork_kernel<steps.value>;
+    if (rows_lds(a) > 32768) e = ensure_dyn_lds((const void*)kernel, kDeclared);
+    if (e == hipSuccess) kernel<<<dim3(1), dim3(kThreads), rows_lds(a), s>>>(a, from, missing, head, jobs, list_of(a));
   });
-  hipError_t e = hipGetLastError();
+  if (e == hipSuccess) e = hipGetLastError();
   for (int at = 0; e == hipSuccess && (at == 0 || at < n_caches); at += kCachesALaunch) {
     const int n = n_caches - at < kCachesALaunch ? n_caches - at : kCachesALaunch;
     fork_copy_kernel<<<dim3(4 * cus), dim3(kCopyThreads), 0, s>>>(a, head, jobs, c[at / kCachesALaunch], n > 0 ? n : 1, at == 0);

@@ -195,7 +195,7 @@ namespace {
 
 int check_pages(const char* who, const moe_kv_pool* pool, const moe_kv_tables* t, PagesArgs* a) {
   if (!pool || !t) return bad(who, "pool or tables is NULL");
-  if (pool->n_pages < 1 || pool->n_pages > (1 << 30)) return bad(who, "need 1 <= n_pages <= 2^30");
+  if (pool->n_pages < 1 || pool->n_pages > (1 << 29)) return bad(who, "need 1 <= n_pages <= 2^29");
   if (pool->n_caches < 0 || pool->n_caches > kMaxCaches || (pool->n_caches > 0 && !pool->caches))
     return bad(who, "need 0 <= n_caches <= 256, and caches");
   if (!pool->refs || !aligned(pool->refs, 16)) return bad(who, "refs must be 16-byte aligned memory");
