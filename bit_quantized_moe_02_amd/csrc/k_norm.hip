@@ -1,10 +1,23 @@
 // Root-mean-square norm with the residual's addition (moe_rms_norm).
 //
-// Memory bound: each value is read and written once.  A vector stays in
+//   h = x + residual, rounded to the residual's type;  y = h / sqrt(mean(h^2) + eps) * weight
+//
+// Bytes bound it: each value is read and written once, a vector staying in
 // registers, 8 columns a thread and pass, between the sum of its squares and the
-// outputs.  Vectors of up to 512 columns take the least power of two of lanes
-// that holds them (several to a wave, no barrier); longer ones a workgroup of 8
-// columns a thread, up to 1024 threads, then two passes of that.
+// outputs.  The sum of squares is held in 64 bits, and where y becomes 8-bit codes so is y:
+// a code next to the border of two is then the one of the formula.  In 64 bits that is some 10 operations a
+// value, 2 to 5 % of the time of many vectors and 0.5 us of a few long ones'.
+//
+// Vectors of up to 512 columns take the least power of two of lanes that holds
+// them (several to a wave, no barrier); longer ones a workgroup of 8 columns a
+// thread, up to 1024 threads, then two passes of that.  Half the threads with twice
+// the passes were slower for 4096 columns (1 row 3.7 for 3.2 us) and 16384 (8192 rows 239
+// for 227) and no faster for 7168.  Lanes add up by moves between registers; through LDS'
+// exchange the same sums cost 0.2 to 0.5 us a call.
+//
+// bf16, sum and outputs: 4096 rows of 7168 columns to bf16 46 us (5.2 TB/s), to codes
+// 48, to both 54; 8192 of 16384 to codes 211 (4.5).  One row of 512 2.1 us (an empty kernel
+// 2.0), of 7168 3.0, as codes 3.9; 64 rows of 7168 as codes 4.3.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -97,8 +110,69 @@ __device__ __forceinline__ void weight8(const NormArgs& a, int col, float* f) {
   }
 }
 
+// The whole number next to q (|q| < 2^31; the even one of two): 1.5 * 2^52 leaves it in the lower bits of the sum.
+__device__ __forceinline__ int whole(double q) {
+#pragma clang fp contract(off)
+  const double at = q + 6755399441055744.0;
+  return (int)__builtin_bit_cast(uint64_t, at);
+}
+
 // |y| as an unsigned number, which orders as |y| does, not a number on top.
 __device__ __forceinline__ uint32_t size_bits(float y) { return __builtin_bit_cast(uint32_t, y) & 0x7FFFFFFFu; }
+
+// The value of the lane d away (d < 16; of lanes that hold the same values in each d).
+template <int D>
+__device__ __forceinline__ uint32_t beside(uint32_t v) {
+  constexpr int kMove = D == 1 ? 0xB1 : D == 2 ? 0x4E : D == 4 ? 0x141 : 0x140;   // within four lanes, mirrored within 8, within 16
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kMove, 0xF, 0xF, true);
+}
+template <int D>
+__device__ __forceinline__ double beside(double v) {
+  const u32x2 b = __builtin_bit_cast(u32x2, v);
+  const uint32_t lo = b[0], hi = b[1];
+  return __builtin_bit_cast(double, (u32x2){beside<D>(lo), beside<D>(hi)});
+}
+// Both values of lanes d away (16: next rows of 16; 32: the halves of the wave), the same two in both.
+template <int D>
+__device__ __forceinline__ u32x2 both(uint32_t v) {
+  return __builtin_bit_cast(u32x2, D == 16 ? __builtin_amdgcn_permlane16_swap(v, v, false, false) : __builtin_amdgcn_permlane32_swap(v, v, false, false));
+}
+template <int LANES>
+__device__ __forceinline__ double sum_of(double v) {   // of LANES neighbours, to each
+  if constexpr (LANES >= 2) v += beside<1>(v);
+  if constexpr (LANES >= 4) v += beside<2>(v);
+  if constexpr (LANES >= 8) v += beside<4>(v);
+  if constexpr (LANES >= 16) v += beside<8>(v);
+  if constexpr (LANES >= 32) {
+    const u32x2 b = __builtin_bit_cast(u32x2, v);
+    const uint32_t lo = b[0], hi = b[1];
+    const u32x2 l = both<16>(lo), h = both<16>(hi);
+    v = __builtin_bit_cast(double, (u32x2){l[0], h[0]}) + __builtin_bit_cast(double, (u32x2){l[1], h[1]});
+  }
+  if constexpr (LANES >= 64) {
+    const u32x2 b = __builtin_bit_cast(u32x2, v);
+    const uint32_t lo = b[0], hi = b[1];
+    const u32x2 l = both<32>(lo), h = both<32>(hi);
+    v = __builtin_bit_cast(double, (u32x2){l[0], h[0]}) + __builtin_bit_cast(double, (u32x2){l[1], h[1]});
+  }
+  return v;
+}
+template <int LANES>
+__device__ __forceinline__ uint32_t max_of(uint32_t v) {
+  if constexpr (LANES >= 2) v = max(v, beside<1>(v));
+  if constexpr (LANES >= 4) v = max(v, beside<2>(v));
+  if constexpr (LANES >= 8) v = max(v, beside<4>(v));
+  if constexpr (LANES >= 16) v = max(v, beside<8>(v));
+  if constexpr (LANES >= 32) {
+    const u32x2 b = both<16>(v);
+    v = max(b[0], b[1]);
+  }
+  if constexpr (LANES >= 64) {
+    const u32x2 b = both<32>(v);
+    v = max(b[0], b[1]);
+  }
+  return v;
+}
 
 constexpr int kResNone = -1;
 
@@ -154,15 +228,13 @@ __global__ __launch_bounds__(LANES <= 64 ? 256 : LANES) void norm_kernel(NormArg
     for (int i = 0; i < 8; ++i) ss = fma((double)h[p][i], (double)h[p][i], ss);
   }
   if (!a.out && !a.codes) return;
-#pragma unroll
-  for (int d = 1; d < (kWave ? LANES : 64); d *= 2) ss += __shfl_xor(ss, d);
+  ss = sum_of<kWave ? LANES : 64>(ss);
   if (!kWave) {
     if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = ss;
     __syncthreads();
-    ss = 0;
-    for (int i = 0; i < kWaves; ++i) ss += part[i];
+    ss = sum_of<kWaves>(part[threadIdx.x % kWaves]);
   }
-  const double inv = 1.0 / sqrt(ss / a.cols + (double)a.eps);
+  const double inv = rsqrt(ss * a.per_col + (double)a.eps);
 
   if (a.out) {
     const float f = (float)inv;
@@ -179,25 +251,26 @@ __global__ __launch_bounds__(LANES <= 64 ? 256 : LANES) void norm_kernel(NormArg
   // 8 bits: y in 64 bits, its sizes compared as 32-bit numbers (rounding keeps their order)
   uint32_t m[PASSES];
   uint32_t all = 0;
+  double y[PASSES][8];
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
     m[p] = 0;
-    for (int i = 0; i < 8; ++i) m[p] = max(m[p], size_bits((float)((double)h[p][i] * inv * (double)w[p][i])));
+    for (int i = 0; i < 8; ++i) {
+      y[p][i] = (double)h[p][i] * inv * (double)w[p][i];
+      m[p] = max(m[p], size_bits((float)y[p][i]));
+    }
     all = max(all, m[p]);
   }
   const int groups = a.group ? (a.cols + a.group - 1) / a.group : 1;
   if (a.group) {                                       // 128 columns: 16 lanes
 #pragma unroll
-    for (int p = 0; p < PASSES; ++p)
-#pragma unroll
-      for (int d = 1; d < (LANES < 16 ? LANES : 16); d *= 2) m[p] = max(m[p], (uint32_t)__shfl_xor((int)m[p], d));
+    for (int p = 0; p < PASSES; ++p) m[p] = max_of<LANES < 16 ? LANES : 16>(m[p]);
   } else {
-#pragma unroll
-    for (int d = 1; d < (kWave ? LANES : 64); d *= 2) all = max(all, (uint32_t)__shfl_xor((int)all, d));
+    all = max_of<kWave ? LANES : 64>(all);
     if (!kWave) {
       if (threadIdx.x % 64 == 0) top[threadIdx.x / 64] = all;
       __syncthreads();
-      for (int i = 0; i < kWaves; ++i) all = max(all, top[i]);
+      all = max_of<kWaves>(top[threadIdx.x % kWaves]);
     }
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) m[p] = all;
@@ -211,10 +284,10 @@ __global__ __launch_bounds__(LANES <= 64 ? 256 : LANES) void norm_kernel(NormArg
     const double back = fine && scale > 0 ? 1.0 / (double)scale : 0.0;
     u32x2 c = {0, 0};
     for (int i = 0; i < 8; ++i) {
-      // (nothing not finite gets here: back is 0 then, and its product is taken for 0)
-      double q = back == 0.0 ? 0.0 : rint((double)h[p][i] * inv * (double)w[p][i] * back);
-      q = fmin(fmax(q, -127.0), 127.0);
-      c[i / 4] |= ((uint32_t)(int)q & 0xFFu) << (8 * (i % 4));
+      // Nothing not finite gets here: back is 0 then, and its product is taken for 0.  (Scales below the normal numbers
+      // are so much rounded that codes can pass 127, to 190 at most.)
+      const int q = back == 0.0 ? 0 : min(max(whole(y[p][i] * back), -127), 127);
+      c[i / 4] |= ((uint32_t)q & 0xFFu) << (8 * (i % 4));
     }
     *(u32x2*)(a.codes + row * a.cs + first + col) = c;
     const int g = a.group ? col / a.group : 0;

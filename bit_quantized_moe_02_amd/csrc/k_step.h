@@ -17,6 +17,7 @@ struct NormArgs {
   int rows, heads, cols, group;     // group 0: the whole vector
   int xt, rt, wt, ot;
   float eps;
+  double per_col;                   // 1 / cols
 };
 hipError_t launch_norm(const NormArgs& a, hipStream_t s);
 

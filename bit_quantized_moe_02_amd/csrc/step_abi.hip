@@ -118,6 +118,7 @@ extern "C" int moe_rms_norm(const moe_norm* p, void* stream) {
   a.cs = p->codes_stride;
   a.scs = p->scale_stride;
   a.rows = p->rows;
+  a.per_col = 1.0 / p->cols;
   a.heads = p->heads;
   a.cols = p->cols;
   a.group = p->group;
