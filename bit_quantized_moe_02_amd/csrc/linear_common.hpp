@@ -1,12 +1,19 @@
 // Products of a few rows with 4-bit weights (moe_linear): the kernel, built
 // for each type of row by k_linear_bf16.hip, k_linear_f16.hip, k_linear_i8.hip.
 //
-// Weight bytes bound it.  A workgroup of 8 waves takes NT tiles of 16 weight rows and all
-// of k: the waves take its tiles of 128 columns in turn, so the workgroup reads
-// one contiguous run of memory, and add their sums up through LDS in wave order (no
-// workspace, no atomics).  A lane's 16 bytes of a tile are its operand of four
-// 16x16x32 products (lane c = 16*g + r: weight row r, 8 columns of each); the rows of
-// x are the other operand, 16 * MT of them at once, read from the caches.
+// A workgroup takes NT tiles of 16 weight rows, up to R rows of x and all of k: its
+// waves take the tiles' steps of 128 columns in turn, so the workgroup reads one
+// contiguous run of memory for each tile, and add their sums up through LDS in wave
+// order (no workspace, no atomics).  A lane's 16 bytes of a tile are its operand of four
+// 16x16x32 products (lane c = 16*g + r: weight row r, 8 columns of each); the rows of x are
+// read in whole stretches and turned into the other operand through the wave's own part of LDS: read as
+// operands, a request for each lane, 64 rows of 7168 codes took 58 us for 16.5.
+//
+// Few rows are bound by the weights' bytes, many by the issue of what a tile's codes and scales need
+// (64 rows: vector instructions 45 %, matrix instructions 27 % of the time, waits the rest).
+// 1 row times 32771 x 7168 24 us in bf16 (scales of 128, 5.0 TB/s), 26 as codes with scales of 32 (5.1); 16 rows of bf16
+// times 7168 x 7168 8.8 us; 64 rows times 7168 x 7168 19.6 us in bf16, 12.5 as codes (525 TFLOP/s); times 28672 x 7168 57
+// and 45.
 //
 // Codes enter the products exactly.  16-bit rows: q goes into the upper
 // mantissa bits of 1.0, u = 1 + q/16 (shift, mask, exclusive or: the codes are stored as q ^ 8),
@@ -194,7 +201,9 @@ __global__ __launch_bounds__(64 * W) void linear_kernel(LinearArgs a) {
     for (int q = 0; q < S::kLoads; ++q)
       x[d][q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(xs, xrow[q] + at, 0, 0));
   };
+  // (the lanes of a wave exchange x through its part of LDS, whose operations are done in order)
   auto turn = [&](int d, int i) {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     const bool half = kInt && (step + i * kSteps) * 128 + (int)unit * 16 + 8 >= a.k;   // (k is a multiple of 8)
 #pragma unroll
     for (int q = 0; q < S::kLoads; ++q) {
@@ -203,6 +212,7 @@ __global__ __launch_bounds__(64 * W) void linear_kernel(LinearArgs a) {
       const uint32_t row = q * S::kRowsALoad + lrow;
       *(u32x4*)(put + q * 1024 + 16 * (unit ^ (row & (S::kLanesARow - 1)))) = v;
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   };
   auto operand = [&](int m, int c) {                                 // 8 columns of row 16 m + r, 32 c + 8 g and on
     if constexpr (kInt) return *(const u32x2*)(get + m * 2048 + 16 * ((2 * c + (g >> 1)) ^ (r & 7)) + 8 * (g & 1));
@@ -380,12 +390,18 @@ hipError_t launch_rows(const LinearArgs& a, int cus, hipStream_t s) {
   return launch_tiles<XT, G, R, 1, R <= 16 ? 8 : 16>(a, s);
 }
 
+// The least rows a workgroup that leave no more workgroups than compute units (each reads the weights, from the caches
+// but once), else as many as there are, up to 64.  Of k = 7168, 64 rows in bf16 times 256 weight rows: 4.5 us with 4, 5.5
+// with 16, 11.8 with 64; times 512, where 4 make 512 workgroups: 6.6, 5.7, 12.9; times 4096, 256 tiles: 37, 17.6, 16.0.
+// 16 rows times 1024: 4.5 with 4, 5.5 with 16; times 2048, 512 workgroups again: 6.6 and 5.8.
 template <int XT, int G>
 hipError_t launch_group(const LinearArgs& a, int cus, hipStream_t s) {
   constexpr int kFew = XT == MOE_DT_I8 ? 8 : 4;        // rows of one load
-  if (a.rows <= kFew) return launch_rows<XT, G, kFew>(a, cus, s);
-  if (a.rows <= 16) return launch_rows<XT, G, 16>(a, cus, s);
-  if (a.rows <= 32) return launch_rows<XT, G, 32>(a, cus, s);
+  const int64_t tiles = (a.n + 15) / 16;
+  const auto take = [&](int r) { return a.rows <= r || tiles * ((a.rows + r - 1) / r) <= cus; };
+  if (take(kFew)) return launch_rows<XT, G, kFew>(a, cus, s);
+  if (take(16)) return launch_rows<XT, G, 16>(a, cus, s);
+  if (take(32)) return launch_rows<XT, G, 32>(a, cus, s);
   return launch_rows<XT, G, 64>(a, cus, s);
 }
 
