@@ -9,10 +9,11 @@
 // read in whole stretches and turned into the other operand through the wave's own part of LDS: read as
 // operands, a request for each lane, 64 rows of 7168 codes took 58 us for 16.5.
 //
-// Few rows are bound by the weights' bytes, many by the issue of what a tile's codes and scales need
-// (64 rows: vector instructions 45 %, matrix instructions 27 % of the time, waits the rest).
-// 1 row times 32771 x 7168 24 us in bf16 (scales of 128, 5.0 TB/s), 26 as codes with scales of 32 (5.1); 16 rows of bf16
-// times 7168 x 7168 8.8 us; 64 rows times 7168 x 7168 19.6 us in bf16, 12.5 as codes (525 TFLOP/s); times 28672 x 7168 57
+// Few rows are bound by the weights' bytes, many by what a compute unit has to do for them, of which none alone is near its
+// peak: of 64 rows of bf16 times 7168 x 7168, 16.7 us, by count matrix instructions are 4 us, vector instructions that make operands
+// of codes 5, x from the second-level cache 4 and through LDS 4.
+// 1 row times 32771 x 7168 24.3 us in bf16 (scales of 128, 5.0 TB/s), 25.7 as codes with scales of 32 (5.1); 16 rows of bf16
+// times 7168 x 7168 8.4 us; 64 rows times 7168 x 7168 16.7 us in bf16, 12.1 as codes (545 TFLOP/s); times 28672 x 7168 57
 // and 45.
 //
 // Codes enter the products exactly.  16-bit rows: q goes into the upper
@@ -122,13 +123,14 @@ __device__ __forceinline__ int zero_of(const Weights<G, Z>& w, int i, uint32_t l
   return (int)(int8_t)z;
 }
 
-// How a workgroup of W waves is made for up to R rows of x and NT tiles of 16 weight rows.
-template <int XT, int R, int NT, int W>
+// How a workgroup is made for up to R rows of x and NT tiles of 16 weight rows.  (12 or 16 waves were not faster for any
+// R and NT: they have no registers for what 8 have in flight.)
+constexpr int kWaves = 8;
+template <int XT, int R, int NT>
 struct Shape {
   static constexpr int kXBytes = XT == MOE_DT_I8 ? 1 : 2;
-  // A wave takes up to 32 rows: 16 waves then have registers (128 each) for what they have in flight.  For more rows
-  // waves of the same columns go side by side and read the same weights.
-  static constexpr int kRows = R < 32 ? R : 32, kSides = R / kRows, kSteps = W / kSides;
+  // A wave takes up to 32 rows.  For more rows waves of the same columns go side by side and read the same weights.
+  static constexpr int kRows = R < 32 ? R : 32, kSides = R / kRows, kSteps = kWaves / kSides;
   static constexpr int kMt = (kRows + 15) / 16;                      // 16-row operands of x
   static constexpr int kLanesARow = 8 * kXBytes;                     // 16 bytes of a row's 128 columns a lane
   static constexpr int kRowsALoad = 64 / kLanesARow;
@@ -136,16 +138,16 @@ struct Shape {
   static constexpr int kXTile = 1024 * kLoads, kSums = kMt * NT * 1024;
   static constexpr int kLds = kXTile > kSums ? kXTile : kSums;       // of a wave
   // (rows past kRows: whatever lies behind them, in its wave's or a neighbour's part)
-  static constexpr int kLdsAll = (W - 1) * kLds + (kLds > 2048 * kXBytes * kMt ? kLds : 2048 * kXBytes * kMt);
+  static constexpr int kLdsAll = (kWaves - 1) * kLds + (kLds > 2048 * kXBytes * kMt ? kLds : 2048 * kXBytes * kMt);
   // Tiles in flight, of x and of the weights alike: loads are waited for in the order in which they were issued, so a
   // later x would hold up the weights in front of it.
   static constexpr int kDepth = R <= 16 ? 2 : 1;
 };
 
 // Z: with zero points.  XG: 8-bit rows with a scale for each 128 columns.
-template <int XT, int G, int R, int NT, int W, bool Z, bool XG>
-__global__ __launch_bounds__(64 * W) void linear_kernel(LinearArgs a) {
-  typedef Shape<XT, R, NT, W> S;
+template <int XT, int G, int R, int NT, bool Z, bool XG>
+__global__ __launch_bounds__(64 * kWaves) void linear_kernel(LinearArgs a) {
+  typedef Shape<XT, R, NT> S;
   constexpr int MT = S::kMt, kSteps = S::kSteps, kGroups = 128 / G, kDepth = S::kDepth;
   constexpr bool kInt = XT == MOE_DT_I8;
   constexpr int kXBytes = S::kXBytes;
@@ -309,8 +311,11 @@ __global__ __launch_bounds__(64 * W) void linear_kernel(LinearArgs a) {
   const int tiles_n = (kc_n - step + kSteps - 1) / kSteps;            // of this wave (0 where there are fewer than waves)
 #pragma unroll
   for (int d = 0; d < kDepth; ++d) {
+    // (in the loop's order: a wait there is for as many loads as may be behind the one it is for on every way to it)
     load_x(d, d);
+    __builtin_amdgcn_sched_barrier(0);
     load_w(d, d);
+    __builtin_amdgcn_sched_barrier(0);
   }
   int i = 0;
   for (; i + kDepth <= tiles_n; i += kDepth) {
@@ -340,7 +345,7 @@ __global__ __launch_bounds__(64 * W) void linear_kernel(LinearArgs a) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) sums[(m * NT + t) * 64 + lane] = total[m][t];
   __syncthreads();
-  for (int at = threadIdx.x; at < R * NT * 16; at += 64 * W) {
+  for (int at = threadIdx.x; at < R * NT * 16; at += 64 * kWaves) {
     // consecutive threads: consecutive weight rows
     const int row = at / (16 * NT) % S::kRows, from = at / (16 * NT) / S::kRows, nn = at % (16 * NT);
     const int m = row / 16, t = nn / 16, l = 16 * (row % 16 / 4) + nn % 16, j = row % 4;
@@ -359,50 +364,67 @@ __global__ __launch_bounds__(64 * W) void linear_kernel(LinearArgs a) {
   }
 }
 
-template <int XT, int G, int R, int NT, int W, bool Z, bool XG>
+template <int XT, int G, int R, int NT, bool Z, bool XG>
 hipError_t launch_one(const LinearArgs& a, hipStream_t s) {
-  typedef Shape<XT, R, NT, W> S;
-  const auto kernel = linear_kernel<XT, G, R, NT, W, Z, XG>;
+  typedef Shape<XT, R, NT> S;
+  const auto kernel = linear_kernel<XT, G, R, NT, Z, XG>;
   if (S::kLdsAll > 65536) {
     const hipError_t e = ensure_dyn_lds((const void*)kernel);
     if (e != hipSuccess) return e;
   }
   const dim3 grid((unsigned)(((a.n + 15) / 16 + NT - 1) / NT), (unsigned)((a.rows + R - 1) / R));
-  kernel<<<grid, dim3(64 * W), S::kLdsAll, s>>>(a);
+  kernel<<<grid, dim3(64 * kWaves), S::kLdsAll, s>>>(a);
   return hipGetLastError();
 }
 
-template <int XT, int G, int R, int NT, int W>
+template <int XT, int G, int R, int NT>
 hipError_t launch_tiles(const LinearArgs& a, hipStream_t s) {
   constexpr bool kInt = XT == MOE_DT_I8;
-  if (kInt && a.x_group) return a.zeros ? launch_one<XT, G, R, NT, W, true, kInt>(a, s) : launch_one<XT, G, R, NT, W, false, kInt>(a, s);
-  return a.zeros ? launch_one<XT, G, R, NT, W, true, false>(a, s) : launch_one<XT, G, R, NT, W, false, false>(a, s);
+  if (kInt && a.x_group) return a.zeros ? launch_one<XT, G, R, NT, true, kInt>(a, s) : launch_one<XT, G, R, NT, false, kInt>(a, s);
+  return a.zeros ? launch_one<XT, G, R, NT, true, false>(a, s) : launch_one<XT, G, R, NT, false, false>(a, s);
 }
 
-template <int XT, int G, int R>
-hipError_t launch_rows(const LinearArgs& a, int cus, hipStream_t s) {
-  const int tiles = (a.n + 15) / 16;
-  // several tiles of weights share the rows' way through LDS, as long as there is a workgroup for nearly every compute unit
-  if constexpr (R >= 16) {
-    if (tiles >= cus * 7 / 2) return launch_tiles<XT, G, R, 4, 8>(a, s);
-  }
-  if (tiles > cus) return launch_tiles<XT, G, R, 2, R <= 16 ? 8 : 12>(a, s);
-  return launch_tiles<XT, G, R, 1, R <= 16 ? 8 : 16>(a, s);
-}
+// A workgroup of R rows and NT tiles: more of either share what the other's operands cost, in fewer workgroups.
+struct Choice {
+  int rows, tiles;
+  int one, more;                                       // 0.1 us a round for k = 7168: one workgroup a compute unit, and where there are more rounds
+};
+constexpr Choice kChoices16[] = {{4, 1, 28, 25},   {4, 2, 40, 49},   {4, 4, 83, 98},    {16, 1, 39, 35},   {16, 2, 56, 52},
+                                 {16, 4, 86, 100}, {32, 2, 93, 81},  {32, 4, 139, 142}, {64, 4, 250, 250}};
+constexpr Choice kChoices8[] = {{8, 1, 24, 24},  {8, 2, 32, 44},  {8, 4, 70, 83},   {16, 1, 26, 26}, {16, 2, 38, 44},
+                                {16, 4, 63, 86}, {32, 2, 55, 53}, {32, 4, 93, 100}, {64, 4, 164, 175}};
 
-// The least rows a workgroup that leave no more workgroups than compute units (each reads the weights, from the caches
-// but once), else as many as there are, up to 64.  Of k = 7168, 64 rows in bf16 times 256 weight rows: 4.5 us with 4, 5.5
-// with 16, 11.8 with 64; times 512, where 4 make 512 workgroups: 6.6, 5.7, 12.9; times 4096, 256 tiles: 37, 17.6, 16.0.
-// 16 rows times 1024: 4.5 with 4, 5.5 with 16; times 2048, 512 workgroups again: 6.6 and 5.8.
+// The choice whose workgroups, a compute unit at a time, take the least time.  Of k = 7168, 64 rows of bf16 times 256
+// weight rows: 4.6 us with 4 rows and a tile a workgroup, 12 with 64 and one; times 4096: 10.8 with 16 and 4, 11.5 with 32 and
+// 2, 14.9 with 64 and one; times 7168: 16.1 with 32 and 4, 18.6 with 32 and 2, 24.3 with 64 and 4; times 28672: 67.7, 76 (64 and
+// 2) and 55.  As codes times 4096: 8.3, 7.7 and 10.0.  One row times 7168: 6.7 with 2 tiles, 6.9 with one, 8.7 with 4.
+// Where there are many rounds the last is not full, and the choices are within a tenth of each other.
 template <int XT, int G>
 hipError_t launch_group(const LinearArgs& a, int cus, hipStream_t s) {
-  constexpr int kFew = XT == MOE_DT_I8 ? 8 : 4;        // rows of one load
+  constexpr const auto& kChoices = XT == MOE_DT_I8 ? kChoices8 : kChoices16;
   const int64_t tiles = (a.n + 15) / 16;
-  const auto take = [&](int r) { return a.rows <= r || tiles * ((a.rows + r - 1) / r) <= cus; };
-  if (take(kFew)) return launch_rows<XT, G, kFew>(a, cus, s);
-  if (take(16)) return launch_rows<XT, G, 16>(a, cus, s);
-  if (take(32)) return launch_rows<XT, G, 32>(a, cus, s);
-  return launch_rows<XT, G, 64>(a, cus, s);
+  int best = 0;
+  int64_t least = INT64_MAX;
+  for (int i = 0; i < 9; ++i) {
+    const Choice& c = kChoices[i];
+    const int64_t parts = (a.rows + c.rows - 1) / c.rows, rounds = (parts * ((tiles + c.tiles - 1) / c.tiles) + cus - 1) / cus;
+    const int64_t time = rounds == 1 ? c.one : rounds * c.more;
+    if (time < least && parts <= 65535) {              // (the grid's second dimension)
+      least = time;
+      best = i;
+    }
+  }
+  switch (best) {
+    case 0: return launch_tiles<XT, G, kChoices[0].rows, 1>(a, s);
+    case 1: return launch_tiles<XT, G, kChoices[1].rows, 2>(a, s);
+    case 2: return launch_tiles<XT, G, kChoices[2].rows, 4>(a, s);
+    case 3: return launch_tiles<XT, G, 16, 1>(a, s);
+    case 4: return launch_tiles<XT, G, 16, 2>(a, s);
+    case 5: return launch_tiles<XT, G, 16, 4>(a, s);
+    case 6: return launch_tiles<XT, G, 32, 2>(a, s);
+    case 7: return launch_tiles<XT, G, 32, 4>(a, s);
+    default: return launch_tiles<XT, G, 64, 4>(a, s);
+  }
 }
 
 }  // namespace
