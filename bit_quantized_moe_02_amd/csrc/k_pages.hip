@@ -75,13 +75,13 @@ __device__ __forceinline__ void load_free(const PagesArgs& a, int base, Free<S>&
   constexpr int kAtOnce = S < 8 ? S : 8;
   const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   // (past the end of it a buffer reads as zeros)
-  const __amdgpu_buffer_rsrc_t refs = __builtin_amdgcn_make_buffer_rsrc(a.refs, 0, a.n_pages * 4, 0x00027000);
+  const __amdgpu_buffer_rsrc_t refs = __builtin_amdgcn_make_buffer_rsrc(a.refs, 0, (int)((uint32_t)a.n_pages * 4), 0x00027000);
 #pragma unroll
   for (int i0 = 0; i0 < S; i0 += kAtOnce) {
     i32x4 v[kAtOnce];
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i)
-      v[i] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(refs, (base + ((i0 + i) * kWaves + wave) * 256 + lane * 4) * 4, 0,
+      v[i] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(refs, ((uint32_t)base + ((i0 + i) * kWaves + wave) * 256 + lane * 4) * 4, 0,
                                                                                kFresh ? 16 : 0));
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) {

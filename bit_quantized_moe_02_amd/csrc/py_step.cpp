@@ -65,6 +65,12 @@ bool scales_of(PyObject* o, int64_t groups, int64_t rows, int64_t dev, float** p
   return true;
 }
 
+// The storage holds the last group's scales up to the next multiple of 4 rows.
+bool whole_scales(PyObject* o, int64_t groups, int64_t rows, int64_t stride) {
+  const at::Tensor& t = THPVariable_Unpack(o);
+  return (t.storage_offset() + (groups - 1) * stride + (rows + 3) / 4 * 4) * 4 <= (int64_t)t.storage().nbytes();
+}
+
 }  // namespace
 
 // step_use(norm, linear, resize, fork, compact): addresses of the library's functions
@@ -135,7 +141,9 @@ PyObject* step_linear(PyObject*, PyObject* const* args, Py_ssize_t n) {
       return refused();
     float* scales = nullptr;
     int64_t scale_stride = 0;
-    if (a.a[7] != Py_None && !scales_of(a.a[7], group ? (wk + group - 1) / group : 1, x.rows, dev, &scales, &scale_stride))
+    const int64_t groups = group ? (wk + group - 1) / group : 1;
+    if (a.a[7] != Py_None && (!scales_of(a.a[7], groups, x.rows, dev, &scales, &scale_stride) ||
+                              (group && !whole_scales(a.a[7], groups, x.rows, scale_stride))))
       return refused();
     const auto w = (const moe_linear_weights*)a.addr(0);
     void* const stream = a.addr(4);

@@ -17,7 +17,7 @@ using namespace qmoe;
 namespace {
 
 constexpr int64_t kMaxRows = 1 << 24;
-constexpr int64_t kMaxProductRows = 1 << 20;     // (64 to a workgroup, numbered in the grid's second dimension)
+constexpr int64_t kMaxProductRows = 1 << 20;     // (at 64 to a workgroup they fit the grid's second dimension)
 constexpr int64_t kMaxStride = 1 << 24;
 constexpr int64_t kMaxGrid = (1 << 24) - 1;      // workgroups: 32-bit thread numbers with up to 256 threads each
 constexpr int kMaxCaches = 256;
@@ -95,6 +95,7 @@ extern "C" int moe_rms_norm(const moe_norm* p, void* stream) {
   }
   if (p->out && (p->out == p->sum || (const void*)p->out == (const void*)p->codes)) return bad(who, "outputs must not overlap");
   if (p->codes && (const void*)p->codes == (const void*)p->sum) return bad(who, "outputs must not overlap");
+  if (p->codes && ((const void*)p->codes == p->x || (const void*)p->codes == p->residual)) return bad(who, "codes must not overlap inputs");
   if ((rc = check_place(who, "sum", p->sum, p->residual_dtype, p->sum_stride, "x", p->x, p->x_dtype, p->x_stride)) != MOE_OK) return rc;
   if ((rc = check_place(who, "sum", p->sum, p->residual_dtype, p->sum_stride, "residual", p->residual, p->residual_dtype,
                         p->residual_stride)) != MOE_OK)

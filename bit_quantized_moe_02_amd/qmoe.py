@@ -875,7 +875,10 @@ def moe_linear(w, x, y, x_scales=None, x_group=0, stream=None):
                 if t.shape[1:].numel() != cols or t.shape[0] != x.shape[0]:
                     raise ValueError(f"{name} has shape {tuple(t.shape)}; the call needs [{x.shape[0]}, {cols}]")
             if x_scales is not None and x_group >= 0:
-                _look_scales(x_scales, "x_scales", moe_scales_shape(x.shape[0], w.k, x_group)[0], x.shape[0], dev)
+                groups, most = moe_scales_shape(x.shape[0], w.k, x_group)
+                _look_scales(x_scales, "x_scales", groups, x.shape[0], dev)
+                if x_group and x_scales.storage_offset() + (groups - 1) * x_scales.stride(0) + most > x_scales.untyped_storage().nbytes() // 4:
+                    raise ValueError(f"x_scales' last group must have room for {most} rows")
         _refused(rc, [])
 
 

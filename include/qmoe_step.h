@@ -51,10 +51,10 @@ extern "C" {
  *   vector v, group g is scales[(v * groups + g) * scale_stride + r], with
  *   scale_stride a multiple of 4, at least rows.
  * Sums of squares are 64-bit (no overflow for any input).
- * At least one of out, codes and sum is wanted; sum needs a residual.  sum may be the
- * residual or x itself, out may be x, residual or... any input whose rows it
- * takes the place of exactly (same type and stride); outputs must not overlap
- * inputs or each other otherwise.  rows = 0: nothing is done (the rows may be NULL). */
+ * At least one of out, codes and sum is wanted; sum needs a residual.  sum may
+ * be x or the residual, and out too, where type and stride are the same, so
+ * that each row takes its own place; outputs must not overlap inputs or each
+ * other otherwise.  rows = 0: nothing is done (the rows may be NULL). */
 typedef struct moe_norm {
   int32_t rows;
   int32_t heads;
@@ -143,11 +143,13 @@ typedef struct moe_linear_weights {
  *   y     y_dtype MOE_DT_BF16, MOE_DT_F16 or MOE_DT_F32, rows y_stride elements apart (at
  *         least n, at most 2^24).
  * Codes and products are exact; 16-bit rows' sums are 32-bit ones, 8-bit
- * rows' are exact inside a group of columns that share both scales and 32-bit between them; the result is
- * rounded once.  A row that holds a value that is not finite gives infinities or
- * not a number; other rows are not touched by it.  Meant for few rows (1 to 64 share one
- * reading of the weights); any number up to 2^20 works.  rows = 0: nothing is done
- * (the rows may be NULL).  y must not overlap the inputs. */
+ * rows' are exact inside a group of columns that share both scales and 32-bit
+ * between them; the result is rounded once.  16-bit rows: twice the sum of a
+ * group's |x| must be below 2^128, or the row overflows.  A row that holds a
+ * value that is not finite gives infinities or not a number; other rows are
+ * not touched by it.  Meant for few rows (1 to 64 share one reading of the
+ * weights); any number up to 2^20 works.  rows = 0: nothing is done (the rows
+ * may be NULL).  y must not overlap the inputs. */
 int moe_linear(const moe_linear_weights* w, int32_t rows, int x_dtype, const void* x, int64_t x_stride,
                const float* x_scales, int64_t scale_stride, int32_t x_group, int y_dtype, void* y, int64_t y_stride,
                void* stream);
@@ -155,10 +157,11 @@ int moe_linear(const moe_linear_weights* w, int32_t rows, int x_dtype, const voi
 /* ---------------------------------------------------------------------------
  * Pages of a cache (include/qmoe_attn.h), kept on the GPU.
  *
- * A pool: n_pages pages, which every one of its caches (the layers of a model;
- * they may differ in heads, not in n_pages and page_tokens; a host array of n_caches, at most 256,
- * read during the call) holds a part of (their scales may be 4-byte aligned here), and refs, device int32 [n_pages]: how many
- * table entries name each page, 0: free.  A new pool is refs of zeros. */
+ * A pool: n_pages (1 to 2^29) pages, which every one of its caches holds a part
+ * of, and refs, device int32 [n_pages]: how many table entries name each page,
+ * 0: free.  A new pool is refs of zeros.  caches is a host array of n_caches (0
+ * to 256: a model's layers), read during the call; they may differ in heads, not
+ * in n_pages and page_tokens, and their scales may be 4-byte aligned here. */
 typedef struct moe_kv_pool {
   int32_t n_pages;
   int32_t n_caches;
@@ -169,8 +172,8 @@ typedef struct moe_kv_pool {
 /* Rows of a page table, one a sequence: row b, of kv_lens[b] positions, holds
  * pages page_table[b][0 .. held-1], held = ceil(kv_lens[b] / page_tokens).
  * page_table: device int32 [seqs][pages_per_seq], rows table_stride apart;
- * kv_lens: device int32 [seqs].  These are moe_kv_batch's.  seqs is 1 to 4096, seqs *
- * pages_per_seq at most 2^30, pages_per_seq * page_tokens too.
+ * kv_lens: device int32 [seqs].  These are moe_kv_batch's.  seqs is 1 to 4096,
+ * seqs * pages_per_seq at most 2^30, pages_per_seq * page_tokens too.
  * Lengths outside [0, pages_per_seq * page_tokens] count as the nearest in it;
  * an entry that names no page of the pool is passed over. */
 typedef struct moe_kv_tables {
@@ -182,9 +185,10 @@ typedef struct moe_kv_tables {
   int32_t* kv_lens;
 } moe_kv_tables;
 
-/* Gives every row b the length new_lens[b] (device int32 [seqs]; negative: the row
- * is left alone).  First rows that get shorter give back the pages they no longer need (their
- * entries become -1; a page is free when its last holder gives it back).
+/* Gives every row b the length new_lens[b] (device int32 [seqs]; negative: the
+ * row is left alone).  First rows that get shorter give back the pages they no
+ * longer need (their entries become -1; a page is free when its last holder
+ * gives it back).
  * Then rows that get longer take free pages: the lowest ids, in ascending order
  * of row and position.  When there are too few, the rows up to the first
  * one that lacks pages get theirs, and that one and the later ones that
@@ -195,8 +199,8 @@ typedef struct moe_kv_tables {
 int moe_kv_resize(const moe_kv_pool* pool, const moe_kv_tables* tables, const int32_t* new_lens, int32_t* missing,
                   void* stream);
 
-/* Lets row b go on from row a = from[b] (device int32 [seqs]; outside of [0, seqs): row b is left
- * alone).  Row b has to be of length 0 and row a longer (both before the call;
+/* Lets row b go on from row a = from[b] (device int32 [seqs]; outside of [0,
+ * seqs): row b is left alone).  Row b has to be of length 0 and row a longer (both before the call;
  * other rows b are left alone).  Row b gets row a's length, shares its full
  * pages, and gets a page of its own for the positions behind them, whose blocks
  * of 16 positions are copied in every cache.

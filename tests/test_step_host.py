@@ -123,7 +123,7 @@ def _norm(q, **kw):
     dict(codes=5 * P + 8), dict(codes_stride=100), dict(scales=P + 4), dict(scale_stride=2), dict(scale_stride=6), dict(scale_stride=0),
     dict(out=None, codes=None, scales=None, sum=None), dict(out=3 * P), dict(codes=3 * P), dict(codes=4 * P),
     dict(sum=P, sum_stride=136), dict(sum=2 * P, sum_stride=136), dict(sum=P, x_dtype=1), dict(out=P, out_stride=256),
-    dict(out=2 * P, out_dtype=1)])
+    dict(out=2 * P, out_dtype=1), dict(codes=P), dict(codes=2 * P)])
 def test_norm_refused(q, kw):
     assert _norm(q, **kw) == q.MOE_ERR_INVALID_ARG and "moe_rms_norm" in q.moe_last_error()
 
