@@ -235,11 +235,13 @@ __global__ __launch_bounds__(kThreads) void resize_kernel(PagesArgs a, const int
       const int to = new_lens[b];
       if (to >= 0) release<__HIP_MEMORY_SCOPE_WORKGROUP>(a, b, pages(a, length(a, to)), rows.x[b], lane, lanes);
     }
-    // (the counts are this workgroup's alone: its atomics done, in the second-level cache, is enough)
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    load_free<true>(a, 0, f);
-    __syncthreads();
+    if (need_all) {
+      // (the counts are this workgroup's alone: its atomics done, in the second-level cache, is enough)
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();
+      load_free<true>(a, 0, f);
+      __syncthreads();
+    }
   }
   const int granted = grant(a, s, which, rows, need_all, f, [&](int first, int n) {
     for (int b = group; b < a.seqs; b += groups) {
