@@ -19,7 +19,9 @@ namespace qmoe {
 namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+
+// v with the (uniform) word in one lane: there is no builtin for the instruction.
+extern "C" __device__ uint32_t write_lane(uint32_t word, uint32_t lane, uint32_t v) __asm("llvm.amdgcn.writelane.i32");
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
 
@@ -27,27 +29,32 @@ struct Scratch {
   int32_t wave[2][kWaves];
 };
 
+// Sums over the lanes up to this one, by moves between registers.
+__device__ __forceinline__ int scan_row(int v) {               // of 16
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  return v;
+}
+__device__ __forceinline__ int scan_wave(int v) {
+  v = scan_row(v);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // the last of the row before, to the second and fourth
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // the last of the first half, to the second
+  return v;
+}
+
 // Sums of v over the threads before this one and over all of them.  `which` alternates between calls, so that one barrier
 // a call is enough.
 __device__ __forceinline__ int scan(Scratch& s, int& which, int v, int* all) {
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  int sum = v;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const int o = __shfl_up(sum, d);
-    if (lane >= d) sum += o;
-  }
+  const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int sum = scan_wave(v);
   if (lane == 63) s.wave[which][wave] = sum;
   __syncthreads();
-  int before = 0, total = 0;
-#pragma unroll
-  for (int i = 0; i < kWaves; ++i) {
-    const int o = s.wave[which][i];
-    before += i < wave ? o : 0;
-    total += o;
-  }
+  const int waves = scan_row(s.wave[which][lane % kWaves]);    // (16 waves)
+  const int before = wave ? __builtin_amdgcn_readlane(waves, wave - 1) : 0;
   which ^= 1;
-  *all = total;
+  *all = __builtin_amdgcn_readlane(waves, kWaves - 1);
   return before + sum - v;
 }
 
@@ -58,44 +65,37 @@ struct Free {
   uint64_t word[kWords];
 };
 
-template <int N>
-__device__ __forceinline__ uint32_t or_row(uint32_t v) {       // with the lane N columns on in its row of 16
-  return v | (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + N, 0xF, 0xF, false);
-}
-
 // Of 64 ids from `id` on, those below n.
 __device__ __forceinline__ uint64_t ids_below(uint32_t id, uint32_t n) {
   return id >= n ? 0 : n - id >= 64 ? ~0ull : (1ull << (n - id)) - 1;
 }
 
-// The window's words (ids past the pool are not free).  A wave's load is 4 ids a lane; 16 lanes put theirs together.
+// The window's words (ids past the pool are not free).  A wave's load is a word's 64 ids, a lane keeps one of its wave's
+// words: a comparison and two moves a word.  (Four ids a lane, put together by 16 lanes, took 4 us of a window of 65536.)
 // kFresh: not from the first-level cache, which does not see the atomics.
 template <bool kFresh = false, int S>
 __device__ __forceinline__ void load_free(const PagesArgs& a, int base, Free<S>& f) {
-  constexpr int kAtOnce = S < 8 ? S : 8;
-  const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  constexpr int kLoads = Free<S>::kWords / kWaves, kAtOnce = kLoads < 16 ? kLoads : 16;
+  const uint32_t lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   // (past the end of it a buffer reads as zeros)
   const __amdgpu_buffer_rsrc_t refs = __builtin_amdgcn_make_buffer_rsrc(a.refs, 0, (int)((uint32_t)a.n_pages * 4), 0x00027000);
+  uint32_t lo = 0, hi = 0;
 #pragma unroll
-  for (int i0 = 0; i0 < S; i0 += kAtOnce) {
-    i32x4 v[kAtOnce];
+  for (int i0 = 0; i0 < kLoads; i0 += kAtOnce) {
+    if ((uint32_t)base + i0 * kWaves * 64 >= (uint32_t)a.n_pages) break;
+    int v[kAtOnce];
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i)
-      v[i] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(refs, ((uint32_t)base + ((i0 + i) * kWaves + wave) * 256 + lane * 4) * 4, 0,
-                                                                               kFresh ? 16 : 0));
+      v[i] = __builtin_amdgcn_raw_buffer_load_b32(refs, ((uint32_t)base + ((i0 + i) * kWaves + wave) * 64 + lane) * 4, 0, kFresh ? 16 : 0);
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) {
-      uint32_t four = 0;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) four |= (uint32_t)(v[i][c] == 0) << c;
-      uint32_t lo = lane & 8 ? 0 : four << (lane % 8 * 4), hi = lane & 8 ? four << (lane % 8 * 4) : 0;
-      lo = or_row<8>(or_row<4>(or_row<2>(or_row<1>(lo))));
-      hi = or_row<8>(or_row<4>(or_row<2>(or_row<1>(hi))));
-      const int at = ((i0 + i) * kWaves + wave) * 4 + lane / 16;
-      if (lane % 16 == 0) f.word[at] = ((uint64_t)hi << 32 | lo) & ids_below(base + at * 64, a.n_pages);
+      const uint64_t w = __builtin_amdgcn_ballot_w64(v[i] == 0);
+      lo = write_lane((uint32_t)w, i0 + i, lo);
+      hi = write_lane((uint32_t)(w >> 32), i0 + i, hi);
     }
-    if (S > kAtOnce) __builtin_amdgcn_sched_barrier(0);
   }
+  const int at = lane * kWaves + wave;
+  if (lane < kLoads) f.word[at] = ((uint64_t)hi << 32 | lo) & ids_below((uint32_t)base + at * 64, a.n_pages);
 }
 
 // A number that is the same in all lanes, as a scalar.
