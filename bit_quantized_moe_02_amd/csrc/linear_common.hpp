@@ -10,7 +10,7 @@
 // operands, a request for each lane, 64 rows of 7168 codes took 58 us for 16.5.
 //
 // Few rows are bound by the weights' bytes, many by what a compute unit has to do for them, of which none alone is near its
-// peak: of 64 rows of bf16 times 7168 x 7168, 16.7 us, by count matrix instructions are 4 us, vector instructions that make operands
+// peak: of 64 rows of bf16 times 7168 x 7168, 16.5 us, by count matrix instructions are 4 us, vector instructions that make operands
 // of codes 5, x from the second-level cache 4 and through LDS 4.
 // 1 row times 32771 x 7168 24.3 us in bf16 (scales of 128, 5.0 TB/s), 25.7 as codes with scales of 32 (5.1); 16 rows of bf16
 // times 7168 x 7168 8.4 us; 64 rows times 7168 x 7168 16.7 us in bf16, 12.1 as codes (545 TFLOP/s); times 28672 x 7168 57
