@@ -140,8 +140,10 @@ struct Shape {
   // (rows past kRows: whatever lies behind them, in its wave's or a neighbour's part)
   static constexpr int kLdsAll = (kWaves - 1) * kLds + (kLds > 2048 * kXBytes * kMt ? kLds : 2048 * kXBytes * kMt);
   // Tiles in flight, of x and of the weights alike: loads are waited for in the order in which they were issued, so a
-  // later x would hold up the weights in front of it.
-  static constexpr int kDepth = R <= 16 ? 2 : 1;
+  // later x would hold up the weights in front of it.  One row times 4096 x 7168 5.0 us with two, 5.8 with one, 5.3 with
+  // three; with more to do for a tile one is enough and its registers are better free: 32 rows of bf16 times 4096 8.4 with
+  // two, 7.9 with one.
+  static constexpr int kDepth = R < 16 || (R == 16 && (NT == 1 || kXBytes == 1)) ? 2 : 1;
 };
 
 // Z: with zero points.  XG: 8-bit rows with a scale for each 128 columns.
