@@ -229,6 +229,7 @@ __global__ __launch_bounds__(64 * kWaves) void linear_kernel(LinearArgs a) {
     for (int t = 0; t < NT; ++t) total[m][t] = (f32x4){0, 0, 0, 0};
 
   auto add = [&](int d) {
+    [[maybe_unused]] f32x4 part[MT][NT];
 #pragma unroll
     for (int gi = 0; gi < kGroups; ++gi) {
       if constexpr (!kInt) {
@@ -293,20 +294,38 @@ __global__ __launch_bounds__(64 * kWaves) void linear_kernel(LinearArgs a) {
             }
           }
         }
+        // Sums and zero points times sums are below 2^23 in size: exact in 32-bit numbers, whose products take a quarter
+        // of the time of whole ones'.
+        f32x4 sum[MT];
+        if constexpr (Z) {
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum[m][j] = (float)accx[m][j];
+        }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           const float s = 0.0625f * scale_of(w[d][t], gi, lane);
-          const int z = Z ? 16 * zero_of(w[d][t], gi, lane) : 0;
+          const float z = Z ? -16.0f * (float)zero_of(w[d][t], gi, lane) : 0.0f;
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              // (below 2^24 in size: exact)
-              const float v = (float)(Z ? acc[m][t][j] - z * accx[m][j] : acc[m][t][j]);
-              total[m][t][j] = fmaf(XG ? s * xg[d][XG ? m : 0][j] : s, v, total[m][t][j]);
+              float v = (float)acc[m][t][j];
+              if constexpr (Z) v = fmaf(z, sum[m][j], v);
+              if constexpr (!XG) total[m][t][j] = fmaf(s, v, total[m][t][j]);
+              else part[m][t][j] = gi ? fmaf(s, v, part[m][t][j]) : s * v;
             }
         }
       }
+    }
+    if constexpr (XG) {                                              // the 128 columns' scale of the rows
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) total[m][t][j] = fmaf(xg[d][m][j], part[m][t][j], total[m][t][j]);
     }
   };
 
