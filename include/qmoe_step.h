@@ -200,12 +200,12 @@ int moe_kv_resize(const moe_kv_pool* pool, const moe_kv_tables* tables, const in
                   void* stream);
 
 /* Lets row b go on from row a = from[b] (device int32 [seqs]; outside of [0,
- * seqs): row b is left alone).  Row b has to be of length 0 and row a longer (both before the call;
- * other rows b are left alone).  Row b gets row a's length, shares its full
- * pages, and gets a page of its own for the positions behind them, whose blocks
- * of 16 positions are copied in every cache.
- * from[b] = b: where row b ends inside a page that others hold too, it gets a copy of
- * that page of its own instead.
+ * seqs): row b is left alone).  Row b has to be of length 0 and row a longer
+ * (both before the call; other rows b are left alone).  Row b gets row a's
+ * length, shares its full pages, and gets a page of its own for the positions
+ * behind them, whose blocks of 16 positions are copied in every cache.
+ * from[b] = b: where row b ends inside a page that others hold too, it gets a
+ * copy of that page of its own instead.
  * Pages are taken and `missing` counted as by moe_kv_resize (a row that lacks
  * its page stays as it is); pages that this call frees are not taken in it.
  * ws: device scratch, no initialization needed; calls that overlap in
@@ -214,11 +214,11 @@ size_t moe_kv_fork_workspace_bytes(const moe_kv_pool* pool, const moe_kv_tables*
 int moe_kv_fork(const moe_kv_pool* pool, const moe_kv_tables* tables, const int32_t* from, int32_t* missing, void* ws,
                 size_t ws_bytes, void* stream);
 
-/* Moves held pages (refs not 0) to the low end of the pool: with n of them, those
- * with ids from n on, in ascending order, go into the free ids below n, in
+/* Moves held pages (refs not 0) to the low end of the pool: with n of them,
+ * those with ids from n on, in ascending order, go into the free ids below n, in
  * ascending order; the caches' pages, refs and the rows' entries follow.
  * Entries that name a moved page must all be among the rows of `tables`.
- * held (device int32 [1], NULL: not wanted): n. */
+ * held (device int32 [1], NULL: not wanted): n.  ws as for moe_kv_fork. */
 size_t moe_kv_compact_workspace_bytes(const moe_kv_pool* pool, const moe_kv_tables* tables);
 int moe_kv_compact(const moe_kv_pool* pool, const moe_kv_tables* tables, int32_t* held, void* ws, size_t ws_bytes,
                    void* stream);
