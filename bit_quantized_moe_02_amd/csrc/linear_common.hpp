@@ -13,8 +13,8 @@
 // peak: of 64 rows of bf16 times 7168 x 7168, 16.5 us, by count matrix instructions are 4 us, vector instructions that make operands
 // of codes 5, x from the second-level cache 4 and through LDS 4.
 // 1 row times 32771 x 7168 24.3 us in bf16 (scales of 128, 5.0 TB/s), 25.7 as codes with scales of 32 (5.1); 16 rows of bf16
-// times 7168 x 7168 8.4 us; 64 rows times 7168 x 7168 16.7 us in bf16, 12.1 as codes (545 TFLOP/s); times 28672 x 7168 57
-// and 45.
+// times 7168 x 7168 8.4 us; 64 rows times 7168 x 7168 16.7 us in bf16, 11.3 as codes (582 TFLOP/s); times 28672 x 7168 57
+// and 43.
 //
 // Codes enter the products exactly.  16-bit rows: q goes into the upper
 // mantissa bits of 1.0, u = 1 + q/16 (shift, mask, exclusive or: the codes are stored as q ^ 8),
@@ -76,10 +76,11 @@ __device__ __forceinline__ u32x4 units(uint32_t w) {
   return r;
 }
 
-// The same as 8 signed bytes 16 (q - 8).
-__device__ __forceinline__ u32x2 bytes(uint32_t w) {
-  const uint32_t lo = (w << 4) & 0xF0F0F0F0u, hi = w & 0xF0F0F0F0u;  // columns 0 4 1 5 and 2 6 3 7
-  return (u32x2){__builtin_amdgcn_perm(hi, lo, 0x06040200u), __builtin_amdgcn_perm(hi, lo, 0x07050301u)};
+// The same as 8 signed bytes 16 (q - 8), in the order of columns 0 4 1 5 2 6 3 7.
+__device__ __forceinline__ u32x2 bytes(uint32_t w) { return (u32x2){(w << 4) & 0xF0F0F0F0u, w & 0xF0F0F0F0u}; }
+// 8 bytes of a row in that order.
+__device__ __forceinline__ u32x2 in_order(uint32_t lo, uint32_t hi) {
+  return (u32x2){__builtin_amdgcn_perm(hi, lo, 0x05010400u), __builtin_amdgcn_perm(hi, lo, 0x07030602u)};
 }
 
 // Reads past the end of a buffer give zeros and cost no traffic: what lies past the last
@@ -213,6 +214,11 @@ __global__ __launch_bounds__(64 * kWaves) void linear_kernel(LinearArgs a) {
     for (int q = 0; q < S::kLoads; ++q) {
       u32x4 v = x[d][q];
       if (half) v[2] = 0, v[3] = 0;
+      if constexpr (kInt) {                                          // (once for all of the weights' tiles)
+        const uint32_t x0 = v[0], x1 = v[1], x2 = v[2], x3 = v[3];
+        const u32x2 a = in_order(x0, x1), b = in_order(x2, x3);
+        v = (u32x4){a[0], a[1], b[0], b[1]};
+      }
       const uint32_t row = q * S::kRowsALoad + lrow;
       *(u32x4*)(put + q * 1024 + 16 * (unit ^ (row & (S::kLanesARow - 1)))) = v;
     }
