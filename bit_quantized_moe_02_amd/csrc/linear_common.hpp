@@ -425,7 +425,8 @@ constexpr Choice kChoices8[] = {{8, 1, 24, 24},  {8, 2, 32, 44},  {8, 4, 70, 83}
 // weight rows: 4.6 us with 4 rows and a tile a workgroup, 12 with 64 and one; times 4096: 10.8 with 16 and 4, 11.5 with 32 and
 // 2, 14.9 with 64 and one; times 7168: 16.1 with 32 and 4, 18.6 with 32 and 2, 24.3 with 64 and 4; times 28672: 67.7, 76 (64 and
 // 2) and 55.  As codes times 4096: 8.3, 7.7 and 10.0.  One row times 7168: 6.7 with 2 tiles, 6.9 with one, 8.7 with 4.
-// Where there are many rounds the last is not full, and the choices are within a tenth of each other.
+// Where there are many rounds the last is not full, and the choices are within a tenth of each other.  Groups of 32 have more
+// to do for each tile: 48 rows of fp16 times 4096 x 4096 10.1 with 16 and 4, 9.6 with 32 and 2.
 template <int XT, int G>
 hipError_t launch_group(const LinearArgs& a, int cus, hipStream_t s) {
   constexpr const auto& kChoices = XT == MOE_DT_I8 ? kChoices8 : kChoices16;
@@ -435,7 +436,7 @@ hipError_t launch_group(const LinearArgs& a, int cus, hipStream_t s) {
   for (int i = 0; i < 9; ++i) {
     const Choice& c = kChoices[i];
     const int64_t parts = (a.rows + c.rows - 1) / c.rows, rounds = (parts * ((tiles + c.tiles - 1) / c.tiles) + cus - 1) / cus;
-    const int64_t time = rounds == 1 ? c.one : rounds * c.more;
+    const int64_t time = rounds * ((rounds == 1 ? c.one : c.more) + (G == 32 ? 4 * c.tiles : 0));
     if (time < least && parts <= 65535) {              // (the grid's second dimension)
       least = time;
       best = i;
