@@ -147,9 +147,9 @@ typedef struct moe_linear_weights {
  * between them; the result is rounded once.  16-bit rows: twice the sum of a
  * group's |x| must be below 2^128, or the row overflows.  A row that holds a
  * value that is not finite gives infinities or not a number; other rows are
- * not touched by it.  Meant for few rows (1 to 64 share one reading of the
- * weights); any number up to 2^20 works.  rows = 0: nothing is done (the rows
- * may be NULL).  y must not overlap the inputs. */
+ * not touched by it.  Meant for few rows (the weights are read from memory
+ * once for each 64); any number up to 2^20 works.  rows = 0: nothing is done
+ * (the rows may be NULL).  y must not overlap the inputs. */
 int moe_linear(const moe_linear_weights* w, int32_t rows, int x_dtype, const void* x, int64_t x_stride,
                const float* x_scales, int64_t scale_stride, int32_t x_group, int y_dtype, void* y, int64_t y_stride,
                void* stream);
@@ -161,7 +161,9 @@ int moe_linear(const moe_linear_weights* w, int32_t rows, int x_dtype, const voi
  * of, and refs, device int32 [n_pages]: how many table entries name each page,
  * 0: free.  A new pool is refs of zeros.  caches is a host array of n_caches (0
  * to 256: a model's layers), read during the call; they may differ in heads, not
- * in n_pages and page_tokens, and their scales may be 4-byte aligned here. */
+ * in n_pages and page_tokens, and their scales may be 4-byte aligned here.
+ * Calls on one pool, or on one page table, must come one after the other (one
+ * stream, or events between). */
 typedef struct moe_kv_pool {
   int32_t n_pages;
   int32_t n_caches;
