@@ -110,12 +110,12 @@ __device__ __forceinline__ void weight8(const NormArgs& a, int col, float* f) {
   }
 }
 
-// The whole number next to q (|q| < 2^31; the even one of two): 1.5 * 2^52 leaves it in the lower bits of the sum.
-__device__ __forceinline__ int whole(double q) {
-#pragma clang fp contract(off)
-  const double at = q + 6755399441055744.0;
-  return (int)__builtin_bit_cast(uint64_t, at);
-}
+// For codes, a quotient q of less than 2^19 gets 1.5 * 2^20 + 1/2 + 2^-31 added: the upper word of the sum is the whole
+// number next to q, above kZero, and the lower one, q's distance above the half between two codes, is at most kBorder where
+// q is within 2^-31 of a half.
+constexpr double kToCode = 1572864.5 + 0x1p-31;
+constexpr int kZero = 0x41380000;
+constexpr uint32_t kBorder = 4;
 
 // |y| as an unsigned number, which orders as |y| does, not a number on top.
 __device__ __forceinline__ uint32_t size_bits(float y) { return __builtin_bit_cast(uint32_t, y) & 0x7FFFFFFFu; }
@@ -283,11 +283,26 @@ __global__ __launch_bounds__(LANES <= 64 ? 256 : LANES) void norm_kernel(NormArg
     const float scale = fine ? __builtin_bit_cast(float, m[p]) / 127.0f : __builtin_nanf("");
     const double back = fine && scale > 0 ? 1.0 / (double)scale : 0.0;
     u32x2 c = {0, 0};
+    auto put = [&](int i, int q) { c[i / 4] |= ((uint32_t)min(max(q, kZero - 127), kZero + 127) & 0xFFu) << (8 * (i % 4)); };
+    uint32_t border = ~0u;
     for (int i = 0; i < 8; ++i) {
-      // Nothing not finite gets here: back is 0 then, and its product is taken for 0.  (Scales below the normal numbers
-      // are so much rounded that codes can pass 127, to 190 at most.)
-      const int q = back == 0.0 ? 0 : min(max(whole(y[p][i] * back), -127), 127);
-      c[i / 4] |= ((uint32_t)q & 0xFFu) << (8 * (i % 4));
+      // (scales below the normal numbers are so much rounded that codes can pass 127, to 190 at most)
+      const uint64_t at = __builtin_bit_cast(uint64_t, fma(y[p][i], back, kToCode));
+      put(i, (int)(at >> 32));
+      border = min(border, (uint32_t)at);
+    }
+    if (back == 0.0) c = (u32x2){0, 0};                   // (products that may be not a number)
+    if (border <= kBorder && back != 0.0) {
+      // The products by reciprocals are within 2^-42 of y / scale, so that only here a code may be on the other side of a
+      // half, or on one: the formula's own divisions, of which one value in 2^29 has need.
+      const double root = sqrt(ss / a.cols + (double)a.eps);
+      c = (u32x2){0, 0};
+      for (int i = 0; i < 8; ++i) {
+        float hv = h[p][i], wv = w[p][i];
+        asm("" : "+v"(hv), "+v"(wv));                     // (their 64-bit forms made anew, not kept: registers)
+        put(i, kZero + (int)rint((double)hv / root * (double)wv / (double)scale));
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
     *(u32x2*)(a.codes + row * a.cs + first + col) = c;
     const int g = a.group ? col / a.group : 0;

@@ -1,0 +1,45 @@
+"""GPU checks of moe_rms_norm against the 64-bit oracle where a code is exactly between two whole numbers."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+import torch  # noqa: E402
+
+from attn_fixture import f64  # noqa: E402
+from oracle import step_oracle as S  # noqa: E402
+
+
+@pytest.fixture(scope="module")
+def q():
+    assert torch.cuda.is_available(), "GPU test needs a GPU"
+    from bit_quantized_moe_02_amd import qmoe
+    return qmoe
+
+
+# Whole numbers whose 64-bit reciprocals are rounded, ones whose are not, and one scaled far from 1.
+SCALES = [1, 3, 49, 98, 103, 107, 161, 197, 256, 49 * 2.0 ** -40]
+
+
+@pytest.mark.parametrize("cols", [8, 64, 392, 512, 2056, 7168, 12296])
+@pytest.mark.parametrize("size", [1.0, 49.0, 3 * 2.0 ** -20])
+def test_codes_on_borders(q, cols, size):
+    """Rows of +-size, whose root mean square is size: y is the weight, and the weights are halves of the scale.  The even
+    neighbour is the code."""
+    rng = np.random.default_rng(cols)
+    for scale in SCALES:
+        for group in (0, 128):
+            half = rng.integers(-127, 127, cols) + 0.5
+            half[::group or cols] = 127
+            w = half * scale
+            x = size * rng.choice([-1.0, 1.0], (2, cols))
+            assert np.array_equal(w.astype(np.float32), w) and np.array_equal(x.astype(np.float32), x)
+            xd, wd = torch.from_numpy(x).float().cuda(), torch.from_numpy(w).float().cuda()
+            cd = torch.empty((2, cols), dtype=torch.int8, device="cuda")
+            sc = torch.empty(q.moe_scales_shape(2, cols, group), device="cuda")
+            q.moe_rms_norm(xd, None, wd, 0.0, codes=cd, scales=sc, group=group)
+            codes, scales = S.codes8(S.rms_norm(x, w, 0.0), group)
+            assert (scales == np.float32(scale)).all() and np.array_equal(codes, np.sign(x) * np.rint(half))
+            assert np.array_equal(f64(sc)[:, :2], scales.T), scale
+            got = cd.cpu().numpy()
+            assert np.array_equal(got, codes), (scale, group, np.argwhere(got != codes)[:4].tolist())
