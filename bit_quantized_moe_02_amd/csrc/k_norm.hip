@@ -238,11 +238,16 @@ __global__ __launch_bounds__(LANES <= 64 ? 256 : LANES) void norm_kernel(NormArg
 
   if (a.out) {
     const float f = (float)inv;
+    // A 32-bit root holds its 24 bits, and is finite, for all but values near the largest (of a mean square above 2^252) and,
+    // without epsilon, the smallest numbers: there in 64 bits.
+    const bool holds = f >= 0x1p-126f && f <= 0x1p127f;
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
       if (!in[p]) continue;
       float y[8];
       for (int i = 0; i < 8; ++i) y[i] = h[p][i] * f * w[p][i];
+      if (!holds)
+        for (int i = 0; i < 8; ++i) y[i] = (float)((double)h[p][i] * inv * (double)w[p][i]);
       store8_as(a.ot, a.out, row * a.os + first + (p * LANES + lane) * 8, y);
     }
   }

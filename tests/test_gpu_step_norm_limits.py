@@ -1,4 +1,5 @@
-"""GPU checks of moe_rms_norm against the 64-bit oracle where a code is exactly between two whole numbers."""
+"""GPU checks of moe_rms_norm against the 64-bit oracle where a code is exactly between two whole numbers, and
+where a root is not one of the 32-bit numbers."""
 import numpy as np
 import pytest
 
@@ -8,6 +9,7 @@ import torch  # noqa: E402
 
 from attn_fixture import f64  # noqa: E402
 from oracle import step_oracle as S  # noqa: E402
+from test_gpu_step_norm import run  # noqa: E402
 
 
 @pytest.fixture(scope="module")
@@ -43,3 +45,27 @@ def test_codes_on_borders(q, cols, size):
             assert np.array_equal(f64(sc)[:, :2], scales.T), scale
             got = cd.cpu().numpy()
             assert np.array_equal(got, codes), (scale, group, np.argwhere(got != codes)[:4].tolist())
+
+
+@pytest.mark.parametrize("cols", [8, 64, 264, 2048, 7168, 16384])
+def test_smallest_and_largest_values(q, cols):
+    """Roots below 2^-126 and above 2^127: values below the normal numbers without epsilon, rows of nearly the largest one."""
+    rng = np.random.default_rng(cols)
+    sign = rng.choice([-1.0, 1.0], (10, cols))
+    x = np.ones((10, cols))
+    x[0] = 1e-39
+    x[1] = 2.0 ** -149                                  # the smallest number
+    x[2] = 2.0 ** -133                                  # the smallest bf16
+    x[3] = 1e-40 * np.abs(rng.standard_normal(cols))
+    x[4, :-1], x[4, -1] = 0, 1e-41
+    x[5] = 2.0 ** -127
+    x[6] = 3.3e38
+    x[7] = 2.0 ** 126
+    x[8] = 2.0 ** 127 * (1 - 2.0 ** -8)
+    x[9] = 3.38e38 * rng.random(cols)
+    for group in (None, 0, 128):
+        for ot, wt in (("fp32", "bf16"), ("bf16", None), ("fp16", "fp32")):
+            run(q, rng, 10, 1, cols, "fp32", None, ot, wt, group, x=x * sign, eps=0.0, what=f"fp32 {ot} {wt} {group}")
+            run(q, rng, 10, 1, cols, "bf16", None, ot, wt, group, x=x * sign, eps=0.0, what=f"bf16 {ot} {wt} {group}")
+            run(q, rng, 10, 1, cols, "bf16", "fp32", ot, wt, group, x=np.zeros_like(x), res=x * sign, eps=0.0, what=f"sum {ot} {wt} {group}")
+            run(q, rng, 10, 1, cols, "fp32", None, ot, wt, group, x=x * sign, eps=1e-6, what=f"eps {ot} {wt} {group}")
