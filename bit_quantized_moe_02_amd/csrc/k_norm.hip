@@ -320,14 +320,17 @@ hipError_t launch_types(const NormArgs& a, hipStream_t s) {
   const int64_t n = (int64_t)a.rows * a.heads;
 #define WAVE(L) norm_kernel<XT, RT, L, 1><<<dim3((unsigned)((n + 256 / L - 1) / (256 / L))), dim3(256), 0, s>>>(a)
 #define GROUP(L, P) norm_kernel<XT, RT, L, P><<<dim3((unsigned)n), dim3(L), 0, s>>>(a)
-  if (a.cols <= 64) WAVE(8);
-  else if (a.cols <= 128) WAVE(16);
-  else if (a.cols <= 256) WAVE(32);
-  else if (a.cols <= 512) WAVE(64);
-  else if (a.cols <= 2048) GROUP(256, 1);
-  else if (a.cols <= 4096) GROUP(512, 1);
-  else if (a.cols <= 8192) GROUP(1024, 1);
-  else GROUP(1024, 2);
+  switch (norm_threads(a.cols)) {
+    case 8: WAVE(8); break;
+    case 16: WAVE(16); break;
+    case 32: WAVE(32); break;
+    case 64: WAVE(64); break;
+    case 256: GROUP(256, 1); break;
+    case 512: GROUP(512, 1); break;
+    default:
+      if (a.cols <= 8192) GROUP(1024, 1);
+      else GROUP(1024, 2);
+  }
 #undef WAVE
 #undef GROUP
   return hipGetLastError();

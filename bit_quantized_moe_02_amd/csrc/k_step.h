@@ -20,6 +20,10 @@ struct NormArgs {
   double per_col;                   // 1 / cols
 };
 hipError_t launch_norm(const NormArgs& a, hipStream_t s);
+// Threads that take a vector: lanes of a wave for up to 512 columns, else a workgroup.
+inline int norm_threads(int cols) {
+  return cols <= 64 ? 8 : cols <= 128 ? 16 : cols <= 256 ? 32 : cols <= 512 ? 64 : cols <= 2048 ? 256 : cols <= 4096 ? 512 : 1024;
+}
 
 // moe_linear.
 struct LinearArgs {

@@ -19,7 +19,8 @@ namespace {
 constexpr int64_t kMaxRows = 1 << 24;
 constexpr int64_t kMaxProductRows = 1 << 20;     // (at 64 to a workgroup they fit the grid's second dimension)
 constexpr int64_t kMaxStride = 1 << 24;
-constexpr int64_t kMaxGrid = (1 << 24) - 1;      // workgroups: 32-bit thread numbers with up to 256 threads each
+constexpr int64_t kMaxVectors = (1 << 24) - 1;
+constexpr int64_t kMaxThreads = (1ll << 32) - 1;  // of a launch
 constexpr int kMaxCaches = 256;
 constexpr int kMaxSeqs = 4096;                   // two numbers a row in LDS
 
@@ -69,8 +70,9 @@ extern "C" int moe_rms_norm(const moe_norm* p, void* stream) {
   if (!p) return bad(who, "the description is NULL");
   if (p->rows < 0 || p->rows > kMaxRows) return bad(who, "need 0 <= rows <= 2^24");
   if (p->cols < 8 || p->cols > 16384 || p->cols % 8 != 0) return bad(who, "cols must be a multiple of 8 in [8, 16384]");
-  if (p->heads < 1 || p->heads > 4096 || (int64_t)p->heads * p->rows > kMaxGrid)
-    return bad(who, "need 1 <= heads <= 4096, rows * heads < 2^24");
+  if (p->heads < 1 || p->heads > 4096 || (int64_t)p->heads * p->rows > kMaxVectors ||
+      (int64_t)p->heads * p->rows * norm_threads(p->cols) > kMaxThreads)
+    return bad(who, "need 1 <= heads <= 4096, rows * heads < 2^24 (cols > 2048: 2^23, cols > 4096: 2^22)");
   if (!(p->eps >= 0) || !isfinite(p->eps)) return bad(who, "eps must be finite and not negative");
   if (!float_type(p->x_dtype) || (p->residual && !float_type(p->residual_dtype)) || (p->weight && !float_type(p->weight_dtype)) ||
       (p->out && !float_type(p->out_dtype)))
@@ -91,7 +93,7 @@ extern "C" int moe_rms_norm(const moe_norm* p, void* stream) {
     if (p->group != 0 && p->group != 128) return fail(MOE_ERR_UNSUPPORTED, std::string(who) + ": group must be 128 or 0");
     if (!aligned(p->scales, 16)) return bad(who, "scales must be 16-byte aligned");
     if (p->scale_stride < p->rows || p->scale_stride % 4 != 0 || p->scale_stride < 4 || p->scale_stride > (1 << 28))
-      return bad(who, "scale_stride must be a multiple of 4, at least rows");
+      return bad(who, "scale_stride must be a multiple of 4, at least rows, at most 2^28");
   }
   if (p->out && (p->out == p->sum || (const void*)p->out == (const void*)p->codes)) return bad(who, "outputs must not overlap");
   if (p->codes && (const void*)p->codes == (const void*)p->sum) return bad(who, "outputs must not overlap");
@@ -152,7 +154,7 @@ extern "C" int moe_linear(const moe_linear_weights* w, int32_t rows, int x_dtype
     if (!x_scales || !aligned(x_scales, 16)) return bad(who, "8-bit rows need x_scales, 16-byte aligned");
     if (x_group != 0 && x_group != 128) return fail(MOE_ERR_UNSUPPORTED, std::string(who) + ": x_group must be 128 or 0");
     if (scale_stride < rows || scale_stride % 4 != 0 || scale_stride < 4 || scale_stride > (1 << 28))
-      return bad(who, "scale_stride must be a multiple of 4, at least rows");
+      return bad(who, "scale_stride must be a multiple of 4, at least rows, at most 2^28");
   } else if (x_scales || x_group) {
     return bad(who, "16-bit rows have no scales");
   }

@@ -31,7 +31,9 @@ extern "C" {
  * Rows of `heads` vectors of `cols` values, a row's vectors back to back, rows
  * `stride` elements apart (a multiple of 8, at least heads * cols, at most
  * 2^24).  Every vector is normed by itself (heads = 1: the hidden rows of a
- * layer; more: queries' or keys' heads).  cols is a multiple of 8, 8 to 16384.
+ * layer; more: queries' or keys' heads).  cols is a multiple of 8, 8 to 16384;
+ * heads is 1 to 4096; rows * heads is below 2^24, where cols > 2048 below 2^23,
+ * where cols > 4096 below 2^22.
  * Types: MOE_DT_BF16, MOE_DT_F16, MOE_DT_F32.
  *
  *   h = x + residual, added in 32 bits and rounded to the residual's type
@@ -49,7 +51,7 @@ extern "C" {
  *   a number the scale is not a number and the codes are 0.
  *   codes int8 as the rows of out, codes_stride apart; the scale of row r,
  *   vector v, group g is scales[(v * groups + g) * scale_stride + r], with
- *   scale_stride a multiple of 4, at least rows.
+ *   scale_stride a multiple of 4, at least rows, at most 2^28.
  * Sums of squares are 64-bit (no overflow for any input).
  * At least one of out, codes and sum is wanted; sum needs a residual.  sum may
  * be x or the residual, and out too, where type and stride are the same, so
@@ -137,7 +139,8 @@ typedef struct moe_linear_weights {
  *         scales, value = code * scale.  Rows x_stride elements apart (a
  *         multiple of 8, at least k, at most 2^24).
  *   x_scales  (MOE_DT_I8; NULL otherwise) as moe_rms_norm writes them for one
- *         vector a row: that of row t, group g at x_scales[g * scale_stride + t];
+ *         vector a row: that of row t, group g at x_scales[g * scale_stride + t]
+ *         (scale_stride a multiple of 4, at least rows, at most 2^28);
  *         x_group 128, or 0: one scale a row.  The last group too has scale_stride
  *         of them, read up to the next multiple of 4 rows.
  *   y     y_dtype MOE_DT_BF16, MOE_DT_F16 or MOE_DT_F32, rows y_stride elements apart (at

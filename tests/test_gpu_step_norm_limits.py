@@ -9,7 +9,7 @@ import torch  # noqa: E402
 
 from attn_fixture import f64  # noqa: E402
 from oracle import step_oracle as S  # noqa: E402
-from test_gpu_step_norm import run  # noqa: E402
+from test_gpu_step_norm import check_out, run  # noqa: E402
 
 
 @pytest.fixture(scope="module")
@@ -69,3 +69,20 @@ def test_smallest_and_largest_values(q, cols):
             run(q, rng, 10, 1, cols, "bf16", None, ot, wt, group, x=x * sign, eps=0.0, what=f"bf16 {ot} {wt} {group}")
             run(q, rng, 10, 1, cols, "bf16", "fp32", ot, wt, group, x=np.zeros_like(x), res=x * sign, eps=0.0, what=f"sum {ot} {wt} {group}")
             run(q, rng, 10, 1, cols, "fp32", None, ot, wt, group, x=x * sign, eps=1e-6, what=f"eps {ot} {wt} {group}")
+
+
+@pytest.mark.parametrize("rows,cols", [((1 << 22) - 1, 4104), ((1 << 23) - 1, 2056)])
+def test_most_rows(q, rows, cols):
+    """As many vectors as the call takes, in place; rows at both ends and around 2^32 elements against the oracle."""
+    rng = np.random.default_rng(cols)
+    block = torch.from_numpy(rng.standard_normal((64, cols))).bfloat16().cuda()
+    x = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda")
+    x.fill_(1.0)
+    at = [0, 1, (1 << 32) // cols - 1, (1 << 32) // cols, (1 << 32) // cols + 1, rows - 2, rows - 1]
+    for i, r in enumerate(at):
+        x[r] = block[i]
+    q.moe_rms_norm(x, x, None, 0.0)
+    for i, r in enumerate(at):
+        check_out(x[r], S.rms_norm(f64(block[i]), 1.0, 0.0), torch.bfloat16, f"row {r}")
+    x[at[0]:at[1] + 1], x[at[2]:at[4] + 1], x[at[5]:] = 1.0, 1.0, 1.0
+    assert bool((x == 1.0).all())
