@@ -11,6 +11,7 @@
 #include <vector>
 
 #include "../../include/qmoe_step.h"
+#include "half.h"
 #include "qmoe_internal.h"
 
 using namespace qmoe;

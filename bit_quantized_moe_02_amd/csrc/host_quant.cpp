@@ -19,6 +19,7 @@
 #include <vector>
 
 #include "../../include/qmoe.h"
+#include "half.h"
 #include "qmoe_internal.h"
 
 namespace qmoe {

@@ -21,7 +21,7 @@
 #include <type_traits>
 
 #include "k_step.h"
-#include "launch_util.h"
+#include "lds_limit.h"
 
 namespace qmoe {
 namespace {
@@ -509,7 +509,7 @@ hipError_t launch_resize(const PagesArgs& a, const int32_t* new_lens, int32_t* m
   hipError_t e = hipSuccess;
   by_size(a, [&](auto steps) {
     const auto kernel = resize_kernel<steps.value>;
-    if (rows_lds(a) > 32768) e = ensure_dyn_lds((const void*)kernel, kDeclared);
+    if (rows_lds(a) > 32768) e = raise_dyn_lds((const void*)kernel, kDeclared);
     if (e == hipSuccess) kernel<<<dim3(1), dim3(kThreads), rows_lds(a), s>>>(a, new_lens, missing, many, list_of(a));
   });
   return e == hipSuccess ? hipGetLastError() : e;
@@ -522,7 +522,7 @@ hipError_t launch_fork(const PagesArgs& a, const int32_t* from, int32_t* missing
   hipError_t e = hipSuccess;
   by_size(a, [&](auto steps) {
     const auto kernel = fork_kernel<steps.value>;
-    if (rows_lds(a) > 32768) e = ensure_dyn_lds((const void*)kernel, kDeclared);
+    if (rows_lds(a) > 32768) e = raise_dyn_lds((const void*)kernel, kDeclared);
     if (e == hipSuccess) kernel<<<dim3(1), dim3(kThreads), rows_lds(a), s>>>(a, from, missing, head, jobs, list_of(a));
   });
   if (e == hipSuccess) e = hipGetLastError();

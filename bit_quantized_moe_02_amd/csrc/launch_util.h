@@ -12,10 +12,9 @@
 
 namespace qmoe {
 
-// Raises a kernel's dynamic-LDS limit to the device maximum less what it
-// declares (`declared` bytes at most), once per kernel per process (the
-// attribute is an upper bound, the launch passes the size).
-inline hipError_t ensure_dyn_lds(const void* fn, int declared = 0) {
+// Raises a kernel's dynamic-LDS limit to the device maximum, once per kernel
+// per process (the attribute is an upper bound, the launch passes the size).
+inline hipError_t ensure_dyn_lds(const void* fn) {
   static std::mutex mu;
   static std::set<const void*> done;
   std::lock_guard<std::mutex> lock(mu);
@@ -23,7 +22,7 @@ inline hipError_t ensure_dyn_lds(const void* fn, int declared = 0) {
   int dev = 0, max_lds = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e == hipSuccess) e = hipDeviceGetAttribute(&max_lds, hipDeviceAttributeMaxSharedMemoryPerBlock, dev);
-  if (e == hipSuccess) e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, max_lds - declared);
+  if (e == hipSuccess) e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, max_lds);
   if (e == hipSuccess) done.insert(fn);
   return e;
 }

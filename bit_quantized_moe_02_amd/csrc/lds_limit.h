@@ -1,0 +1,27 @@
+// A kernel's limit of dynamic LDS, for the step kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <mutex>
+#include <set>
+
+namespace qmoe {
+
+// Raises a kernel's dynamic-LDS limit to the device maximum less what it
+// declares (`declared` bytes at most), once per kernel per process (the
+// attribute is an upper bound, the launch passes the size).
+inline hipError_t raise_dyn_lds(const void* fn, int declared) {
+  static std::mutex mu;
+  static std::set<const void*> done;
+  std::lock_guard<std::mutex> lock(mu);
+  if (done.count(fn)) return hipSuccess;
+  int dev = 0, max_lds = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e == hipSuccess) e = hipDeviceGetAttribute(&max_lds, hipDeviceAttributeMaxSharedMemoryPerBlock, dev);
+  if (e == hipSuccess) e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, max_lds - declared);
+  if (e == hipSuccess) done.insert(fn);
+  return e;
+}
+
+}  // namespace qmoe

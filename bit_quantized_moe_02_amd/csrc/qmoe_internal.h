@@ -19,10 +19,6 @@ constexpr int kTileCols = 256;
 
 inline int64_t pad256(int64_t k) { return (k + 255) / 256 * 256; }
 
-// Nearest fp16 to a double (one rounding, ties to even; infinity beyond its range), and an fp16's value.
-uint16_t f64_to_f16_rne(double x);
-double f16_value(uint16_t h);
-
 // Bytes of one tile of each format; 0 for an unknown format.
 int tile_bytes(int fmt);
 
