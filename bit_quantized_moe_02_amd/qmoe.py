@@ -824,16 +824,25 @@ def moe_linear_quantize(w: np.ndarray, group: int = 128, with_zeros: bool = Fals
     return codes, scales, zeros
 
 
+def _small(a, name):
+    """a as contiguous uint8; raises for values that these do not hold (the library refuses the rest of what it must)."""
+    a = np.asarray(a)
+    b = a if a.dtype == np.uint8 else np.clip(a, 0, 255).astype(np.uint8) if a.dtype.kind in "iuf" and not np.isnan(a).any() else None
+    if b is None or (b is not a and not np.array_equal(a, b)):
+        raise ValueError(f"{name} must be whole numbers of 0 to 15")
+    return np.ascontiguousarray(b)
+
+
 def moe_linear_pack(codes: np.ndarray, scales: np.ndarray, zeros: np.ndarray | None = None, group: int = 128,
                     n_threads: int = 0) -> np.ndarray:
-    """Codes, scales and zero points (host) -> packed uint8 bytes (host)."""
-    codes = np.ascontiguousarray(codes, dtype=np.uint8)
+    """Codes, scales (rounded to fp16) and zero points (host) -> packed uint8 bytes (host)."""
+    codes = _small(codes, "codes")
     if codes.ndim != 2:
         raise ValueError("codes must be [n, k]")
     n, k = codes.shape
     groups = (n, -(-k // group) if group > 0 else 1)
     scales = np.ascontiguousarray(scales, dtype=np.float16)
-    zeros = None if zeros is None else np.ascontiguousarray(zeros, dtype=np.uint8)
+    zeros = None if zeros is None else _small(zeros, "zeros")
     if scales.shape != groups or (zeros is not None and zeros.shape != groups):
         raise ValueError(f"scales and zeros must be {list(groups)}")
     out = np.empty(max(moe_linear_packed_bytes(n, k, group, zeros is not None), 1), np.uint8)

@@ -1,5 +1,6 @@
 """CPU checks of the step calls' limits on sizes, each one past the limit with all else in order, and each at the limit with
-another fault that is looked at later."""
+another fault that is looked at later; and of values that a cast would change."""
+import numpy as np
 import pytest
 
 from test_step_host import P, _norm, q  # noqa: F401
@@ -16,3 +17,17 @@ def test_norm_rows(q, cols, heads, most):  # noqa: F811
         kw[name] = cols * heads
     assert _norm(q, rows=most + 1, **kw) == q.MOE_ERR_INVALID_ARG and "rows" in q.moe_last_error()
     assert _norm(q, rows=most, **dict(kw, x=None)) == q.MOE_ERR_INVALID_ARG and "x is NULL" in q.moe_last_error()
+
+
+@pytest.mark.parametrize("bad", [np.int64(256), np.int32(-256), np.uint16(512 + 7), np.int64(16), np.int8(-1), np.float32(7.5), np.float64("nan"),
+                                 np.float32("inf"), np.float64(-0.25)])
+def test_pack_refuses_what_bytes_do_not_hold(q, bad):  # noqa: F811
+    """Codes and zero points of other types come as they are or not at all."""
+    scales = np.ones((4, 2), np.float16)
+    for name in ("codes", "zeros"):
+        a = dict(codes=np.full((4, 64), 3, bad.dtype), zeros=np.full((4, 2), 5, bad.dtype))
+        fine = q.moe_linear_pack(a["codes"], scales, a["zeros"], 32)
+        assert np.array_equal(fine, q.moe_linear_pack(a["codes"].astype(np.uint8), scales, a["zeros"].astype(np.uint8), 32))
+        a[name][2, 1] = bad
+        with pytest.raises((ValueError, q.QmoeError)):
+            q.moe_linear_pack(a["codes"], scales, a["zeros"], 32)
