@@ -29,7 +29,7 @@
 
 #include "../../include/qmoe_step.h"
 #include "k_step.h"
-#include "launch_util.h"
+#include "lds_limit.h"
 
 namespace qmoe {
 namespace {
@@ -396,7 +396,7 @@ hipError_t launch_one(const LinearArgs& a, hipStream_t s) {
   typedef Shape<XT, R, NT> S;
   const auto kernel = linear_kernel<XT, G, R, NT, Z, XG>;
   if (S::kLdsAll > 65536) {
-    const hipError_t e = ensure_dyn_lds((const void*)kernel);
+    const hipError_t e = raise_dyn_lds((const void*)kernel, 0);
     if (e != hipSuccess) return e;
   }
   const dim3 grid((unsigned)(((a.n + 15) / 16 + NT - 1) / NT), (unsigned)((a.rows + R - 1) / R));
