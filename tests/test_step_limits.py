@@ -1,9 +1,11 @@
 """CPU checks of the step calls' limits on sizes, each one past the limit with all else in order, and each at the limit with
 another fault that is looked at later; and of values that a cast would change."""
+import ctypes
+
 import numpy as np
 import pytest
 
-from test_step_host import P, _norm, q  # noqa: F401
+from test_step_host import _norm, _page_calls, q  # noqa: F401
 
 MANY = dict(codes=None, scales=None, heads=1, x_stride=16384, residual_stride=16384, sum_stride=16384, out_stride=16384)
 
@@ -31,3 +33,15 @@ def test_pack_refuses_what_bytes_do_not_hold(q, bad):  # noqa: F811
         a[name][2, 1] = bad
         with pytest.raises((ValueError, q.QmoeError)):
             q.moe_linear_pack(a["codes"], scales, a["zeros"], 32)
+
+
+def test_most_pages(q):  # noqa: F811
+    """2^29 pages are a pool, one more is none, with nothing else that could be wrong."""
+    for f in (q.lib.moe_kv_fork_workspace_bytes, q.lib.moe_kv_compact_workspace_bytes):
+        for n, fine in (((1 << 29), True), ((1 << 29) + 1, False), (1, True), (0, False)):
+            (pool, tables), calls = _page_calls(q, pool=dict(n_pages=n, caches=None), n_caches=0)
+            pool.n_caches = 0
+            assert (f(ctypes.byref(pool), ctypes.byref(tables)) > 0) == fine, n
+            if not fine:
+                for call in calls:
+                    assert call() == q.MOE_ERR_INVALID_ARG and "n_pages" in q.moe_last_error()
