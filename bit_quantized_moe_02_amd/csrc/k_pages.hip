@@ -163,7 +163,9 @@ __device__ __forceinline__ int grant(const PagesArgs& a, Scratch& s, int& which,
     granted = fits;
   }
   int passed = 0;                                             // free pages of the windows before
-  for (int base = 0; passed < granted; base += kWindow) {
+  // (The windows are looked through once more: should another call on the pool have taken pages in between, there are fewer
+  // than were counted, and the pool's end ends it.)
+  for (int base = 0; passed < granted && base < a.n_pages; base += kWindow) {
     int all = free_pages;
     if (a.n_pages > kWindow) {
       __syncthreads();
@@ -181,7 +183,7 @@ __device__ __forceinline__ int grant(const PagesArgs& a, Scratch& s, int& which,
     }
     passed += all;
   }
-  return granted;
+  return min(granted, passed);
 }
 
 __device__ __forceinline__ int length(const PagesArgs& a, int v) { return min(max(v, 0), a.per_seq << a.shift); }
@@ -450,7 +452,7 @@ __global__ __launch_bounds__(kThreads) void compact_kernel(PagesArgs a, int32_t*
     __syncthreads();
   }
   if (t == 0) {
-    ws[0] = moves;
+    ws[0] = min(moves, holes);                                 // (the same, unless another call changed the pool meanwhile)
     ws[1] = n;
     if (held) *held = n;
   }
@@ -459,8 +461,8 @@ __global__ __launch_bounds__(kThreads) void compact_kernel(PagesArgs a, int32_t*
 __global__ __launch_bounds__(kCopyThreads) void compact_copy_kernel(PagesArgs a, const int32_t* ws, PageCopy c, int n_caches,
                                                                     bool first) {
   const int32_t *rank = ws + 4, *dst = rank + a.n_pages, *src = dst + a.n_pages;
-  const int n = ws[1];
-  const int64_t units = (int64_t)ws[0] * n_caches;
+  const int n = ws[1], moves = ws[0];
+  const int64_t units = (int64_t)moves * n_caches;
   const int parts = parts_of((int)min(units, (int64_t)gridDim.x));
   for (int64_t w = blockIdx.x; w < units * parts; w += gridDim.x) {
     const int64_t unit = w / parts;
@@ -480,7 +482,7 @@ __global__ __launch_bounds__(kCopyThreads) void compact_copy_kernel(PagesArgs a,
       const int p = row[j];
       if (p < n || p >= a.n_pages) continue;
       const int k = rank[p];
-      if (k >= 0) row[j] = dst[k];
+      if (k >= 0 && k < moves) row[j] = dst[k];
     }
   }
 }
