@@ -5,7 +5,7 @@
 // Bytes bound it: each value is read and written once, a vector staying in
 // registers, 8 columns a thread and pass, between the sum of its squares and the
 // outputs.  The sum of squares is held in 64 bits, and where y becomes 8-bit codes so is y:
-// a code next to the border of two is then the one of the formula.  In 64 bits that is some 10 operations a
+// a code next to the border of two, or on it, is then the one of the formula.  In 64 bits that is some 10 operations a
 // value, 2 to 5 % of the time of many vectors and 0.5 us of a few long ones'.
 //
 // Vectors of up to 512 columns take the least power of two of lanes that holds
@@ -15,9 +15,10 @@
 // for 227) and no faster for 7168.  Lanes add up by moves between registers; through LDS'
 // exchange the same sums cost 0.2 to 0.5 us a call.
 //
-// bf16, sum and outputs: 4096 rows of 7168 columns to bf16 46 us (5.2 TB/s), to codes
-// 48, to both 54; 8192 of 16384 to codes 211 (4.5).  One row of 512 2.1 us (an empty kernel
-// 2.0), of 7168 3.0, as codes 3.9; 64 rows of 7168 as codes 4.3.
+// bf16, sum and outputs: 4096 rows of 7168 columns to bf16 45 us (5.2 TB/s), to codes
+// 43 (4.8), to both 52; 8192 of 16384 to codes 214 (4.4).  One row of 512 2.1 us (an empty kernel
+// 2.0), of 7168 3.0, as codes 3.8; 64 rows of 7168 as codes 4.3.  Heads of 128 without a sum: 48 of
+// one token 2.5 us, of 64 2.7, of 8192 40 (5.1 TB/s).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -280,38 +281,51 @@ __global__ __launch_bounds__(LANES <= 64 ? 256 : LANES) void norm_kernel(NormArg
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) m[p] = all;
   }
+  u32x2 c[PASSES];
+  float scale[PASSES];
+  uint32_t border = ~0u;
+  auto put = [&](u32x2& c, int i, int q) {
+    c[i / 4] |= ((uint32_t)min(max(q, kZero - 127), kZero + 127) & 0xFFu) << (8 * (i % 4));
+  };
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    const bool fine = m[p] < 0x7F800000u;
+    scale[p] = fine ? __builtin_bit_cast(float, m[p]) / 127.0f : __builtin_nanf("");
+    const double back = fine && scale[p] > 0 ? 1.0 / (double)scale[p] : 0.0;
+    c[p] = (u32x2){0, 0};
+    uint32_t next = ~0u;
+    for (int i = 0; i < 8; ++i) {
+      // (scales below the normal numbers are so much rounded that codes can pass 127, to 190 at most)
+      const uint64_t at = __builtin_bit_cast(uint64_t, fma(y[p][i], back, kToCode));
+      put(c[p], i, (int)(at >> 32));
+      next = min(next, (uint32_t)at);
+    }
+    if (back == 0.0) c[p] = (u32x2){0, 0};                // (products that may be not a number)
+    else border = min(border, next);
+  }
+  if (border <= kBorder) {
+    // The products by reciprocals are within 2^-42 of y / scale, so that only here a code may be on the other side of a
+    // half, or on one: the formula's own divisions, of which one value in 2^29 has need.
+    const double root = sqrt(ss / a.cols + (double)a.eps);
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+      if (!(scale[p] > 0)) continue;
+      c[p] = (u32x2){0, 0};
+      for (int i = 0; i < 8; ++i) {
+        float hv = h[p][i], wv = w[p][i];
+        asm("" : "+v"(hv), "+v"(wv));                     // (their 64-bit forms made anew, not kept: registers)
+        put(c[p], i, kZero + (int)rint((double)hv / root * (double)wv / (double)scale[p]));
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
     if (!in[p]) continue;
     const int col = (p * LANES + lane) * 8;
-    const bool fine = m[p] < 0x7F800000u;
-    const float scale = fine ? __builtin_bit_cast(float, m[p]) / 127.0f : __builtin_nanf("");
-    const double back = fine && scale > 0 ? 1.0 / (double)scale : 0.0;
-    u32x2 c = {0, 0};
-    auto put = [&](int i, int q) { c[i / 4] |= ((uint32_t)min(max(q, kZero - 127), kZero + 127) & 0xFFu) << (8 * (i % 4)); };
-    uint32_t border = ~0u;
-    for (int i = 0; i < 8; ++i) {
-      // (scales below the normal numbers are so much rounded that codes can pass 127, to 190 at most)
-      const uint64_t at = __builtin_bit_cast(uint64_t, fma(y[p][i], back, kToCode));
-      put(i, (int)(at >> 32));
-      border = min(border, (uint32_t)at);
-    }
-    if (back == 0.0) c = (u32x2){0, 0};                   // (products that may be not a number)
-    if (border <= kBorder && back != 0.0) {
-      // The products by reciprocals are within 2^-42 of y / scale, so that only here a code may be on the other side of a
-      // half, or on one: the formula's own divisions, of which one value in 2^29 has need.
-      const double root = sqrt(ss / a.cols + (double)a.eps);
-      c = (u32x2){0, 0};
-      for (int i = 0; i < 8; ++i) {
-        float hv = h[p][i], wv = w[p][i];
-        asm("" : "+v"(hv), "+v"(wv));                     // (their 64-bit forms made anew, not kept: registers)
-        put(i, kZero + (int)rint((double)hv / root * (double)wv / (double)scale));
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    }
-    *(u32x2*)(a.codes + row * a.cs + first + col) = c;
+    *(u32x2*)(a.codes + row * a.cs + first + col) = c[p];
     const int g = a.group ? col / a.group : 0;
-    if (col == g * (a.group ? a.group : 1)) a.scales[((int64_t)head * groups + g) * a.scs + row] = scale;
+    if (col == g * (a.group ? a.group : 1)) a.scales[((int64_t)head * groups + g) * a.scs + row] = scale[p];
   }
 }
 
