@@ -11,10 +11,10 @@
 //
 // Few rows are bound by the weights' bytes, many by what a compute unit has to do for them, of which none alone is near its
 // peak: of 64 rows of bf16 times 7168 x 7168, 16.5 us, by count matrix instructions are 4 us, vector instructions that make operands
-// of codes 5, x from the second-level cache 4 and through LDS 4.
-// 1 row times 32771 x 7168 24.3 us in bf16 (scales of 128, 5.0 TB/s), 25.7 as codes with scales of 32 (5.1); 16 rows of bf16
-// times 7168 x 7168 8.4 us; 64 rows times 7168 x 7168 16.7 us in bf16, 11.3 as codes (582 TFLOP/s); times 28672 x 7168 57
-// and 43.
+// of codes 5 (half of it twice: a wave's operands serve 32 rows), x from the second-level cache 4 and through LDS 4.
+// 1 row times 32771 x 7168 25 to 27 us in bf16 (scales of 128, 4.5 to 4.8 TB/s), 26.8 as codes with scales of 32 (4.9), 22.8 with
+// scales of 128 (5.3); 16 rows of bf16 times 7168 x 7168 8.0 us; 64 rows times 7168 x 7168 16.5 us in bf16, 11.3 as codes
+// (584 TFLOP/s); times 28672 x 7168 59 and 43.
 //
 // Codes enter the products exactly.  16-bit rows: q goes into the upper
 // mantissa bits of 1.0, u = 1 + q/16 (shift, mask, exclusive or: the codes are stored as q ^ 8),
@@ -125,7 +125,7 @@ __device__ __forceinline__ int zero_of(const Weights<G, Z>& w, int i, uint32_t l
 }
 
 // How a workgroup is made for up to R rows of x and NT tiles of 16 weight rows.  (12 or 16 waves were not faster for any
-// R and NT: they have no registers for what 8 have in flight.)
+// R and NT.)
 constexpr int kWaves = 8;
 template <int XT, int R, int NT>
 struct Shape {
@@ -421,7 +421,8 @@ constexpr Choice kChoices16[] = {{4, 1, 28, 25},   {4, 2, 40, 49},   {4, 4, 83, 
 constexpr Choice kChoices8[] = {{8, 1, 24, 24},  {8, 2, 32, 44},  {8, 4, 70, 83},   {16, 1, 26, 26}, {16, 2, 38, 44},
                                 {16, 4, 63, 86}, {32, 2, 55, 53}, {32, 4, 93, 100}, {64, 4, 164, 175}};
 
-// The choice whose workgroups, a compute unit at a time, take the least time.  Of k = 7168, 64 rows of bf16 times 256
+// The choice whose workgroups, a compute unit at a time, take the least time, as it was measured for k = 7168 without zero
+// points or scales of groups of x (other k were not).  Of k = 7168, in one sweep, 64 rows of bf16 times 256
 // weight rows: 4.6 us with 4 rows and a tile a workgroup, 12 with 64 and one; times 4096: 10.8 with 16 and 4, 11.5 with 32 and
 // 2, 14.9 with 64 and one; times 7168: 16.1 with 32 and 4, 18.6 with 32 and 2, 24.3 with 64 and 4; times 28672: 67.7, 76 (64 and
 // 2) and 55.  As codes times 4096: 8.3, 7.7 and 10.0.  One row times 7168: 6.7 with 2 tiles, 6.9 with one, 8.7 with 4.
